@@ -15,6 +15,9 @@ Functions keep the C names:
     q4nx_repack_q4k(chunks, rows, cols, out=None)-> uint8 q4_1 chunks
     q4nx_argmax(logits, out=None)                -> int32 [M]
 
+and, from ``serving.py``, the operators around the products in a decode step
+(q4nx_kv_append, q4nx_kv_read, q4nx_kv_attention, q4nx_gemm_lora, q4nx_logprobs).
+
 ``w`` is a :class:`Weight`: a uint8 CUDA tensor of chunk bytes plus kind, rows
 and cols (the tile grid of the "Q4NX chunks" section of the 1bit engine
 "NPU engine" page).
@@ -32,7 +35,7 @@ Q4NX_Q4_1, Q4NX_Q4_K, Q4NX_Q8_KR, Q4NX_Q8_BLK = 1, 2, 3, 4
 Q4NX_OUT_BF16, Q4NX_OUT_F32 = 0, 1
 # statuses of include/q4nx.h
 (Q4NX_OK, Q4NX_E_NULL, Q4NX_E_KIND, Q4NX_E_SHAPE, Q4NX_E_SHORT, Q4NX_E_ALIGN, Q4NX_E_M, Q4NX_E_WORKSPACE,
- Q4NX_E_UNSUPPORTED, Q4NX_E_CUDA, Q4NX_E_DEVICE_TIMEOUT, Q4NX_E_DTYPE) = range(12)
+ Q4NX_E_UNSUPPORTED, Q4NX_E_CUDA, Q4NX_E_DEVICE_TIMEOUT, Q4NX_E_DTYPE, Q4NX_E_INDEX) = range(13)
 KINDS = {"q4_1": Q4NX_Q4_1, "q4_k": Q4NX_Q4_K, "q8_kr": Q4NX_Q8_KR, "q8_blk": Q4NX_Q8_BLK}
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -155,12 +158,12 @@ def _cuda(t: torch.Tensor, name: str):
 
 # Workspaces: zero-filled once.  The GEMV family (q4nx_gemv, _gemv_top1,
 # _gemv_batch) leaves its workspace zero-filled after every call and relies on
-# that; the GEMM leaves partial tiles behind, so the two families never share
-# one.  One per (family, device, stream); calls on one stream are ordered, so
+# that; the GEMM leaves partial tiles behind, and so does the attention over
+# the 4-bit cache, so the families never share one.  One per (family, device, stream); calls on one stream are ordered, so
 # they never overlap.
 _ws_lock = threading.Lock()
 _ws: dict[tuple[str, int, int], torch.Tensor] = {}
-WS_FAMILIES = ("gemv", "gemm")
+WS_FAMILIES = ("gemv", "gemm", "kv")
 
 
 def workspace(device: torch.device, nbytes: int, family: str = "gemv") -> torch.Tensor:
@@ -414,8 +417,9 @@ def q4nx_argmax(logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.
 
 def q4nx_check(ws: torch.Tensor | None = None, device=None) -> None:
     """Raise if a bounded in-kernel wait of an earlier call on this workspace (default:
-    this stream's GEMV and GEMM workspaces) gave up.  A workspace that reports
-    such an error must be zero-filled before its next use: the default ones
+    this stream's GEMV, GEMM and cache workspaces) gave up, or if such a call
+    met an index out of range in device memory.  A workspace that reports
+    a wait that gave up must be zero-filled before its next use: the default ones
     are zero-filled here before raising; a caller's own `ws` is left to the
     caller."""
     if ws is not None:
@@ -429,3 +433,11 @@ def q4nx_check(ws: torch.Tensor | None = None, device=None) -> None:
             with torch.cuda.device(w.device):
                 w.zero_()
         _check(st, "q4nx_check")
+
+
+from . import serving as _serving  # noqa: E402  (needs the names above)
+from .serving import (Adapters, KVCache, Logprobs, Q4NX_MAX_TOP, q4nx_adapters, q4nx_gemm_lora,  # noqa: E402,F401
+                      q4nx_kv_append, q4nx_kv_attention, q4nx_kv_batch, q4nx_kv_cache, q4nx_kv_page_bytes, q4nx_kv_read,
+                      q4nx_logprobs)
+
+EXPORTS += _serving.EXPORTS

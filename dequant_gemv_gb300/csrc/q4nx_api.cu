@@ -15,6 +15,7 @@
 #include "q4nx_checks.h"
 #include "q4nx_device.cuh"
 #include "q4nx_kernels.h"
+#include "q4nx_kv.cuh"
 
 namespace q4nx {
 
@@ -129,7 +130,7 @@ const char* q4nx_status_str(int status) {
     case Q4NX_OK: return "ok";
     case Q4NX_E_NULL: return "a required pointer is NULL";
     case Q4NX_E_KIND: return "unknown chunk kind";
-    case Q4NX_E_SHAPE: return "rows must be a positive multiple of 32 and cols of 256";
+    case Q4NX_E_SHAPE: return "a size, count or stride is out of range (a weight's rows: a positive multiple of 32, cols of 256)";
     case Q4NX_E_SHORT: return "buffer shorter than its layout needs";
     case Q4NX_E_ALIGN: return "device buffer not 16-byte aligned";
     case Q4NX_E_M: return "M must be in 1..64";
@@ -138,6 +139,7 @@ const char* q4nx_status_str(int status) {
     case Q4NX_E_CUDA: return "CUDA launch failed";
     case Q4NX_E_DEVICE_TIMEOUT: return "a bounded in-kernel wait gave up";
     case Q4NX_E_DTYPE: return "unknown output dtype";
+    case Q4NX_E_INDEX: return "an index in device memory was out of range";
     default: return "unknown status";
   }
 }
@@ -343,7 +345,7 @@ int q4nx_check(void* workspace_dev, void* stream) {
   const uint32_t zero = 0;
   if (cudaMemcpyAsync(workspace_dev, &zero, sizeof zero, cudaMemcpyHostToDevice, s) != cudaSuccess) return Q4NX_E_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return Q4NX_E_CUDA;
-  return Q4NX_E_DEVICE_TIMEOUT;
+  return err == kErrIndex ? Q4NX_E_INDEX : Q4NX_E_DEVICE_TIMEOUT;
 }
 
 }  // extern "C"

@@ -81,6 +81,48 @@ uint64_t gemm_workspace_bytes(int64_t TR, int64_t TC, int M);
 cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, const void* X, int M, void* Y,
                         int out_f32, void* workspace, cudaStream_t s);
 
+// ---- 4-bit key/value cache and the attention that reads it (q4nx_kv.cuh) ----
+struct KvPool;
+struct KvBatch;
+constexpr int kKvMaxBatch = 1024;                 // requests per call
+constexpr int kKvMaxCtas = 304;                   // CTAs of an attention launch, at most
+cudaError_t launch_kv_append(int D, const KvPool& p, const KvBatch& kb, const void* k, const void* v, int64_t stride,
+                             uint32_t* err, cudaStream_t s);
+cudaError_t launch_kv_read(int D, const KvPool& p, const KvBatch& kb, void* k, void* v, int out_f32, uint32_t* err,
+                           cudaStream_t s);
+uint64_t attention_workspace_bytes(int D);
+cudaError_t launch_attention(int D, const KvPool& pool, const KvBatch& kb, const void* q, int64_t q_stride, int heads,
+                             float scale, int64_t window, void* out, int out_f32, float* lse, void* workspace,
+                             const DeviceInfo& info, cudaStream_t s);
+
+// ---- low-rank adapters beside a projection ----
+struct LoraCall {
+  const void *x, *a, *b;       // bf16 [M][K], [count][R][K], [count][N][R]
+  const float* scale;          // [count]
+  const int32_t* ids;          // [M]
+  float* t;                    // scratch [64][R]
+  const float* base;           // the product with W, binary32 [M][N] (may be y)
+  void* y;                     // [M][N]
+  uint32_t* err;
+  int64_t K, N;
+  int M, R, count;
+};
+cudaError_t launch_lora_shrink(const LoraCall& c, cudaStream_t s);
+cudaError_t launch_lora_expand(const LoraCall& c, int out_f32, cudaStream_t s);
+
+// ---- log-probabilities ----
+constexpr int kMaxTopLogprobs = 32;
+struct LogprobsCall {
+  const void* logits;
+  int f32, M, top;
+  int64_t V, stride;           // columns, elements between rows
+  const int32_t* tokens;
+  float *logprob, *entropy, *lse;   // NULL: not wanted
+  int32_t* top_idx;
+  float* top_lp;
+};
+cudaError_t launch_logprobs(const LogprobsCall& c, const DeviceInfo& info, cudaStream_t s);
+
 // Workspace layout shared by the GEMV launcher and kernel.
 constexpr uint64_t kWsErrBytes = 16;              // error word (+ padding)
 constexpr int kMaxCtas = 1024;                    // upper bound of CTAs per GEMV launch

@@ -1,0 +1,332 @@
+// q4nx_logprobs.cu -- log-probabilities of rows of logits in one pass:
+//   lse = log sum exp x,  lp(token) = x[token] - lse,  H = lse - sum p x,
+// and the `top` largest with their indexes (ties: lowest index).
+//
+// Bound: the logits' bytes, once; at one row, latency.  A cluster of C CTAs
+// takes a row; each thread keeps the running maximum m, z = sum exp(x - m) and
+// w = sum exp(x - m) (x - m) of its elements, moved to a new maximum once per
+// batch of loads (exp of 0 at the maximum, never an overflow; a centred w
+// keeps the entropy free of cancellation).
+//
+// Top alternatives without a second pass over memory: the j-th largest of a
+// warp's 32 thread maxima, j = ceil(top / warps), is reached by at least j
+// elements of that warp, so the smallest such value over the warps is a floor
+// for the CTA's top elements.  Only threads whose own maximum reaches the
+// floor read their elements again (from L2; a few per cent of them), and the
+// elements at or above it, about a hundred, get their ranks by counting.  Rows with
+// more than kCand such elements (many equal ones) take `top` rounds of
+// "largest below the previous" instead.
+#include <cooperative_groups.h>
+
+#include "q4nx_kernels.h"
+#include "q4nx_kv.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace q4nx {
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCand = 1024;          // candidates of a CTA
+constexpr int kBatch = 8;            // 16-byte loads a thread has in flight
+constexpr int kMaxTop = 32, kMaxCluster = 8;
+constexpr float kLog2e = 1.44269504088896f;
+
+struct Args {
+  const uint8_t* logits;
+  int64_t V, pitch;                  // columns, bytes between rows
+  const int32_t* tokens;
+  float *logprob, *entropy, *lse;
+  int32_t* top_idx;
+  float* top_lp;
+  int top;
+};
+
+struct Stat {
+  float m, z, w;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
+// what is subtracted from x for a running maximum m: a row of -inf alone stays all zeros
+__device__ __forceinline__ float shift_of(float m) { return m == neg_inf() ? 0.f : m; }
+
+__device__ __forceinline__ void move_to(Stat& s, float m) {
+  const float d = shift_of(s.m) - shift_of(m);         // <= 0 once s holds anything
+  const float f = s.z == 0.f ? 0.f : ex2(d * kLog2e);
+  s.w = f == 0.f ? 0.f : f * fmaf(s.z, d, s.w);
+  s.z *= f;
+  s.m = m;
+}
+__device__ __forceinline__ Stat join(Stat a, Stat b) {
+  const float m = fmaxf(a.m, b.m);
+  move_to(a, m);
+  move_to(b, m);
+  return {m, a.z + b.z, a.w + b.w};
+}
+__device__ __forceinline__ void add(Stat& s, float x, float shift) {
+  const float d = x - shift;
+  const float e = ex2(d * kLog2e);
+  s.z += e;
+  s.w = fmaf(e, fmaxf(d, -300.f), s.w);                // e is 0 there, and 0 * -inf is not
+}
+__device__ __forceinline__ uint32_t ord_of(float v) { return static_cast<uint32_t>(argmax_key(v, 0) >> 32); }
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  if (o == 0xFFFFFFFFu) return __int_as_float(0x7fc00000);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+
+template <bool BF16>
+struct Row {
+  static constexpr int VE = BF16 ? 8 : 4;              // elements per 16-byte load
+  const uint8_t* p;
+  int64_t V;
+  int64_t head;                                        // elements before the first 16-byte boundary
+  int64_t vecs;                                        // whole 16-byte loads
+  int64_t tail;                                        // elements after them
+  __device__ Row(const uint8_t* row, int64_t v) : p(row), V(v) {
+    const int es = BF16 ? 2 : 4;
+    head = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / es;
+    if (head > V) head = V;
+    vecs = (V - head) / VE;
+    tail = V - head - vecs * VE;
+  }
+  __device__ float at(int64_t i) const {
+    if constexpr (BF16) return bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(p) + i));
+    else return __ldg(reinterpret_cast<const float*>(p) + i);
+  }
+  __device__ uint4 load(int64_t v) const { return __ldg(reinterpret_cast<const uint4*>(p + head * (BF16 ? 2 : 4)) + v); }
+  __device__ static float pick(const uint4& u, int e) {
+    const uint32_t w = (e / (VE / 4)) == 0 ? u.x : (e / (VE / 4)) == 1 ? u.y : (e / (VE / 4)) == 2 ? u.z : u.w;
+    if constexpr (BF16) return (e & 1) ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
+    else return __uint_as_float(w);
+  }
+};
+
+// The elements of one thread: every kThreads-th load of the CTA's share, and
+// (first CTA) one of the row's unaligned ends.
+template <bool BF16, typename F>
+__device__ __forceinline__ void for_elements(const Row<BF16>& row, int64_t v0, int64_t v1, int64_t end_elem, F f) {
+  constexpr int VE = Row<BF16>::VE;
+  for (int64_t v = v0 + threadIdx.x; v < v1; v += kThreads) {
+    const uint4 u = row.load(v);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) f(Row<BF16>::pick(u, e), row.head + v * VE + e);
+  }
+  if (end_elem >= 0) f(row.at(end_elem), end_elem);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
+  constexpr int VE = Row<BF16>::VE;
+  __shared__ Stat stats[kWarps];
+  __shared__ uint32_t floor_of[kWarps];
+  __shared__ uint64_t cand[kCand];
+  __shared__ uint64_t best[kMaxTop];                   // this CTA's, largest first
+  __shared__ uint64_t all[kMaxTop * kMaxCluster];
+  __shared__ uint64_t reduce[kWarps];
+  __shared__ Stat cta;
+  __shared__ int found;
+  __shared__ float final_lse;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t m = blockIdx.y;
+  const Row<BF16> row(a.logits + m * a.pitch, a.V);
+  const int64_t v0 = row.vecs * rank / C, v1 = row.vecs * (rank + 1) / C;
+  int64_t end_elem = -1;
+  if (rank == 0) {
+    if (tid < row.head) end_elem = tid;
+    else if (tid - row.head < row.tail) end_elem = row.V - row.tail + (tid - row.head);
+  }
+  Stat s = {neg_inf(), 0.f, 0.f};
+  float big = neg_inf();
+  bool any = end_elem >= 0;
+  if (any) {
+    const float x = row.at(end_elem);
+    s.m = big = fmaxf(x, neg_inf());
+    add(s, x, shift_of(s.m));
+  }
+  for (int64_t v = v0 + tid; v < v1; v += kBatch * kThreads) {
+    uint4 u[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (v + k * kThreads < v1) u[k] = row.load(v + k * kThreads);
+    float mx = s.m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (v + k * kThreads < v1) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) mx = fmaxf(mx, Row<BF16>::pick(u[k], e));
+      }
+    move_to(s, mx);
+    const float shift = shift_of(mx);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (v + k * kThreads < v1) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) add(s, Row<BF16>::pick(u[k], e), shift);
+      }
+    big = mx;
+    any = true;
+  }
+  // the largest value of this thread in the order of the top list (NaN above
+  // all); a NaN total means a NaN or +inf among them: look again at which
+  uint32_t mine = any ? ord_of(big) : 0u;
+  if (a.top > 0 && s.z != s.z) for_elements<BF16>(row, v0, v1, end_elem, [&](float x, int64_t) { mine = max(mine, ord_of(x)); });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Stat t;
+    t.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+    t.z = __shfl_xor_sync(0xffffffffu, s.z, o);
+    t.w = __shfl_xor_sync(0xffffffffu, s.w, o);
+    s = lane & o ? join(t, s) : join(s, t);            // the same order on both sides
+  }
+  if (lane == 0) stats[warp] = s;
+  if (a.top > 0) {
+    uint32_t left = mine, kth = 0;
+    for (int j = 0; j < (a.top + kWarps - 1) / kWarps; ++j) {
+      kth = __reduce_max_sync(0xffffffffu, left);
+      const uint32_t who = __ballot_sync(0xffffffffu, left == kth);
+      if (lane == __ffs(who) - 1) left = 0;
+    }
+    if (lane == 0) floor_of[warp] = kth;
+  }
+  if (tid == 0) found = 0;
+  __syncthreads();
+  if (warp == 0) {
+    Stat t = lane < kWarps ? stats[lane] : Stat{neg_inf(), 0.f, 0.f};
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      Stat r;
+      r.m = __shfl_down_sync(0xffffffffu, t.m, o);
+      r.z = __shfl_down_sync(0xffffffffu, t.z, o);
+      r.w = __shfl_down_sync(0xffffffffu, t.w, o);
+      t = join(t, r);
+    }
+    if (lane == 0) cta = t;
+  }
+  if (a.top > 0) {
+    uint32_t floor = 0xFFFFFFFFu;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) floor = min(floor, floor_of[w]);
+    if (mine >= floor && any) {
+      for_elements<BF16>(row, v0, v1, end_elem, [&](float x, int64_t i) {
+        const uint64_t key = argmax_key(x, static_cast<uint32_t>(i));
+        if (static_cast<uint32_t>(key >> 32) >= floor) {
+          const int at = atomicAdd(&found, 1);
+          if (at < kCand) cand[at] = key;
+        }
+      });
+    }
+    if (tid < kMaxTop) best[tid] = 0;
+    __syncthreads();
+    const int n = found;
+    if (n <= kCand) {
+      for (int c = tid; c < n; c += kThreads) {
+        const uint64_t key = cand[c];
+        int above = 0;
+        for (int o = 0; o < n; ++o) above += cand[o] > key;
+        if (above < a.top) best[above] = key;
+      }
+    } else {
+      uint64_t prev = ~uint64_t(0);
+      for (int k = 0; k < a.top; ++k) {
+        uint64_t b = 0;
+        for_elements<BF16>(row, v0, v1, end_elem, [&](float x, int64_t i) {
+          const uint64_t key = argmax_key(x, static_cast<uint32_t>(i));
+          if (key < prev) b = umax64(b, key);
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) b = umax64(b, __shfl_xor_sync(0xffffffffu, b, o));
+        if (lane == 0) reduce[warp] = b;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) b = umax64(b, reduce[w]);
+        if (tid == 0) best[k] = b;
+        prev = b;
+        __syncthreads();
+        if (prev == 0) break;                          // fewer elements than asked for in this share
+      }
+    }
+  }
+  cluster.sync();
+  if (rank == 0) {
+    if (tid == 0) {
+      Stat t = cta;
+      for (int c = 1; c < C; ++c) t = join(t, *cluster.map_shared_rank(&cta, c));
+      const bool none = t.z == 0.f;                    // every logit is -inf
+      const float log_z = none ? neg_inf() : logf(t.z);
+      const float lse = t.m + log_z;
+      final_lse = lse;
+      if (a.lse != nullptr) a.lse[m] = lse;
+      if (a.entropy != nullptr) a.entropy[m] = none ? 0.f : log_z - t.w / t.z;
+      if (a.logprob != nullptr) {
+        const int64_t tok = a.tokens[m];
+        float lp = __int_as_float(0x7fc00000);         // no such token
+        if (tok >= 0 && tok < a.V) lp = none ? neg_inf() : row.at(tok) - lse;
+        a.logprob[m] = lp;
+      }
+    }
+    if (a.top > 0) {
+      for (int e = tid; e < a.top * C; e += kThreads) {
+        const int c = e / a.top;
+        all[e] = cluster.map_shared_rank(&best[0], c)[e - c * a.top];
+      }
+      __syncthreads();
+      const int n = a.top * C;
+      if (tid < n) {
+        const uint64_t key = all[tid];
+        int above = 0;
+        for (int o = 0; o < n; ++o) above += all[o] > key;
+        if (key != 0 && above < a.top) {
+          const float lse = final_lse;
+          a.top_idx[m * a.top + above] = argmax_index(key);
+          a.top_lp[m * a.top + above] = lse == neg_inf() ? neg_inf() : value_of(key) - lse;
+        }
+      }
+    }
+  }
+  cluster.sync();                                      // peers keep their shared memory until rank 0 has read it
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobsCall& c, const DeviceInfo& info, cudaStream_t s) {
+  Args a;
+  a.logits = static_cast<const uint8_t*>(c.logits);
+  a.V = c.V;
+  a.pitch = c.stride * (c.f32 ? 4 : 2);
+  a.tokens = c.tokens;
+  a.logprob = c.logprob;
+  a.entropy = c.entropy;
+  a.lse = c.lse;
+  a.top_idx = c.top_idx;
+  a.top_lp = c.top_lp;
+  a.top = c.top;
+  // as many CTAs a row as keep all rows' CTAs (two per SM) on the GPU at once
+  int cluster = kMaxCluster;
+  while (cluster > 1 && static_cast<int64_t>(c.M) * cluster > 2 * info.sms) cluster /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(c.M));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return c.f32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a) : cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a);
+}
+
+}  // namespace q4nx

@@ -59,7 +59,8 @@ enum q4nx_status {
     Q4NX_E_UNSUPPORTED = 8,     /* valid kind, but not for this operation / size       */
     Q4NX_E_CUDA = 9,            /* a CUDA call failed (launch error)                   */
     Q4NX_E_DEVICE_TIMEOUT = 10, /* a bounded in-kernel wait gave up (see q4nx_check)   */
-    Q4NX_E_DTYPE = 11           /* unknown output dtype                                */
+    Q4NX_E_DTYPE = 11,          /* unknown output dtype                                */
+    Q4NX_E_INDEX = 12           /* an index read on the device was out of range (see q4nx_check) */
 };
 
 /* Output element type of the products. */
@@ -220,6 +221,128 @@ int q4nx_pack_q4_1(int src_type, const void* src_dev, uint64_t src_bytes, int64_
  * the first NaN wins; +0 and -0 are equal.  1 <= M <= 65535, 1 <= V < 2^31. */
 int q4nx_argmax(const float* logits_dev, int M, int64_t V, int32_t* idx_dev, void* stream);
 
+/* ---- Operators around the products in a decode step -------------------- */
+
+/* A key/value cache held in 4 bits: pages of page_tokens tokens, handed out by
+ * the caller, each holding keys and values of kv_heads heads of head_dim
+ * channels.  A group of 32 channels of one token is kept as 4-bit codes with a
+ * bf16 scale and middle, value = (code - 8) * scale + mid: 0.625 bytes per
+ * value, 20 * head_dim bytes per 16 tokens and head (keys and values).  Page p
+ * starts at p * q4nx_kv_page_bytes; its bytes need no initial content, and
+ * their order inside a page is the library's own (q4nx_kv_read gives the values). */
+typedef struct q4nx_kv_cache {
+    void* pool_dev;           /* device, 16-byte aligned                          */
+    uint64_t bytes;           /* length of the pool                               */
+    int32_t head_dim;         /* 64, 128 or 256                                   */
+    int32_t kv_heads;         /* 1..1024                                          */
+    int32_t page_tokens;      /* positive multiple of 16                          */
+    int32_t reserved;         /* must be 0                                        */
+    int64_t pages;
+} q4nx_kv_cache;
+
+/* Bytes of one page, 0 for sizes that no cache has. */
+uint64_t q4nx_kv_page_bytes(int head_dim, int kv_heads, int page_tokens);
+
+/* The requests of one call.  Tokens q_start[b] .. q_start[b+1]-1 of the call's
+ * token arrays are the last ones of request b, whose cache holds lens[b]
+ * tokens with them: token j of its T has position lens[b] - T + j.  Position p
+ * lies in page table[b][p / page_tokens].  A request may have no tokens in the
+ * call.  Tokens from q_start[batch] on belong to no request.  Ranges out of order or
+ * outside 0..tokens, lengths below 0 or beyond the table, and table entries
+ * that are needed and not a page are skipped (nothing is read or written for
+ * them, outputs of the tokens concerned are undefined) and reported as
+ * Q4NX_E_INDEX by q4nx_check on the call's workspace. */
+typedef struct q4nx_kv_batch {
+    const int32_t* q_start_dev;   /* device int32 [batch + 1]                     */
+    const int32_t* lens_dev;      /* device int32 [batch]                         */
+    const int32_t* table_dev;     /* device int32 [batch][table_cols]             */
+    int32_t batch;                /* 1..1024                                      */
+    int32_t table_cols;
+    int64_t tokens;               /* rows of the call's token arrays, 0..INT32_MAX */
+} q4nx_kv_batch;
+
+/* Workspace of the three cache entry points (one size for all): zero-filled
+ * before its first use and again after Q4NX_E_DEVICE_TIMEOUT; partial results
+ * stay behind in it, so it is not shared with the GEMV or GEMM.  0 for a bad cache. */
+uint64_t q4nx_kv_workspace(const q4nx_kv_cache* cache);
+
+/* Quantize the call's new keys and values into the cache.
+ * k_dev, v_dev: bf16 [tokens][kv_heads][head_dim], kv_stride elements from token
+ * to token (a multiple of 8; both may be parts of one merged projection's output).
+ * Per group of 32 channels, each step one IEEE binary32 operation: lo, hi =
+ * min, max; scale = bf16((hi - lo) / 15); mid = bf16(lo + 8*scale); code =
+ * clamp(rint((x - mid) / scale), -8, 7) + 8, ties to even, 8 where scale is 0.
+ * A group that holds a NaN or an infinity, or whose range overflows binary32
+ * or bf16, reads as NaN.  Tokens at positions below 0 are not kept.  No two
+ * tokens of a call may have the same place (requests may share pages that none
+ * of them writes).  Only bytes of the new tokens are written. */
+int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* k_dev, const void* v_dev,
+                   int64_t kv_stride, void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
+/* The cached values of the call's tokens: k_dev, v_dev [tokens][kv_heads][head_dim]
+ * of out_dtype.  (code - 8) * scale is exact in binary32 and the addition of
+ * mid rounds once, bf16 once more; zero for tokens at positions below 0 or of no request. */
+int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k_dev, void* v_dev, int out_dtype,
+                 void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
+/* Attention of the call's tokens over their requests' caches:
+ *   out[t][h] = sum_j p_j v[j][h'] / sum_j p_j,  p_j = exp(scale * q[t][h] . k[j][h']),
+ * h' = h / (heads / kv_heads), over the positions j up to the token's own and,
+ * where window > 0, the last `window` of those.  The token's own key and value
+ * have to be in the cache (q4nx_kv_append comes first).
+ * q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token
+ * (a multiple of 8).  out_dev: [tokens][heads][head_dim] of out_dtype.  lse_dev:
+ * fp32 [tokens][heads], log sum_j p_j, or NULL.  heads: a multiple of kv_heads, up to 1024.
+ * A row that sees nothing (a position below 0) gives zeros and -Inf.  NaN and
+ * infinities in positions that a row does not see do not reach it.  Rows of
+ * tokens of no request are not written.
+ * Accuracy: the cached values enter exactly, sums are binary32; each weight
+ * p_j times a value scale is rounded to fp16 (2^-12 of itself).
+ * Deterministic: partial sums are joined in a fixed order. */
+int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
+                      int heads, float scale, int64_t window, void* out_dev, int out_dtype, float* lse_dev,
+                      void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
+/* Low-rank adapters of one projection, all of one rank (8, 16, 32, 64 or 128; a
+ * smaller adapter is padded with zeros). */
+typedef struct q4nx_adapters {
+    const void* a_dev;        /* bf16 [count][rank][cols], 16-byte aligned        */
+    const void* b_dev;        /* bf16 [count][rows][rank], 16-byte aligned        */
+    const float* scale_dev;   /* fp32 [count]                                     */
+    uint64_t a_bytes, b_bytes;
+    int32_t count;
+    int32_t rank;
+} q4nx_adapters;
+
+/* A shared projection with each token's own adapter, 1 <= M <= 64:
+ *   Y[m] = w X[m] + scale[id] * b[id] (a[id] X[m]),  id = ids[m];  id < 0: no adapter.
+ * Kinds, M, X, Y, out_dtype and workspace as for q4nx_gemm_m64 (whose accuracy
+ * the product with w has); the adapters' products are exact bf16 products
+ * summed in binary32, and the sum is rounded once.  An id of count or more
+ * adds nothing and is reported as Q4NX_E_INDEX by q4nx_check.  scratch_dev:
+ * q4nx_gemm_lora_scratch(w, M) bytes, 16-byte aligned, any content, free again
+ * after the call's work on the stream. */
+int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_adapters* adapters, const int32_t* ids_dev,
+                   void* Y_dev, int out_dtype, void* workspace_dev, uint64_t workspace_bytes, void* scratch_dev,
+                   uint64_t scratch_bytes, void* stream);
+uint64_t q4nx_gemm_lora_scratch(const q4nx_weight* w, int M);
+
+/* Log-probabilities of rows of logits (dtype Q4NX_OUT_F32 or Q4NX_OUT_BF16, [M][V], `stride`
+ * elements from row to row, no alignment beyond the element's):
+ *   lse = log sum exp x;  logprob[m] = x[tokens[m]] - lse;
+ *   entropy[m] = lse - sum p x,  p = exp(x - lse);
+ *   the `top` largest x of the row, largest first, ties to the lowest index:
+ *   top_idx[m][top], top_logprob[m][top] = x - lse.
+ * logprob (with tokens), entropy and lse may be NULL: not wanted.  0 <= top <=
+ * 32 and <= V; 1 <= M <= 65535; 1 <= V <= INT32_MAX.  A token outside 0..V-1 gives NaN.
+ * A logit of -Inf has probability 0; a row of nothing else gives lse and
+ * log-probabilities -Inf and entropy 0.  A NaN or +Inf in a row makes its
+ * numbers NaN; its indexes follow q4nx_argmax's order (NaN above +Inf).  All outputs fp32 / int32. */
+#define Q4NX_MAX_TOP 32
+int q4nx_logprobs(const void* logits_dev, int dtype, int M, int64_t V, int64_t stride, const int32_t* tokens_dev, int top,
+                  float* logprob_dev, float* entropy_dev, float* lse_dev, int32_t* top_idx_dev, float* top_logprob_dev,
+                  void* stream);
+
 /* GEMV without any allocation, for callers that may not allocate device memory
  * at all: code that runs under a strict no-allocation policy once set up (for
  * example a real-time decode loop, or a plug-in inside a framework that owns
@@ -256,7 +379,9 @@ int q4nx_check_noalloc(void* stream);
  * Returns Q4NX_OK, or Q4NX_E_DEVICE_TIMEOUT if a bounded in-kernel wait of a
  * call that used this workspace gave up (its outputs are then invalid, and
  * the workspace must be zero-filled before it is used again: the calls that
- * gave up may have left counters and posted sums in it). */
+ * gave up may have left counters and posted sums in it), or Q4NX_E_INDEX if
+ * such a call met an index out of range in device memory (a length, page or
+ * adapter; the workspace stays usable). */
 int q4nx_check(void* workspace_dev, void* stream);
 
 #ifdef __cplusplus
