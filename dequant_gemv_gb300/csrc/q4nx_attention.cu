@@ -26,14 +26,19 @@
 // rows side by side; movmatrix turns p*sv into the B operand of the second
 // product.
 //
-// Work: units (request, kv head, group of NT*8 query rows); their 16-token
-// blocks form one sequence that the CTAs divide evenly, so ragged lengths need
-// no plan.  A CTA has kWarps consumer warps, each taking every kWarps-th block
-// of the CTA's range from a ring of block copies that a producer warp keeps
-// full (lane = ring stage: each lane looks up its own pages and issues its own
-// bulk copy).  Units that end inside a CTA's range leave finished; a unit
-// split between CTAs leaves partial sums, and the CTA that posts last joins
-// them in the order of the CTAs, so the result does not depend on timing.
+// Work: units (request, kv head, group of NT*8 query rows); their 32-token
+// steps form one sequence of positions, divided between the CTAs so that ragged
+// lengths need no plan (a unit counts kUnitCost steps more than it has, for
+// its beginning and end), and a CTA's range evenly between its warps.  A warp
+// goes through its positions by itself and keeps copies of its next steps in
+// flight in a ring of its own: its lanes look up the pages of 32 steps at a
+// time, and lane 0 sends the next copy as soon as a stage is read out.  A unit
+// that ends inside a warp's range is written from its registers; what the
+// ranges cut is joined once, at the CTA's end, in shared memory, and units cut
+// between CTAs by the CTA that posts last, in the order of the CTAs, so that the
+// result does not depend on timing.  (With all warps of a CTA on one unit at
+// a time every unit cost the CTA 4 us of waiting and joining: 71 us instead
+// of XX for 48 requests of 600 to 6000 tokens, 8 kv heads.)
 #include "q4nx_kernels.h"
 #include "q4nx_kv.cuh"
 
@@ -41,22 +46,53 @@ namespace q4nx {
 
 namespace {
 
-constexpr int kWarps = 7;                        // consumer warps; with the producer 8, so that 128 (two CTAs per SM) or 255 registers are left a thread
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
 constexpr float kRefNone = -3.0e38f;             // reference of a row that has seen nothing
-constexpr int kSnapBlocks = 16;                  // units up to this many blocks are not split
-constexpr int kMinBlocks = 8;                    // fewer blocks than this are not worth a CTA
+constexpr int kUnitCost = 4;                     // what a unit costs besides its steps, in steps
+constexpr int kCutSteps = 4;                     // a unit is cut between CTAs only this far from its ends
+constexpr int kMinCost = kUnitCost + 2;          // less is not worth a CTA
+// 16-token blocks of one step (a ring stage), and stages of a warp's ring
+__host__ __device__ constexpr int step_blocks(int D) { return D == 256 ? 1 : 2; }
+__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 2 : 4; }
+__host__ __device__ constexpr int stage_bytes(int D) { return step_blocks(D) * kv_block_bytes(D); }
 
-// A multiple of kWarps: one warp consumes all phases of a stage in order (a
-// warp ahead of another by two phases would take an old phase's completion for its own).
-__host__ __device__ constexpr int ring_stages(int D) { return kWarps * (D == 256 ? 2 : D == 128 ? 3 : 4); }
-__host__ __device__ constexpr int row_pitch(int D) { return D + 4; }   // floats; rows 2i of a store fall on different banks
-__host__ __device__ constexpr size_t attention_smem(int D, int NT) {
-  return static_cast<size_t>(ring_stages(D)) * kv_block_bytes(D) +          // ring
-         static_cast<size_t>(kWarps) * 8 * NT * row_pitch(D) * 4 +          // the warps' sums
-         static_cast<size_t>(kWarps) * 8 * NT * 2 * 4 +                     // their references and totals
-         ring_stages(D) * 16 + (kKvMaxBatch + 1) * 8 + 16;
-}
+// The piece of a unit that a warp works on: what it has to know of it, in
+// shared memory (in registers it would push the running sums out).
+template <int RB>
+struct Piece {
+  int64_t q0, row0, T;      // first token of the request, first query row of the unit, tokens of the request
+  int64_t start, n, cost;   // the unit's first position, its steps, the costs before it
+  int h, rows;              // kv head, query rows
+  int first_full, end_full; // steps of the request that every row sees whole
+  int step0;                // the request's step at the warp's first position, as if the unit went back there
+  int end;                  // where the piece ends, in steps from the warp's first position
+  bool whole;               // all of the unit
+  int lo[RB], hi[RB];       // a row sees positions lo < p <= hi
+};
+
+// What is left to know of a unit of which a warp has a part.
+struct Cut {
+  int64_t q0, row0, start, n, cost;
+  int h, rows;
+};
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int RB = 8 * NT, S = ring_stages(D);
+  alignas(128) uint8_t ring[kWarps][S][stage_bytes(D)];
+  uint64_t full[kWarps][S];
+  alignas(16) const uint8_t* src[kWarps][32][step_blocks(D)];   // where the blocks of a warp's next 32 steps lie
+  Piece<RB> piece[kWarps];
+  // A warp's parts of cut units, entry 2*warp for the unit it began with, 2*warp
+  // + 1 for the one it ended with (start -1: none): reference and total of each row
+  Cut cut[2 * kWarps];
+  float2 ml[2 * kWarps][RB];
+  float2 total[2 * kWarps][RB];                       // those of the CTA's parts of the unit together
+  int64_t prefix[kKvMaxBatch + 1], cost[kKvMaxBatch + 1];
+  int64_t begin, end;
+  int stopped, joins[2];
+};
 
 struct AttnArgs {
   KvPool pool;
@@ -70,7 +106,8 @@ struct AttnArgs {
   float* lse;               // [tokens][heads] or NULL
   uint32_t* err;
   uint32_t* counters;       // [kKvMaxCtas], zero between calls
-  float* partial;           // [2*grid][RB][D + 2]
+  float* partial;           // [2*grid][RB][D + 2]: a CTA's parts of the unit it began and the one it ended with
+  float* stash;             // [grid][kWarps][RB*D]: a warp's part of the unit it began with
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -123,7 +160,6 @@ __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), e
 __device__ __forceinline__ float inv_pow2(float f) { return __uint_as_float((254u << 23) - __float_as_uint(f)); }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
 // N 32-bit words from shared memory (N = 1, 2 or 4).
 template <int N>
@@ -139,11 +175,16 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
   }
 }
 
-// How the blocks of all units are divided: position x of 0..total-1 is block
-// x - unit_start of a unit; the units of request b begin at prefix[b].
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {   // of numbers >= 0; short where they are
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// How the steps of all units are divided: position x is step x - start of a
+// unit; the units of request b begin at position prefix[b], and the costs
+// before them add up to cost[b].
 struct Plan {
-  const int64_t* prefix;    // shared memory, [batch + 1]
-  int64_t total;
+  const int64_t *prefix, *cost;    // shared memory, [batch + 1]
+  int64_t total;                   // of the costs
   int ctas;
   int batch;
 };
@@ -151,57 +192,65 @@ struct Plan {
 struct Unit {
   int b, h;
   int64_t rg;               // group of RB query rows
-  int64_t start, n;         // first position, number of blocks
-  int64_t first_block;      // first 16-token block of the request that any row sees
+  int64_t start, n;         // first position, number of steps
+  int64_t cost;             // the cost before it
+  int64_t first;            // first step of the request that any row sees
   KvRequest rq;
 };
 
-__device__ __forceinline__ int64_t first_visible_block(const KvRequest& rq, int64_t window) {
+template <int D>
+__device__ __forceinline__ int64_t first_visible_step(const KvRequest& rq, int64_t window) {
+  constexpr int kStepTokens = step_blocks(D) * kKvBlock;
   if (window <= 0) return 0;
   const int64_t f = rq.L - rq.T + 1 - window;
-  return f > 0 ? f / kKvBlock : 0;
+  return f > 0 ? f / kStepTokens : 0;
 }
-__device__ __forceinline__ int64_t unit_blocks(const KvRequest& rq, int64_t window) {
-  const int64_t n = (rq.L + kKvBlock - 1) / kKvBlock - first_visible_block(rq, window);
+template <int D>
+__device__ __forceinline__ int64_t unit_steps(const KvRequest& rq, int64_t window) {
+  constexpr int kStepTokens = step_blocks(D) * kKvBlock;
+  const int64_t n = (rq.L + kStepTokens - 1) / kStepTokens - first_visible_step<D>(rq, window);
   return n > 0 ? n : 1;     // an empty request's rows are written too
 }
 
-template <int RB>
-__device__ Unit find_unit(const AttnArgs& a, const Plan& pl, int64_t x) {
+// The unit that holds position x, or (by_cost) the one whose cost range holds x.
+template <int D, int RB>
+__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Plan& pl, int64_t x, bool by_cost = false) {
+  const int64_t* at = by_cost ? pl.cost : pl.prefix;
   int lo = 0, hi = pl.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (pl.prefix[mid] <= x) lo = mid;
+    if (at[mid] <= x) lo = mid;
     else hi = mid;
   }
   Unit u;
   u.b = lo;
   u.rq = kv_request(a.kb, a.pool.page_blocks, lo);
-  u.n = unit_blocks(u.rq, a.window);
-  u.first_block = first_visible_block(u.rq, a.window);
-  const int64_t groups = (u.rq.T * a.group + RB - 1) / RB;
-  const int64_t k = (x - pl.prefix[lo]) / u.n;
-  u.h = static_cast<int>(k / groups);
+  u.n = unit_steps<D>(u.rq, a.window);
+  u.first = first_visible_step<D>(u.rq, a.window);
+  const int64_t groups = quot(u.rq.T * a.group + RB - 1, RB);
+  const int64_t k = quot(x - at[lo], by_cost ? u.n + kUnitCost : u.n);
+  u.h = static_cast<int>(quot(k, groups));
   u.rg = k - u.h * groups;
   u.start = pl.prefix[lo] + k * u.n;
+  u.cost = pl.cost[lo] + k * (u.n + kUnitCost);
   return u;
 }
 
-// First position of CTA c: an even share, moved to the end of the unit it
-// falls into where that unit is too small to be split.
-template <int RB>
+// First position of CTA c: where its share of the costs begins, moved to the
+// end of a unit that it falls into less than kCutSteps from.
+template <int D, int RB>
 __device__ int64_t bound(const AttnArgs& a, const Plan& pl, int c) {
-  if (c >= pl.ctas) return pl.total;
-  const int64_t q = pl.total / pl.ctas, rest = pl.total - q * pl.ctas;
+  if (c >= pl.ctas) return pl.prefix[pl.batch];
+  const int64_t q = quot(pl.total, pl.ctas), rest = pl.total - q * pl.ctas;
   const int64_t x = q * c + (c < rest ? c : rest);
-  if (x >= pl.total) return pl.total;
-  const Unit u = find_unit<RB>(a, pl, x);
-  return (u.n <= kSnapBlocks && x != u.start) ? u.start + u.n : x;
+  const Unit u = find_unit<D, RB>(a, pl, x, true);
+  const int64_t in = x - u.cost - kUnitCost;
+  return u.start + (in < kCutSteps && in < u.n - kCutSteps + 1 ? 0 : in > u.n - kCutSteps ? u.n : in);
 }
-// The CTA whose even share holds position x.
+// The CTA whose share of the costs holds x.
 __device__ __forceinline__ int share_of(const Plan& pl, int64_t x) {
-  const int64_t q = pl.total / pl.ctas, rest = pl.total - q * pl.ctas;
-  return static_cast<int>(x < (q + 1) * rest ? x / (q + 1) : rest + (x - (q + 1) * rest) / q);
+  const int64_t q = quot(pl.total, pl.ctas), rest = pl.total - q * pl.ctas;
+  return static_cast<int>(x < (q + 1) * rest ? quot(x, q + 1) : rest + quot(x - (q + 1) * rest, q));
 }
 
 // The running state of a warp over its blocks of one piece of a unit.  Pairs
@@ -220,15 +269,15 @@ struct State {
 };
 
 template <int D, int NT>
-__device__ __forceinline__ void load_q(const AttnArgs& a, const Unit& u, State<D, NT>& st) {
+__device__ __forceinline__ void load_q(const AttnArgs& a, const Piece<8 * NT>& u, State<D, NT>& st) {
   constexpr int NG = D / 32;
   const int lane = threadIdx.x & 31, i = lane & 3, n = lane >> 2;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int64_t r = u.rg * (8 * NT) + 8 * t + n;
-    const int64_t tq = r / a.group;
-    const bool have = tq < u.rq.T;
-    const uint16_t* src = a.q + (u.rq.q0 + tq) * a.q_stride + static_cast<int64_t>(u.h * a.group + static_cast<int>(r - tq * a.group)) * D;
+    const int64_t r = u.row0 + 8 * t + n;
+    const int64_t tq = quot(r, a.group);
+    const bool have = tq < u.T;
+    const uint16_t* src = a.q + (u.q0 + tq) * a.q_stride + static_cast<int64_t>(u.h * a.group + static_cast<int>(r - tq * a.group)) * D;
     uint4 w[NG];
     float big = 0.f;
 #pragma unroll
@@ -294,15 +343,19 @@ __device__ __forceinline__ void reset(State<D, NT>& st) {
   }
 }
 
-// A row's new reference: y0, y1 its logits at this lane's two tokens, m0, m1
-// those tokens' largest value scales.  Returns the factor on the row's O; *f is that
-// on its sums of p.
-__device__ __forceinline__ float move_reference(float y0, float y1, float m0, float m1, float& ref, float& fs, float* f) {
-  float m = fmaxf(y0, y1);
+// A row's new reference: y(n) its logits at this lane's two tokens of block n,
+// m0, m1 those tokens' largest value scales.  Returns the factor on the row's O;
+// *f is that on its sums of p.
+template <int NB, typename Y>
+__device__ __forceinline__ float move_reference(Y y, const float (&m0)[NB], const float (&m1)[NB], float& ref, float& fs, float* f) {
+  float m = ref;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) m = fmaxf(m, fmaxf(y(n).x, y(n).y));
 #pragma unroll
   for (int x = 16; x > 2; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  m = fmaxf(m, ref);
-  float tm = fmaxf(ex2(y0 - m) * m0, ex2(y1 - m) * m1);
+  float tm = 0.f;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) tm = fmaxf(tm, fmaxf(ex2(y(n).x - m) * m0[n], ex2(y(n).y - m) * m1[n]));
 #pragma unroll
   for (int x = 16; x > 2; x >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
   *f = ex2(ref - m);
@@ -317,104 +370,119 @@ __device__ __forceinline__ float move_reference(float y0, float y1, float m0, fl
   return of;
 }
 
-// One block of 16 tokens (shared-memory address `blk`).  MASK: some row does
-// not see some token; `seen` then has bit 4t + e set where row e&1 of tile t sees
-// token lane/4 + 8*(e>>1).
-template <int D, int NT, bool MASK>
-__device__ __forceinline__ void block_step(State<D, NT>& st, uint32_t blk, uint32_t seen) {
-  constexpr int NG = D / 32, NH = (NG + 3) / 4, NW = NG < 4 ? NG : 4;
+// NB blocks of 16 tokens (shared-memory address `blk0`), taken together: two
+// give the scheduler twice the independent work between the dependent stages
+// (34.3 us for the loop over 131071 tokens; 35.6 one at a time).  Where `full` is
+// not set some row does not see some token: bit 4t + e of seen[n] is set where
+// row e&1 of tile t sees token lane/4 + 8*(e>>1) of block n, and clear_hidden has
+// made the blocks' values finite.
+template <int D, int NT, int NB>
+__device__ __forceinline__ void block_step(State<D, NT>& st, uint32_t blk0, bool full, const uint32_t (&seen)[NB]) {
+  constexpr int NG = D / 32, NH = (NG + 3) / 4, NW = NG < 4 ? NG : 4, BB = kv_block_bytes(D);
   const int lane = threadIdx.x & 31, i = lane & 3, tk = lane >> 2;
   const float none = -__int_as_float(0x7f800000);
-  float s[NT][4];
-  // mid * Q
+  float s[NB][NT][4];
+  uint32_t v0[NB][NG / 2], v1[NB][NG / 2];                       // value scales of tokens tk, tk + 8
+  float m0[NB], m1[NB];                                          // the largest of each token
 #pragma unroll
-  for (int hf = 0; hf < NH; ++hf) {
-    const int g = NG < 4 ? (i & (NG - 1)) : 4 * hf + i;
-    const uint32_t z0 = lds_u16(blk + 17 * D + (tk * NG + g) * 2) * 0x10001u;
-    const uint32_t z1 = lds_u16(blk + 17 * D + ((tk + 8) * NG + g) * 2) * 0x10001u;
+  for (int n = 0; n < NB; ++n) {
+    const uint32_t blk = blk0 + n * BB;
+    // mid * Q
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (hf == 0) mma<false>(s[t], z0, z1, z0, z1, st.qs[t][hf][0], st.qs[t][hf][1], 0.f, 0.f, 0.f, 0.f);
-      else mma_add<false>(s[t], z0, z1, z0, z1, st.qs[t][hf][0], st.qs[t][hf][1]);
-    }
-  }
-#pragma unroll
-  for (int hf = 0; hf < NH; ++hf) {
-    uint32_t w0[NW], w1[NW];                                     // the codes of tokens tk and tk + 8
-    lds_words<NW>(w0, blk + hf * 1024 + lane * (4 * NW));
-    lds_words<NW>(w1, blk + hf * 1024 + (lane + 32) * (4 * NW));
-    uint32_t s0[NW / 2], s1[NW / 2];
-    lds_words<NW / 2>(s0, blk + 16 * D + tk * (2 * NG) + 8 * hf);
-    lds_words<NW / 2>(s1, blk + 16 * D + (tk + 8) * (2 * NG) + 8 * hf);
-#pragma unroll
-    for (int gw = 0; gw < NW; ++gw) {
-      const int g = 4 * hf + gw;
-      const uint32_t x0 = w0[gw], x1 = w1[gw], y0 = x0 >> 8, y1 = x1 >> 8;
-      constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;
-      const float k0 = gw & 1 ? bf_hi(s0[gw >> 1]) : bf_lo(s0[gw >> 1]);
-      const float k1 = gw & 1 ? bf_hi(s1[gw >> 1]) : bf_lo(s1[gw >> 1]);
+    for (int hf = 0; hf < NH; ++hf) {
+      const int g = NG < 4 ? (i & (NG - 1)) : 4 * hf + i;
+      const uint32_t z0 = lds_u16(blk + 17 * D + (tk * NG + g) * 2) * 0x10001u;
+      const uint32_t z1 = lds_u16(blk + 17 * D + ((tk + 8) * NG + g) * 2) * 0x10001u;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float acc[4];
-        mma<true>(acc, x0 & kLo, x1 & kLo, x0 & kHi, x1 & kHi, st.qb[t][g][0], st.qb[t][g][1], st.q8[t][g].x, st.q8[t][g].y,
-                  st.q8[t][g].x, st.q8[t][g].y);
-        mma_add<true>(acc, y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi, st.qb[t][g][2], st.qb[t][g][3]);
-        const float2 a = ffma2(both(k0), make_float2(acc[0], acc[1]), make_float2(s[t][0], s[t][1]));
-        const float2 b = ffma2(both(k1), make_float2(acc[2], acc[3]), make_float2(s[t][2], s[t][3]));
-        s[t][0] = a.x, s[t][1] = a.y, s[t][2] = b.x, s[t][3] = b.y;
+        if (hf == 0) mma<false>(s[n][t], z0, z1, z0, z1, st.qs[t][hf][0], st.qs[t][hf][1], 0.f, 0.f, 0.f, 0.f);
+        else mma_add<false>(s[n][t], z0, z1, z0, z1, st.qs[t][hf][0], st.qs[t][hf][1]);
       }
     }
-  }
-  // the value scales of tokens tk, tk + 8, and the largest of each
-  uint32_t v0[NG / 2], v1[NG / 2];
-  if constexpr (NG == 8) {
-    lds_words<4>(v0, blk + 18 * D + tk * 16);
-    lds_words<4>(v1, blk + 18 * D + (tk + 8) * 16);
-  } else {
-    lds_words<NG / 2>(v0, blk + 18 * D + tk * (2 * NG));
-    lds_words<NG / 2>(v1, blk + 18 * D + (tk + 8) * (2 * NG));
-  }
-  float m0 = 0x1p-100f, m1 = 0x1p-100f;                          // not 0: a p without bound has to be seen
 #pragma unroll
-  for (int e = 0; e < NG / 2; ++e) {
-    m0 = fmaxf(m0, fmaxf(bf_lo(v0[e]), bf_hi(v0[e])));
-    m1 = fmaxf(m1, fmaxf(bf_lo(v1[e]), bf_hi(v1[e])));
+    for (int hf = 0; hf < NH; ++hf) {
+      uint32_t w0[NW], w1[NW];                                   // the codes of tokens tk and tk + 8
+      lds_words<NW>(w0, blk + hf * 1024 + lane * (4 * NW));
+      lds_words<NW>(w1, blk + hf * 1024 + (lane + 32) * (4 * NW));
+      uint32_t s0[NW / 2], s1[NW / 2];
+      lds_words<NW / 2>(s0, blk + 16 * D + tk * (2 * NG) + 8 * hf);
+      lds_words<NW / 2>(s1, blk + 16 * D + (tk + 8) * (2 * NG) + 8 * hf);
+#pragma unroll
+      for (int gw = 0; gw < NW; ++gw) {
+        const int g = 4 * hf + gw;
+        const uint32_t x0 = w0[gw], x1 = w1[gw], y0 = x0 >> 8, y1 = x1 >> 8;
+        constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;
+        const float k0 = gw & 1 ? bf_hi(s0[gw >> 1]) : bf_lo(s0[gw >> 1]);
+        const float k1 = gw & 1 ? bf_hi(s1[gw >> 1]) : bf_lo(s1[gw >> 1]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float acc[4];
+          mma<true>(acc, x0 & kLo, x1 & kLo, x0 & kHi, x1 & kHi, st.qb[t][g][0], st.qb[t][g][1], st.q8[t][g].x, st.q8[t][g].y,
+                    st.q8[t][g].x, st.q8[t][g].y);
+          mma_add<true>(acc, y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi, st.qb[t][g][2], st.qb[t][g][3]);
+          const float2 a = ffma2(both(k0), make_float2(acc[0], acc[1]), make_float2(s[n][t][0], s[n][t][1]));
+          const float2 b = ffma2(both(k1), make_float2(acc[2], acc[3]), make_float2(s[n][t][2], s[n][t][3]));
+          s[n][t][0] = a.x, s[n][t][1] = a.y, s[n][t][2] = b.x, s[n][t][3] = b.y;
+        }
+      }
+    }
+    if constexpr (NG == 8) {
+      lds_words<4>(v0[n], blk + 18 * D + tk * 16);
+      lds_words<4>(v1[n], blk + 18 * D + (tk + 8) * 16);
+    } else {
+      lds_words<NG / 2>(v0[n], blk + 18 * D + tk * (2 * NG));
+      lds_words<NG / 2>(v1[n], blk + 18 * D + (tk + 8) * (2 * NG));
+    }
+    m0[n] = m1[n] = 0x1p-100f;                                   // not 0: a p without bound has to be seen
+#pragma unroll
+    for (int e = 0; e < NG / 2; ++e) {
+      m0[n] = fmaxf(m0[n], fmaxf(bf_lo(v0[n][e]), bf_hi(v0[n][e])));
+      m1[n] = fmaxf(m1[n], fmaxf(bf_lo(v1[n][e]), bf_hi(v1[n][e])));
+    }
   }
   // logits of tile t relative to `ref`, -inf where not seen
-  auto logits = [&](int t, float2 ref, float2& y0, float2& y1) {
-    y0 = ffma2(make_float2(s[t][0], s[t][1]), st.cr[t], ref);
-    y1 = ffma2(make_float2(s[t][2], s[t][3]), st.cr[t], ref);
-    if constexpr (MASK) {
-      const uint32_t h = seen >> (4 * t);
+  auto logits = [&](int n, int t, float2 ref, float2& y0, float2& y1) {
+    y0 = ffma2(make_float2(s[n][t][0], s[n][t][1]), st.cr[t], ref);
+    y1 = ffma2(make_float2(s[n][t][2], s[n][t][3]), st.cr[t], ref);
+    if (!full) {
+      const uint32_t h = seen[n] >> (4 * t);
       y0 = make_float2(h & 1 ? y0.x : none, h & 2 ? y0.y : none);
       y1 = make_float2(h & 4 ? y1.x : none, h & 8 ? y1.y : none);
     }
   };
-  float2 p0[NT], p1[NT], f0[NT], f1[NT];                         // p at tokens tk, tk + 8; times fs
+  float2 p0[NB][NT], p1[NB][NT];                                 // p at tokens tk, tk + 8
   auto weights = [&](int t) {
-    float2 y0, y1;
-    logits(t, make_float2(-st.ref[t].x, -st.ref[t].y), y0, y1);
-    p0[t] = ex2(y0);
-    p1[t] = ex2(y1);
-    f0[t] = mul2(p0[t], st.fs[t]);
-    f1[t] = mul2(p1[t], st.fs[t]);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float2 y0, y1;
+      logits(n, t, make_float2(-st.ref[t].x, -st.ref[t].y), y0, y1);
+      p0[n][t] = ex2(y0);
+      p1[n][t] = ex2(y1);
+    }
   };
   float top = 0.f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     weights(t);
-    top = fmaxf(top, fmaxf(fmaxf(f0[t].x, f0[t].y) * m0, fmaxf(f1[t].x, f1[t].y) * m1));
+    float2 big = both(0.f);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      big.x = fmaxf(big.x, fmaxf(p0[n][t].x * m0[n], p1[n][t].x * m1[n]));
+      big.y = fmaxf(big.y, fmaxf(p0[n][t].y * m0[n], p1[n][t].y * m1[n]));
+    }
+    top = fmaxf(top, fmaxf(big.x * st.fs[t].x, big.y * st.fs[t].y));
   }
   // The reference and the power of two move only when p * scale outgrows its
-  // place (below 2^10 when it was set, 2^13 is let pass), so that most blocks
-  // rescale nothing; a first block's p is infinite and moves them.
+  // place (below 2^10 when it was set, 2^13 is let pass), so that most steps
+  // rescale nothing; a first step's p is infinite and moves them.
   if (__any_sync(0xffffffffu, top > 8192.f)) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float2 y0, y1, f, of;
-      logits(t, both(0.f), y0, y1);
-      of.x = move_reference(y0.x, y1.x, m0, m1, st.ref[t].x, st.fs[t].x, &f.x);
-      of.y = move_reference(y0.y, y1.y, m0, m1, st.ref[t].y, st.fs[t].y, &f.y);
+      float2 y0[NB], y1[NB], f, of;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) logits(n, t, both(0.f), y0[n], y1[n]);
+      of.x = move_reference<NB>([&](int n) { return make_float2(y0[n].x, y1[n].x); }, m0, m1, st.ref[t].x, st.fs[t].x, &f.x);
+      of.y = move_reference<NB>([&](int n) { return make_float2(y0[n].y, y1[n].y); }, m0, m1, st.ref[t].y, st.fs[t].y, &f.y);
       st.l[t] = mul2(st.l[t], f);
       st.corr[t][0] *= f.x;
       st.corr[t][1] *= f.y;
@@ -428,212 +496,405 @@ __device__ __forceinline__ void block_step(State<D, NT>& st, uint32_t blk, uint3
       weights(t);
     }
   }
-  // sum of p * mid: mids [group][token] as A, p in two bf16 parts as B
-  {
-    const int g = tk & (NG - 1);
-    uint32_t z[2];
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z[0]) : "r"(blk + 19 * D + g * 32 + 4 * i));
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z[1]) : "r"(blk + 19 * D + g * 32 + 4 * i + 16));
-    if constexpr (MASK) {
-      // unseen tokens may hold anything, and 0 times it has to be 0; a NaN that a
-      // row does see reaches it through the scale, which is NaN with the mid
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if ((z[e] & 0x7F80u) == 0x7F80u) z[e] &= 0xFFFF0000u;
-        if ((z[e] & 0x7F800000u) == 0x7F800000u) z[e] &= 0xFFFFu;
-      }
-    }
+  for (int n = 0; n < NB; ++n) {
+    const uint32_t blk = blk0 + n * BB;
+    // sum of p * mid: mids [group][token] as A, p in two bf16 parts as B
+    const int g0 = tk & (NG - 1);
+    uint32_t z[2];
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z[0]) : "r"(blk + 19 * D + g0 * 32 + 4 * i));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z[1]) : "r"(blk + 19 * D + g0 * 32 + 4 * i + 16));
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      st.l[t] = fadd2(st.l[t], fadd2(p0[t], p1[t]));
-      const uint32_t h0 = pack_bf16x2(p0[t].x, p0[t].y), h1 = pack_bf16x2(p1[t].x, p1[t].y);
-      const uint32_t r0 = pack_bf16x2(p0[t].x - bf_lo(h0), p0[t].y - bf_hi(h0));
-      const uint32_t r1 = pack_bf16x2(p1[t].x - bf_lo(h1), p1[t].y - bf_hi(h1));
+      const float2 q0 = p0[n][t], q1 = p1[n][t];
+      st.l[t] = fadd2(st.l[t], fadd2(q0, q1));
+      const uint32_t h0 = pack_bf16x2(q0.x, q0.y), h1 = pack_bf16x2(q1.x, q1.y);
+      const uint32_t r0 = pack_bf16x2(q0.x - bf_lo(h0), q0.y - bf_hi(h0));
+      const uint32_t r1 = pack_bf16x2(q1.x - bf_lo(h1), q1.y - bf_hi(h1));
       mma_add<false>(st.corr[t], z[0], 0u, z[1], 0u, movmatrix(h0), movmatrix(h1));
       mma_add<false>(st.corr[t], z[0], 0u, z[1], 0u, movmatrix(r0), movmatrix(r1));
+      p0[n][t] = mul2(q0, st.fs[t]);
+      p1[n][t] = mul2(q1, st.fs[t]);
+    }
+    // values: group g is the channel tiles 2g, 2g + 1
+#pragma unroll
+    for (int q = 0; q < D / 64; ++q) {
+      uint32_t w[4];
+      lds_words<4>(w, blk + 8 * D + (q * 32 + lane) * 16);
+#pragma unroll
+      for (int gg = 0; gg < 2; ++gg) {
+        const int g = 2 * q + gg;
+        const float u0 = g & 1 ? bf_hi(v0[n][g >> 1]) : bf_lo(v0[n][g >> 1]);
+        const float u1 = g & 1 ? bf_hi(v1[n][g >> 1]) : bf_lo(v1[n][g >> 1]);
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float2 x0 = mul2(p0[n][t], both(u0)), x1 = mul2(p1[n][t], both(u1));
+          b[t][0] = movmatrix(pack_f16x2(x0.x, x0.y));
+          b[t][1] = movmatrix(pack_f16x2(x1.x, x1.y));
+        }
+#pragma unroll
+        for (int mm = 0; mm < 2; ++mm) {
+          // fp16 1024 + c less 1032, and 1024 + 16c less 1152
+          const uint32_t x = w[2 * gg + mm], y = x >> 8;
+          const uint32_t c0 = hadd2(lop3_and_or(x, 0x000F000Fu, 0x64006400u), 0xE408E408u);
+          const uint32_t c1 = hadd2(lop3_and_or(x, 0x00F000F0u, 0x64006400u), 0xE480E480u);
+          const uint32_t c2 = hadd2(lop3_and_or(y, 0x000F000Fu, 0x64006400u), 0xE408E408u);
+          const uint32_t c3 = hadd2(lop3_and_or(y, 0x00F000F0u, 0x64006400u), 0xE480E480u);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_add<true>(st.o[t][2 * g + mm], c0, c1, c2, c3, b[t][0], b[t][1]);
+        }
+      }
     }
   }
-  // values: group g is the channel tiles 2g, 2g + 1
+}
+
+// The rows that see the tokens of block `blk` (16 positions), as block_step wants them.
+template <int NT>
+__device__ __forceinline__ uint32_t seen_bits(const Piece<8 * NT>& u, int blk) {
+  const int lane = threadIdx.x & 31, i = lane & 3, tk = lane >> 2;
+  uint32_t seen = 0;
 #pragma unroll
-  for (int q = 0; q < D / 64; ++q) {
-    uint32_t w[4];
-    lds_words<4>(w, blk + 8 * D + (q * 32 + lane) * 16);
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int gg = 0; gg < 2; ++gg) {
-      const int g = 2 * q + gg;
-      const float u0 = g & 1 ? bf_hi(v0[g >> 1]) : bf_lo(v0[g >> 1]);
-      const float u1 = g & 1 ? bf_hi(v1[g >> 1]) : bf_lo(v1[g >> 1]);
-      uint32_t b[NT][2];
+    for (int e = 0; e < 4; ++e) {
+      const int r = 8 * t + 2 * i + (e & 1), tok = blk * kKvBlock + tk + 8 * (e >> 1);
+      if (tok <= u.hi[r] && tok > u.lo[r]) seen |= 1u << (4 * t + e);
+    }
+  return seen;
+}
+
+// Makes 0 * value 0 in a block (address `at`, 16 positions from tok0) that some
+// row does not see whole.  Tokens that no row sees may hold anything: their value
+// scales and mids become 0.  A token that some rows see may be kept as NaN:
+// it becomes 0 too, and the rows that see it get their NaN here, in that group
+// alone (its logit, where the key is NaN, is masked row by row in any case).
+template <int D, int NT>
+__device__ __forceinline__ void clear_hidden(State<D, NT>& st, const Piece<8 * NT>& u, uint32_t at, int tok0, uint32_t seen) {
+  constexpr int NG = D / 32;
+  const int lane = threadIdx.x & 31, i = lane & 3, tk = lane >> 2;
+  bool odd = false;                                              // a scale that is no number, on this lane's token
+  if (lane < kKvBlock) {
+    const bool hidden = tok0 + lane <= u.lo[0] || tok0 + lane > u.hi[u.rows - 1];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float2 x0 = mul2(f0[t], both(u0)), x1 = mul2(f1[t], both(u1));
-        if constexpr (MASK) {                                    // an unseen token's scale may be anything
-          const uint32_t h = seen >> (4 * t);
-          x0 = make_float2(h & 1 ? x0.x : 0.f, h & 2 ? x0.y : 0.f);
-          x1 = make_float2(h & 4 ? x1.x : 0.f, h & 8 ? x1.y : 0.f);
+    for (int g = 0; g < NG; ++g) {
+      const uint32_t s_at = at + 18 * D + (lane * NG + g) * 2, m_at = at + 19 * D + (g * kKvBlock + lane) * 2;
+      if (hidden) {
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(s_at), "h"(static_cast<uint16_t>(0)) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(m_at), "h"(static_cast<uint16_t>(0)) : "memory");
+      } else {
+        odd |= (lds_u16(s_at) & 0x7F80u) == 0x7F80u;
+      }
+    }
+  }
+  if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+    for (int g = 0; g < NG; ++g) {
+      bool bad[2];                                               // this lane's tokens tk, tk + 8
+#pragma unroll
+      for (int h = 0; h < 2; ++h) bad[h] = (lds_u16(at + 18 * D + ((tk + 8 * h) * NG + g) * 2) & 0x7F80u) == 0x7F80u;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool hit = (bad[0] && (seen >> (4 * t + e) & 1)) || (bad[1] && (seen >> (4 * t + e + 2) & 1));
+          if (__ballot_sync(0xffffffffu, hit) & (0x11111111u << i))
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m)
+              if ((m >> 1) == g) st.o[t][m][e] = st.o[t][m][e + 2] = __int_as_float(0x7fc00000);
         }
-        b[t][0] = movmatrix(pack_f16x2(x0.x, x0.y));
-        b[t][1] = movmatrix(pack_f16x2(x1.x, x1.y));
-      }
+      __syncwarp();
 #pragma unroll
-      for (int mm = 0; mm < 2; ++mm) {
-        // fp16 1024 + c less 1032, and 1024 + 16c less 1152
-        const uint32_t x = w[2 * gg + mm], y = x >> 8;
-        const uint32_t c0 = hadd2(lop3_and_or(x, 0x000F000Fu, 0x64006400u), 0xE408E408u);
-        const uint32_t c1 = hadd2(lop3_and_or(x, 0x00F000F0u, 0x64006400u), 0xE480E480u);
-        const uint32_t c2 = hadd2(lop3_and_or(y, 0x000F000Fu, 0x64006400u), 0xE408E408u);
-        const uint32_t c3 = hadd2(lop3_and_or(y, 0x00F000F0u, 0x64006400u), 0xE480E480u);
+      for (int h = 0; h < 2; ++h)
+        if (bad[h] && i == 0) {
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 18 * D + ((tk + 8 * h) * NG + g) * 2), "h"(static_cast<uint16_t>(0)) : "memory");
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 19 * D + (g * kKvBlock + tk + 8 * h) * 2), "h"(static_cast<uint16_t>(0)) : "memory");
+        }
+    }
+  }
+  // the stage's next content comes by an asynchronous copy: it is ordered after these stores
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
+// The piece of unit u that begins at position from + n of the warp whose range is [from, to).
+template <int D, int NT>
+__device__ __forceinline__ void set_piece(const AttnArgs& a, const Unit& u, Piece<8 * NT>& p, int64_t from, int64_t to, int n) {
+  constexpr int RB = 8 * NT, kStepTokens = step_blocks(D) * kKvBlock;
+  const int lane = threadIdx.x & 31;
+  const int64_t x = from + n;
+  const int64_t base = u.rq.L - u.rq.T, row0 = u.rg * RB;
+  const int64_t left = u.rq.T * a.group - row0, rows = left < RB ? left : RB;
+  __syncwarp();                                                  // the previous piece is read out
+  if (lane == 0) {
+    p.q0 = u.rq.q0;
+    p.row0 = row0;
+    p.T = u.rq.T;
+    p.start = u.start;
+    p.n = u.n;
+    p.cost = u.cost;
+    p.h = u.h;
+    p.rows = static_cast<int>(rows);
+    const int64_t pos_first = base + quot(row0, a.group), pos_last = base + quot(row0 + rows - 1, a.group);
+    const int64_t hidden = a.window > 0 ? pos_last - a.window : -1;          // the last position that some row does not see
+    p.first_full = hidden < 0 ? 0 : static_cast<int>(hidden / kStepTokens + 1);
+    p.end_full = pos_first < 0 ? 0 : static_cast<int>((pos_first + 1) / kStepTokens);
+    p.step0 = static_cast<int>(u.first + (x - u.start) - n);
+    const int64_t end = u.start + u.n < to ? u.start + u.n : to;
+    p.end = static_cast<int>(end - from);
+    p.whole = x == u.start && end == u.start + u.n;
+  }
+  if (lane < RB) {
+    const int64_t pos = base + quot(row0 + lane, a.group);
+    p.hi[lane] = static_cast<int>(pos < u.rq.L ? pos : u.rq.L - 1);
+    p.lo[lane] = static_cast<int>(a.window > 0 && pos - a.window > -1 ? pos - a.window : -1);
+  }
+  __syncwarp();
+}
+
+// Row `row` of request (q0), kv head h: its place among the outputs' rows.
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, int64_t q0, int h, int64_t row) {
+  const int64_t tq = quot(row, a.group);
+  return (q0 + tq) * a.heads + h * a.group + (row - tq * a.group);
+}
+template <typename Out>
+__device__ __forceinline__ void put(const AttnArgs& a, int64_t at, float y) {
+  if constexpr (sizeof(Out) == 4) static_cast<float*>(a.out)[at] = y;
+  else static_cast<uint16_t*>(a.out)[at] = f32_to_bf16_bits(y);
+}
+__device__ __forceinline__ float log_total(float m, float l) {
+  return l == 0.f ? -__int_as_float(0x7f800000) : (m + lg2(l)) * 0.693147180559945f;
+}
+
+// The parts of unit u, cut between CTAs c0..c1, joined by the CTA that posted
+// last, in the order of the CTAs.  `ring` is free.
+template <int D, int NT, typename Out>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, Smem<D, NT>& sm, const Cut& u, int c0, int c1) {
+  constexpr int RB = 8 * NT, kBatch = 10;
+  constexpr int64_t kPitch = RB * (D + 2);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, parts = c1 - c0 + 1, rows = u.rows;
+  auto part = [&](int c) { return a.partial + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * kPitch; };
+  float2* ml = reinterpret_cast<float2*>(sm.ring);             // [parts][RB]
+  float2* total = ml + kKvMaxCtas * RB;                        // [RB]
+  static_assert(sizeof(float2) * (kKvMaxCtas + 1) * RB <= sizeof(sm.ring));
+  // items of 4 channels, each by `ways` threads (a power of two) that take every ways-th part
+  const int items = rows * (D / 4);
+  int ways = 1;
+  while (2 * ways * items <= kThreads) ways *= 2;
+  __syncthreads();
+  for (int j = tid; j < parts * RB; j += kThreads)
+    if (j % RB < rows) ml[j] = __ldcg(reinterpret_cast<const float2*>(part(j / RB) + RB * D) + j % RB);
+#pragma unroll 1
+  for (int j0 = 0; j0 < items * ways; j0 += kThreads) {
+    const int j = j0 + tid, way = j & (ways - 1), item = j / ways, r = item / (D / 4);
+    const bool have = item < items;
+    float4 v[kBatch], o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_add<true>(st.o[t][2 * g + mm], c0, c1, c2, c3, b[t][0], b[t][1]);
+    for (int k = 0; k < kBatch; ++k)
+      if (have && way + k * ways < parts) v[k] = __ldcg(reinterpret_cast<const float4*>(part(way + k * ways)) + item);
+    if (j0 == 0) {                                              // the weights, while the first loads are under way
+      __syncthreads();
+      for (int q = warp; q < rows; q += kWarps) {
+        float m = kRefNone, l = 0.f;
+        for (int c = lane; c < parts; c += 32) m = fmaxf(m, ml[c * RB + q].x);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        for (int c = lane; c < parts; c += 32) {
+          const float2 w = ml[c * RB + q];
+          const float f = ex2(w.x - m);
+          ml[c * RB + q].x = f;
+          l = fmaf(f, w.y, l);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        if (lane == 0) total[q] = make_float2(m, l);
       }
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int c = way;;) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (have && c + k * ways < parts) {
+          const float f = ml[(c + k * ways) * RB + r].x;
+          o.x = fmaf(f, v[k].x, o.x), o.y = fmaf(f, v[k].y, o.y), o.z = fmaf(f, v[k].z, o.z), o.w = fmaf(f, v[k].w, o.w);
+        }
+      c += kBatch * ways;
+      if (c >= parts) break;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (have && c + k * ways < parts) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c + k * ways)) + item);
+    }
+    // the ways of an item are neighbouring lanes: a fixed tree
+    for (int x = 1; x < ways && x < 32; x <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+    }
+    if (have && way == 0) {
+      const float2 t = total[r];
+      const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
+      const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
+      const int64_t d = at * D + (item & (D / 4 - 1)) * 4;
+      put<Out>(a, d, t.y == 0.f ? 0.f : o.x * inv);
+      put<Out>(a, d + 1, t.y == 0.f ? 0.f : o.y * inv);
+      put<Out>(a, d + 2, t.y == 0.f ? 0.f : o.z * inv);
+      put<Out>(a, d + 3, t.y == 0.f ? 0.f : o.w * inv);
+      if ((item & (D / 4 - 1)) == 0 && a.lse != nullptr) a.lse[at] = log_total(t.x, t.y);
     }
   }
 }
 
 template <int D, int NT, typename Out>
 __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attention_kernel(const AttnArgs a) {
-  constexpr int RB = 8 * NT, S = ring_stages(D), BB = kv_block_bytes(D), NG = D / 32;
-  static_assert(S % kWarps == 0 && S <= 32);
+  constexpr int RB = 8 * NT, S = ring_stages(D), SB = step_blocks(D), BB = kv_block_bytes(D), NG = D / 32;
+  constexpr int kRegs = NT * (D / 16) * 4;                       // a lane's share of a warp's sums
+  // blocks of a step taken together, as far as the registers reach
+  constexpr int NB = D == 64 || (D == 128 && NT == 1) ? 2 : 1;
+  static_assert(D == 256 || NT > 1 || sizeof(Smem<D, NT>) <= 113 * 1024);      // two CTAs per SM
+  static_assert(kRegs * 128 <= S * stage_bytes(D));              // a warp's sums fit its ring
   extern __shared__ __align__(128) uint8_t smem[];
-  float* sum = reinterpret_cast<float*>(smem + S * BB);                    // [warp][RB][row_pitch]
-  float* ml = sum + kWarps * RB * row_pitch(D);                            // [warp][RB][2]
-  uint64_t* full = reinterpret_cast<uint64_t*>(ml + kWarps * RB * 2);
-  uint64_t* empty = full + S;
-  int64_t* prefix = reinterpret_cast<int64_t*>(empty + S);
-  int* flag = reinterpret_cast<int*>(prefix + kKvMaxBatch + 1);            // [0] joins, [1] a wait gave up
+  Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (lane < S) {
+    mbar_init(&sm.full[warp][lane], 1);
+    fence_barrier_init();
+  }
+  if (lane < 2) sm.cut[2 * warp + lane].start = -1;
+  if (tid == 0) {
+    sm.prefix[0] = sm.cost[0] = 0;
+    sm.stopped = 0;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // the requests' blocks and their prefix sums
+  // the requests' steps and costs, and their prefix sums
   const int B = a.kb.batch;
   for (int b = tid; b < B; b += kThreads) {
     const KvRequest rq = kv_request(a.kb, a.pool.page_blocks, b);
     if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
-    prefix[b + 1] = rq.T > 0 ? (rq.T * a.group + RB - 1) / RB * a.pool.kv_heads * unit_blocks(rq, a.window) : 0;
-  }
-  if (tid == 0) {
-    prefix[0] = 0;
-    flag[1] = 0;
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    fence_barrier_init();
+    const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<D>(rq, a.window);
+    sm.prefix[b + 1] = units * n;
+    sm.cost[b + 1] = units * (n + kUnitCost);
   }
   __syncthreads();
-  if (warp == 0) {
-    int64_t run = 0;
+  if (warp < 2) {
+    int64_t *sum = warp ? sm.cost : sm.prefix, run = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
-      int64_t v = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+      int64_t v = b0 + lane < B ? sum[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
       }
       v += run;
-      if (b0 + lane < B) prefix[b0 + lane + 1] = v;
+      if (b0 + lane < B) sum[b0 + lane + 1] = v;
       run = __shfl_sync(0xffffffffu, v, 31);
     }
   }
   __syncthreads();
   Plan pl;
-  pl.prefix = prefix;
-  pl.total = prefix[B];
+  pl.prefix = sm.prefix;
+  pl.cost = sm.cost;
   pl.batch = B;
-  const int64_t want = pl.total / kMinBlocks;
+  pl.total = sm.cost[B];
+  const int64_t want = pl.total / kMinCost;
   pl.ctas = want < 1 ? 1 : want < gridDim.x ? static_cast<int>(want) : gridDim.x;
   if (pl.total == 0 || blockIdx.x >= pl.ctas) return;
-  const int64_t begin = bound<RB>(a, pl, blockIdx.x), end = bound<RB>(a, pl, blockIdx.x + 1);
-  if (begin >= end) return;
+  if (tid < 2) (tid ? sm.end : sm.begin) = bound<D, RB>(a, pl, blockIdx.x + tid);
+  __syncthreads();
+  if (sm.begin >= sm.end) return;
+  const int steps = static_cast<int>(sm.end - sm.begin);
+  const int first = static_cast<int>(static_cast<int64_t>(steps) * warp / kWarps);       // this warp's steps of the CTA's
+  const int mine = static_cast<int>(static_cast<int64_t>(steps) * (warp + 1) / kWarps) - first;
 
-  if (warp == kWarps) {
-    // ---- producer: lane s fills stage s ----
-    if (lane < S) {
-      uint32_t phase = 1;
-      bool ok = true;
-      Unit u = {};
-      for (int64_t x = begin + lane; x < end; x += S) {
-        if (x >= u.start + u.n) u = find_unit<RB>(a, pl, x);
-        const int64_t blk = u.first_block + (x - u.start);
-        const uint8_t* src = blk * kKvBlock < u.rq.L ? kv_block_ptr(a.pool, a.kb, D, u.b, u.h, blk) : nullptr;
-        if (src == nullptr && blk * kKvBlock < u.rq.L) atomicOr(a.err, kErrIndex);
-        if (!mbar_wait_bounded(&empty[lane], phase)) {           // a fresh barrier passes a wait for phase 1
-          atomicOr(a.err, kErrTimeout);
-          ok = false;
-          break;
+  // The blocks of the warp's steps `from` .. +31 (step `from` lies in unit u); nullptr: nothing to copy.
+  auto look_up = [&](int from, Unit u) {
+    if (from + lane < mine) {
+      const int64_t x = sm.begin + first + from + lane;
+      if (x >= u.start + u.n) u = find_unit<D, RB>(a, pl, x);
+#pragma unroll
+      for (int j = 0; j < SB; ++j) {
+        const int64_t blk = (u.first + (x - u.start)) * SB + j;
+        const uint8_t* at = nullptr;
+        if (blk * kKvBlock < u.rq.L) {
+          at = kv_block_ptr(a.pool, a.kb, D, u.b, u.h, blk);
+          if (at == nullptr) atomicOr(a.err, kErrIndex);
         }
-        if (src != nullptr) {
-          mbar_arrive_expect_tx(&full[lane], BB);
-          bulk_g2s(smem + lane * BB, src, BB, &full[lane]);
-        } else {
-          mbar_arrive_expect_tx(&full[lane], 0);
-        }
-        phase ^= 1;
+        sm.src[warp][lane][j] = at;
       }
-      // the copy that nobody took (a wait gave up) lands before the CTA leaves
-      if (!ok) mbar_wait_bounded(&full[lane], phase);
     }
-    return;
+    __syncwarp();
+  };
+  // Send the copies of the warp's step n into its stage.
+  auto fetch = [&](int n) {
+    if (lane == 0) {
+      const int stage = n % S;
+      const uint8_t* at[SB];
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int j = 0; j < SB; ++j) {
+        at[j] = sm.src[warp][n & 31][j];
+        bytes += at[j] != nullptr ? BB : 0;
+      }
+      mbar_arrive_expect_tx(&sm.full[warp][stage], bytes);
+#pragma unroll
+      for (int j = 0; j < SB; ++j)
+        if (at[j] != nullptr) bulk_g2s(sm.ring[warp][stage] + j * BB, at[j], BB, &sm.full[warp][stage]);
+    }
+    __syncwarp();
+  };
+  if (mine > 0) {
+    const Unit u = find_unit<D, RB>(a, pl, sm.begin + first);
+    look_up(0, u);
+    for (int n = 0; n < S && n < mine; ++n) fetch(n);
+    set_piece<D, NT>(a, u, sm.piece[warp], sm.begin + first, sm.begin + first + mine, 0);
   }
 
-  // ---- consumers ----
   State<D, NT> st;
   const int i = lane & 3, tk = lane >> 2;
-  const uint32_t ring = smem_u32(smem);
-  for (int64_t ps = begin; ps < end;) {
-    const Unit u = find_unit<RB>(a, pl, ps);
-    const int64_t pe = u.start + u.n < end ? u.start + u.n : end;
-    load_q<D, NT>(a, u, st);
+  Piece<RB>& p = sm.piece[warp];
+  bool ok = true;
+  for (int n = 0; n < mine;) {
+    if (n > 0) set_piece<D, NT>(a, find_unit<D, RB>(a, pl, sm.begin + first + n), p, sm.begin + first, sm.begin + first + mine, n);
+    load_q<D, NT>(a, p, st);
     reset<D, NT>(st);
-    const int64_t base = u.rq.L - u.rq.T;
-    const int64_t row0 = u.rg * RB;
-    const int64_t rows = u.rq.T * a.group - row0 < RB ? u.rq.T * a.group - row0 : RB;
-    // blocks that every row sees whole: first_full <= block < end_full
-    const int64_t pos_first = base + row0 / a.group, pos_last = base + (row0 + rows - 1) / a.group;
-    const int64_t hidden = a.window > 0 ? pos_last - a.window : -1;          // the last position that some row does not see
-    const int first_full = hidden < 0 ? 0 : static_cast<int>(hidden / kKvBlock + 1);
-    const int end_full = pos_first < 0 ? 0 : static_cast<int>((pos_first + 1) / kKvBlock);
-    // positions that this lane's rows see: lo < position <= hi (none for rows beyond the last)
-    int lo[NT][2], hi[NT][2];
+    for (const int end = p.end; n < end; ++n) {
+      const int stage = n % S;
+      if (!mbar_wait_bounded(&sm.full[warp][stage], (n / S) & 1)) ok = false;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int step = p.step0 + n;
+      const uint32_t addr = smem_u32(sm.ring[warp][stage]);
+      const bool full = step >= p.first_full && step < p.end_full;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int j = 0; j < SB; j += NB) {
+        uint32_t seen[NB] = {};
+        if (!full) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int64_t r = row0 + 8 * t + 2 * i + e;
-        const int64_t pos = base + r / a.group;
-        hi[t][e] = static_cast<int>(pos < u.rq.L ? pos : u.rq.L - 1);
-        lo[t][e] = static_cast<int>(a.window > 0 && pos - a.window > -1 ? pos - a.window : -1);
-      }
-    const int skip = static_cast<int>((ps - begin) % kWarps);
-    uint32_t k = static_cast<uint32_t>(ps - begin) + (warp >= skip ? warp - skip : warp - skip + kWarps);
-    const uint32_t k_end = static_cast<uint32_t>(pe - begin);
-    const int blk0 = static_cast<int>(u.first_block + (ps - u.start)) - static_cast<int>(ps - begin);
-    for (; k < k_end; k += kWarps) {
-      const uint32_t round = k / S, stage = k - round * S;
-      if (!mbar_wait_bounded(&full[stage], round & 1)) {
-        flag[1] = 1;
-        atomicOr(a.err, kErrTimeout);
-        break;
-      }
-      const int blk = blk0 + static_cast<int>(k);
-      const uint32_t addr = ring + stage * BB;
-      if (blk >= first_full && blk < end_full) {
-        block_step<D, NT, false>(st, addr, 0);
-      } else {
-        uint32_t seen = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = blk * kKvBlock + tk + 8 * (e >> 1);
-            if (tok <= hi[t][e & 1] && tok > lo[t][e & 1]) seen |= 1u << (4 * t + e);
+          for (int m = 0; m < NB; ++m) {
+            const int blk = step * SB + j + m;
+            seen[m] = seen_bits<NT>(p, blk);
+            clear_hidden<D, NT>(st, p, addr + (j + m) * BB, blk * kKvBlock, seen[m]);
           }
-        block_step<D, NT, true>(st, addr, seen);
+        }
+        block_step<D, NT, NB>(st, addr + j * BB, full, seen);
       }
-      __syncwarp();
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty[stage])) : "memory");
+      __syncwarp();                                               // the stage is read out
+      if (n + S < mine) {
+        if (((n + S) & 31) == 0) look_up(n + S, find_unit<D, RB>(a, pl, sm.begin + first + n + S));
+        fetch(n + S);
+      }
     }
-    // this warp's sums, in the values' own units
+    if (!__all_sync(0xffffffffu, ok)) {
+      // a wait gave up: the copies under way land before the CTA leaves
+      if (lane == 0) {
+        sm.stopped = 1;
+        atomicOr(a.err, kErrTimeout);
+      }
+      for (int m = n; m < n + S && m < mine; ++m) mbar_wait_bounded(&sm.full[warp][m % S], (m / S) & 1);
+      break;
+    }
+    // the sums in the values' own units, the totals complete in every lane
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const float2 back = make_float2(inv_pow2(st.fs[t].x), inv_pow2(st.fs[t].y));
@@ -642,102 +903,145 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
         st.l[t].x += __shfl_xor_sync(0xffffffffu, st.l[t].x, o);
         st.l[t].y += __shfl_xor_sync(0xffffffffu, st.l[t].y, o);
       }
-      float* row = sum + (warp * RB + 8 * t + 2 * i) * row_pitch(D);
-      float* next = row + row_pitch(D);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const float z0 = __shfl_sync(0xffffffffu, st.corr[t][0], 4 * g + i), z1 = __shfl_sync(0xffffffffu, st.corr[t][1], 4 * g + i);
 #pragma unroll
         for (int m = 2 * g; m < 2 * g + 2; ++m) {
-          row[16 * m + tk] = fmaf(st.o[t][m][0], back.x, z0);
-          next[16 * m + tk] = fmaf(st.o[t][m][1], back.y, z1);
-          row[16 * m + tk + 8] = fmaf(st.o[t][m][2], 0.0625f * back.x, z0);
-          next[16 * m + tk + 8] = fmaf(st.o[t][m][3], 0.0625f * back.y, z1);
-        }
-      }
-      if (tk == 0) {
-        float* at = ml + (warp * RB + 8 * t + 2 * i) * 2;
-        at[0] = st.ref[t].x;
-        at[1] = st.l[t].x;
-        at[2] = st.ref[t].y;
-        at[3] = st.l[t].y;
-      }
-    }
-    bar_consumers();
-    const bool whole = ps == u.start && pe == u.start + u.n;
-    const int slot = 2 * blockIdx.x + (ps == begin ? 0 : 1);
-    float* part = a.partial + static_cast<int64_t>(slot) * RB * (D + 2);
-    for (int idx = tid; idx < static_cast<int>(rows) * D; idx += kWarps * 32) {
-      const int r = idx / D, d = idx - r * D;
-      float m = ml[r * 2];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, ml[(w * RB + r) * 2]);
-      float o = 0.f, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(ml[(w * RB + r) * 2] - m);
-        o = fmaf(f, sum[(w * RB + r) * row_pitch(D) + d], o);
-        l = fmaf(f, ml[(w * RB + r) * 2 + 1], l);
-      }
-      if (whole) {
-        const int64_t rr = row0 + r, tq = rr / a.group;
-        const int64_t at = (u.rq.q0 + tq) * a.heads + u.h * a.group + (rr - tq * a.group);
-        const float y = l == 0.f ? 0.f : o / l;
-        if constexpr (sizeof(Out) == 4) static_cast<float*>(a.out)[at * D + d] = y;
-        else static_cast<uint16_t*>(a.out)[at * D + d] = f32_to_bf16_bits(y);
-        if (d == 0 && a.lse != nullptr) a.lse[at] = l == 0.f ? -__int_as_float(0x7f800000) : (m + lg2(l)) * 0.693147180559945f;
-      } else {
-        __stcg(part + r * D + d, o);
-        if (d == 0) {
-          __stcg(part + RB * D + 2 * r, m);
-          __stcg(part + RB * D + 2 * r + 1, l);
+          st.o[t][m][0] = fmaf(st.o[t][m][0], back.x, z0);
+          st.o[t][m][1] = fmaf(st.o[t][m][1], back.y, z1);
+          st.o[t][m][2] = fmaf(st.o[t][m][2], 0.0625f * back.x, z0);
+          st.o[t][m][3] = fmaf(st.o[t][m][3], 0.0625f * back.y, z1);
         }
       }
     }
-    if (!whole) {
-      // the CTAs that hold a piece of this unit; the last one to post joins them
-      const int c0 = share_of(pl, u.start), c1 = share_of(pl, u.start + u.n - 1);
-      __threadfence();
-      bar_consumers();
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(a.counters + c0, 1u);
-        const bool last = before == static_cast<uint32_t>(c1 - c0);
-        if (last) a.counters[c0] = 0;
-        flag[0] = last;
-      }
-      bar_consumers();
-      if (flag[0]) {
-        __threadfence();
-        // CTA c0's piece is its first one only where its range begins with the unit
-        const int first = 2 * c0 + (bound<RB>(a, pl, c0) == u.start ? 0 : 1);
-        const int64_t pitch = static_cast<int64_t>(RB) * (D + 2);
-        const float* p0 = a.partial + first * pitch;
-        for (int idx = tid; idx < static_cast<int>(rows) * D; idx += kWarps * 32) {
-          const int r = idx / D, d = idx - r * D;
-          float m = __ldcg(p0 + RB * D + 2 * r);
-          for (int c = c0 + 1; c <= c1; ++c) m = fmaxf(m, __ldcg(a.partial + 2 * c * pitch + RB * D + 2 * r));
-          float f = ex2(__ldcg(p0 + RB * D + 2 * r) - m);
-          float o = f * __ldcg(p0 + r * D + d), l = f * __ldcg(p0 + RB * D + 2 * r + 1);
-#pragma unroll 4
-          for (int c = c0 + 1; c <= c1; ++c) {
-            const float* p = a.partial + 2 * c * pitch;
-            f = ex2(__ldcg(p + RB * D + 2 * r) - m);
-            o = fmaf(f, __ldcg(p + r * D + d), o);
-            l = fmaf(f, __ldcg(p + RB * D + 2 * r + 1), l);
+    if (p.whole) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * t + 2 * i + e;
+          if (r < p.rows) {
+            const float l = e ? st.l[t].y : st.l[t].x, inv = 1.f / l;
+            const int64_t at = out_row(a, p.q0, p.h, p.row0 + r);
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+              put<Out>(a, at * D + 16 * m + tk, l == 0.f ? 0.f : st.o[t][m][e] * inv);
+              put<Out>(a, at * D + 16 * m + tk + 8, l == 0.f ? 0.f : st.o[t][m][e + 2] * inv);
+            }
+            if (tk == 0 && a.lse != nullptr) a.lse[at] = log_total(e ? st.ref[t].y : st.ref[t].x, l);
           }
-          const int64_t rr = row0 + r, tq = rr / a.group;
-          const int64_t at = (u.rq.q0 + tq) * a.heads + u.h * a.group + (rr - tq * a.group);
-          const float y = l == 0.f ? 0.f : o / l;
-          if constexpr (sizeof(Out) == 4) static_cast<float*>(a.out)[at * D + d] = y;
-          else static_cast<uint16_t*>(a.out)[at * D + d] = f32_to_bf16_bits(y);
-          if (d == 0 && a.lse != nullptr) a.lse[at] = l == 0.f ? -__int_as_float(0x7f800000) : (m + lg2(l)) * 0.693147180559945f;
+        }
+    } else {
+      // a part: of the unit the warp began with (it goes on with others) or ended with
+      const int which = n < mine ? 0 : 1;
+      float* to = which ? reinterpret_cast<float*>(sm.ring[warp]) + lane
+                        : a.stash + (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * (RB * D) + lane;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[32 * ((t * (D / 16) + m) * 4 + e)] = st.o[t][m][e];
+        if (tk == 0) {
+          sm.ml[2 * warp + which][8 * t + 2 * i] = make_float2(st.ref[t].x, st.l[t].x);
+          sm.ml[2 * warp + which][8 * t + 2 * i + 1] = make_float2(st.ref[t].y, st.l[t].y);
         }
       }
+      if (lane == 0) sm.cut[2 * warp + which] = {p.q0, p.row0, p.start, p.n, p.cost, p.h, p.rows};
     }
-    bar_consumers();                                             // the sums are read out
-    if (flag[1]) break;
-    ps = pe;
   }
+  __syncthreads();
+  if (sm.stopped) return;
+
+  // Weights of the parts: entry c, row r against the largest reference among
+  // the entries of the same unit.
+  for (int j = tid; j < 2 * kWarps * RB; j += kThreads) {
+    const int c = j / RB, r = j % RB;
+    const int64_t unit = sm.cut[c].start;
+    float m = kRefNone, l = 0.f;
+#pragma unroll 4
+    for (int o = 0; o < 2 * kWarps; ++o)
+      if (sm.cut[o].start == unit && unit >= 0) m = fmaxf(m, sm.ml[o][r].x);
+#pragma unroll 4
+    for (int o = 0; o < 2 * kWarps; ++o)
+      if (sm.cut[o].start == unit && unit >= 0) l = fmaf(ex2(sm.ml[o][r].x - m), sm.ml[o][r].y, l);
+    sm.total[c][r] = make_float2(m, l);
+  }
+  // the entries with a part, and those that begin a unit
+  const int64_t mine_at = lane < 2 * kWarps ? sm.cut[lane].start : -1;
+  const uint32_t parts = __ballot_sync(0xffffffffu, mine_at >= 0), below = parts & ((1u << lane) - 1);
+  const int64_t before = __shfl_sync(0xffffffffu, mine_at, below ? 31 - __clz(below) : lane);
+  uint32_t begins = __ballot_sync(0xffffffffu, mine_at >= 0 && (below == 0 || before != mine_at));
+  __syncthreads();
+  int edge[2] = {-1, -1};                                         // entries of units cut between CTAs: begun before this one, going on after it
+  constexpr int kEach = kRegs * 32 / kThreads;                    // a thread's places of the sums: register warp%4 + ..., lane
+  const int e = warp & 3, d0 = 16 * (warp >> 2) + tk + 8 * (e >> 1);     // channels d0 + 32 j of rows row, row + 8
+  const int row = 2 * i + (e & 1);
+#pragma unroll 1
+  while (begins != 0) {
+    const int e0 = __ffs(begins) - 1;
+    begins &= begins - 1;
+    uint32_t left = parts & ~((1u << e0) - 1) & (begins ? (begins & (0u - begins)) - 1 : ~0u);
+    const Cut& u = sm.cut[e0];
+    const bool inside = u.start >= sm.begin && u.start + u.n <= sm.end;
+    const int which = u.start >= sm.begin ? 1 : 0;
+    if (!inside) edge[which] = e0;
+    float o[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) o[j] = 0.f;
+#pragma unroll 1
+    for (; left != 0; left &= left - 1) {
+      const int c = __ffs(left) - 1;
+      const float* from = c & 1 ? reinterpret_cast<const float*>(sm.ring[c >> 1])
+                                : a.stash + (static_cast<int64_t>(blockIdx.x) * kWarps + (c >> 1)) * (RB * D);
+      float x[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) x[j] = from[tid + kThreads * j];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float f = ex2(sm.ml[c][row + 8 * t].x - sm.total[c][row + 8 * t].x);
+#pragma unroll
+        for (int j = 0; j < kEach / NT; ++j) o[t * (kEach / NT) + j] = fmaf(f, x[t * (kEach / NT) + j], o[t * (kEach / NT) + j]);
+      }
+    }
+    float* part = a.partial + static_cast<int64_t>(2 * blockIdx.x + which) * RB * (D + 2);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = row + 8 * t;
+      if (r >= u.rows) break;
+      const float2 v = sm.total[e0][r];
+      const bool head = e < 2 && warp < 4 && tk == 0;             // one thread per row
+      if (inside) {
+        const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
+        const float inv = v.y == 0.f ? 0.f : 1.f / v.y;
+#pragma unroll
+        for (int j = 0; j < kEach / NT; ++j) put<Out>(a, at * D + d0 + 32 * j, v.y == 0.f ? 0.f : o[t * (kEach / NT) + j] * inv);
+        if (head && a.lse != nullptr) a.lse[at] = log_total(v.x, v.y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kEach / NT; ++j) __stcg(part + r * D + d0 + 32 * j, o[t * (kEach / NT) + j]);
+        if (head) __stcg(reinterpret_cast<float2*>(part + RB * D) + r, v);
+      }
+    }
+  }
+  if (edge[0] < 0 && edge[1] < 0) return;
+  __syncthreads();
+  // the CTAs with a part of a unit: those whose shares begin where it may be cut, and the one before
+  if (tid < 2 && edge[tid] >= 0) {
+    const Cut& u = sm.cut[edge[tid]];
+    const int c0 = share_of(pl, u.cost + kUnitCost + kCutSteps - 1), c1 = share_of(pl, u.cost + kUnitCost + u.n - kCutSteps);
+    // release: the CTA's parts, stored before the barrier, come first; acquire: the last one sees the others'
+    uint32_t count;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(count) : "l"(a.counters + c0) : "memory");
+    const bool last = count == static_cast<uint32_t>(c1 - c0);
+    if (last) a.counters[c0] = 0;
+    sm.joins[tid] = last ? c0 << 16 | c1 : -1;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k)
+    if (edge[k] >= 0 && sm.joins[k] >= 0) join_parts<D, NT, Out>(a, sm, sm.cut[edge[k]], sm.joins[k] >> 16, sm.joins[k] & 0xFFFF);
 }
 
 template <int D, int NT, typename Out>
@@ -748,7 +1052,7 @@ cudaError_t launch_variant(const AttnArgs& a, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = attention_smem(D, NT);
+  cfg.dynamicSmemBytes = sizeof(Smem<D, NT>);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -761,7 +1065,9 @@ cudaError_t launch_variant(const AttnArgs& a, int grid, cudaStream_t s) {
 }  // namespace
 
 uint64_t attention_workspace_bytes(int D) {
-  return 16 + kKvMaxCtas * 4 + static_cast<uint64_t>(2 * kKvMaxCtas) * 16 * (D + 2) * 4;
+  // the error word, a counter per CTA, and per CTA (half as many with two row
+  // tiles) two parts of 8 rows and one of each warp
+  return 16 + kKvMaxCtas * 4 + static_cast<uint64_t>(kKvMaxCtas) * 8 * (2 * (D + 2) + kWarps * D) * 4;
 }
 
 cudaError_t launch_attention(int D, const KvPool& pool, const KvBatch& kb, const void* q, int64_t q_stride, int heads,
@@ -786,7 +1092,9 @@ cudaError_t launch_attention(int D, const KvPool& pool, const KvBatch& kb, const
   const int64_t rows = kb.tokens * a.group;
   const bool two = rows > static_cast<int64_t>(8) * kb.batch;
   const int per_sm = D == 256 || two ? 1 : 2;
-  const int grid = info.sms * per_sm < kKvMaxCtas ? info.sms * per_sm : kKvMaxCtas;
+  const int most = two ? kKvMaxCtas / 2 : kKvMaxCtas;
+  const int grid = info.sms * per_sm < most ? info.sms * per_sm : most;
+  a.stash = a.partial + static_cast<int64_t>(kKvMaxCtas) * 8 * 2 * (D + 2);
 #define Q4NX_ATTN(DD)                                                                                             \
   case DD:                                                                                                        \
     return two ? (out_f32 ? launch_variant<DD, 2, float>(a, grid, s) : launch_variant<DD, 2, uint16_t>(a, grid, s)) \
