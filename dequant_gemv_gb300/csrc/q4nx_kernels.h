@@ -100,14 +100,15 @@ struct LoraCall {
   const void *x, *a, *b;       // bf16 [M][K], [count][R][K], [count][N][R]
   const float* scale;          // [count]
   const int32_t* ids;          // [M]
-  float* t;                    // scratch [64][R]
+  float* t;                    // scratch: lora_splits(K) * 64 * R numbers, then 64 pairs of int
   const float* base;           // the product with W, binary32 [M][N] (may be y)
   void* y;                     // [M][N]
   uint32_t* err;
   int64_t K, N;
   int M, R, count;
 };
-cudaError_t launch_lora_shrink(const LoraCall& c, cudaStream_t s);
+int lora_splits(int64_t K);     // parts into which shrink cuts the columns
+cudaError_t launch_lora_shrink(const LoraCall& c, const DeviceInfo& info, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraCall& c, int out_f32, cudaStream_t s);
 
 // ---- log-probabilities ----

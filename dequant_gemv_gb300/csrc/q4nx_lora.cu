@@ -2,9 +2,10 @@
 //   Y[m] = W x_m + s[id_m] * B[id_m] (A[id_m] x_m),   id_m < 0: W x_m alone.
 // Two kernels around the product with W: `shrink` forms t_m = s * A x_m
 // (binary32, [64][rank]), `expand` adds B t_m to the product's binary32 output
-// and rounds once.  Both are bound by the adapters' bytes when the requests
-// use many (64 adapters of rank 16 at 12288 x 4096: 34 MB beside 31 MB of W),
-// so each reads an adapter once per launch however many tokens use it.
+// and rounds once.  Both are bound by the adapters' bytes when the requests use many (64 adapters of rank 16 at
+// 12288 x 4096: 34 MB beside 31 MB of W), and by latency otherwise: each
+// issues all loads of a step before the first product.
+#include <algorithm>
 #include <cooperative_groups.h>
 
 #include "q4nx_kernels.h"
@@ -24,12 +25,13 @@ struct LoraArgs {
   const uint16_t* b;        // [count][N][R]
   const float* scale;       // [count]
   const int32_t* ids;       // [M]
-  float* t;                 // [64][R]
+  float* t;                 // [splits][64][R]
+  int2* sorted;             // [M]: the tokens with their adapters, in the order of the adapters
   const float* base;        // [M][N]
   void* y;                  // [M][N]
   uint32_t* err;
   int64_t K, N;
-  int M, R, count;
+  int M, R, count, splits;
 };
 
 // A token's adapter, -1 for none; one outside the pool is reported and adds nothing.
@@ -50,110 +52,156 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// t = s * A x of every token of one adapter, 16 rows of A: a cluster of 8 CTAs
-// of 8 warps divides the columns in steps of 32 (lane 4n + i of a step holds
-// columns 8i..8i+7 of A's rows n, n + 8 and of token n: two k16 products, the
-// columns in the same order on both sides, every load 16 bytes).  The warps' sums meet in
-// shared memory and the CTAs' through distributed shared memory, in a fixed
-// order.  Grid: (8, rank/16, M); a cluster whose token is not the first of its
-// adapter has nothing to do.
-constexpr int kShrinkCluster = 8, kShrinkWarps = 8;
+// t = s * A x of every token, in items: one adapter, 16 rows of A, kSplitCols
+// columns (or their share, where the columns are cut into kMaxSplits parts,
+// which `expand` adds in order).  A cluster of 8 CTAs of 8 warps divides an
+// item's columns in steps of 32 (lane 4n + i of a step holds columns
+// 8i..8i+7 of A's rows n, n + 8 and of token n: two k16 products, the columns in
+// the same order on both sides, every load 16 bytes): two steps a warp, whose loads
+// are issued together.  What counts is how many loads the whole GPU has in
+// flight: without the parts, at rank 64, 12288 columns and 64 tokens, 32 CTAs took
+// 33 us.  The warps' sums meet in shared memory and the CTAs'
+// through distributed shared memory, in a fixed order.
+constexpr int kShrinkWarps = 8, kShrinkCluster = 8, kShrinkPerSm = 3;
+constexpr int kSplitCols = 4096, kMaxSplits = 8;
 
-__global__ void __cluster_dims__(kShrinkCluster, 1, 1) __launch_bounds__(kShrinkWarps * 32)
-    lora_shrink_kernel(const LoraArgs p) {
-  __shared__ int ids[kMaxTokens], list[kMaxTokens];
+__global__ void __cluster_dims__(kShrinkCluster, 1, 1) __launch_bounds__(kShrinkWarps * 32, kShrinkPerSm) lora_shrink_kernel(const LoraArgs p) {
+  __shared__ int ids[kMaxTokens], list[kMaxTokens], lead[kMaxTokens];
+  __shared__ uint32_t leads[2];
   __shared__ int count;
   __shared__ float part[kShrinkWarps][16][kMaxTokens + 1];
-  __shared__ float cta[16][kMaxTokens];
+  __shared__ float sum[kMaxTokens][16];
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster.block_rank());
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid < kMaxTokens) ids[tid] = adapter_of(p, tid);
   __syncthreads();
-  const int u = blockIdx.z, id = ids[u];
-  bool first = id >= 0;
-  for (int m = 0; m < u; ++m) first &= ids[m] != id;
-  if (!first) return;                                    // the whole cluster alike
-  if (tid == 0) {
-    int n = 0;
-    for (int m = u; m < p.M; ++m)
-      if (ids[m] == id) list[n++] = m;
-    count = n;
+  if (tid < kMaxTokens) {                                  // the first token of each adapter, in order
+    const int id = ids[tid];
+    bool first = id >= 0;
+#pragma unroll 8
+    for (int m = 0; m < kMaxTokens; ++m) first &= m >= tid || ids[m] != id;
+    const uint32_t b = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) leads[warp] = b;
+    __syncwarp();
   }
   __syncthreads();
-  const int n = count, tiles = (n + 7) / 8;
-  const int i = lane & 3, q = lane >> 2, r0 = blockIdx.y * 16;
-  const bool row1 = r0 + q + 8 < p.R;                    // rank is a multiple of 8
-  const uint16_t* a0 = p.a + (static_cast<int64_t>(id) * p.R + r0 + q) * p.K + 8 * i;
-  const uint16_t* a1 = a0 + 8 * p.K;
-  float acc[8][4] = {};
-  const int64_t steps = p.K / 32, stride = kShrinkCluster * kShrinkWarps;
-  for (int64_t s = rank * kShrinkWarps + warp; s < steps; s += stride) {
-    const uint4 wa = __ldg(reinterpret_cast<const uint4*>(a0 + 32 * s));
-    uint4 wb = make_uint4(0, 0, 0, 0);
-    if (row1) wb = __ldg(reinterpret_cast<const uint4*>(a1 + 32 * s));
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t >= tiles) break;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (8 * t + q < n) x = __ldg(reinterpret_cast<const uint4*>(p.x + list[8 * t + q] * p.K + 32 * s + 8 * i));
-      mma_bf16(acc[t], wa.x, wb.x, wa.y, wb.y, x.x, x.y);
-      mma_bf16(acc[t], wa.z, wb.z, wa.w, wb.w, x.z, x.w);
+  if (tid < kMaxTokens && (leads[warp] >> lane & 1))
+    lead[(warp ? __popc(leads[0]) : 0) + __popc(leads[warp] & ((1u << lane) - 1))] = tid;
+  if (blockIdx.x == 0 && tid < p.M) {                       // for `expand`
+    int at = 0;
+    const int id = ids[tid];
+#pragma unroll 8
+    for (int m = 0; m < kMaxTokens; ++m) at += m < p.M && (ids[m] < id || (ids[m] == id && m < tid));
+    p.sorted[at] = make_int2(tid, id);
+  }
+  const int adapters = __popc(leads[0]) + __popc(leads[1]), tiles_r = (p.R + 15) / 16;
+  const int items = adapters * tiles_r * p.splits;
+  const int i = lane & 3, q = lane >> 2;
+  const int64_t steps = p.K / 32;
+#pragma unroll 1
+  for (int item = blockIdx.x / kShrinkCluster; item < items; item += gridDim.x / kShrinkCluster) {      // the whole cluster alike
+    const int split = item % p.splits, r0 = item / p.splits % tiles_r * 16;
+    __syncthreads();                                       // lead is written; the last item's list and part are read
+    const int u = lead[item / p.splits / tiles_r], id = ids[u];
+    if (warp < 2) {                                        // its tokens, in order
+      const uint32_t lo = __ballot_sync(0xffffffffu, ids[lane] == id), hi = __ballot_sync(0xffffffffu, ids[lane + 32] == id);
+      const uint32_t mine = warp ? hi : lo;
+      if (mine >> lane & 1) list[(warp ? __popc(lo) : 0) + __popc(mine & ((1u << lane) - 1))] = tid;
+      if (tid == 0) count = __popc(lo) + __popc(hi);
     }
-  }
+    __syncthreads();
+    const int n = count, tiles = (n + 7) / 8;
+    const bool row1 = r0 + q + 8 < p.R;                    // rank is a multiple of 8
+    const uint16_t* a0 = p.a + (static_cast<int64_t>(id) * p.R + r0 + q) * p.K + 8 * i;
+    float acc[8][4] = {};
+    constexpr int kStride = kShrinkCluster * kShrinkWarps;
+    const int64_t s1 = steps * (split + 1) / p.splits;
+    for (int64_t s = steps * split / p.splits + rank * kShrinkWarps + warp; s < s1; s += 2 * kStride) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const bool two = s + kStride < s1;
+      uint4 wa[2], wb[2];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    if (t >= tiles) break;
+      for (int k = 0; k < 2; ++k) {
+        const uint16_t* at = a0 + 32 * (s + k * kStride);
+        wa[k] = k == 0 || two ? __ldg(reinterpret_cast<const uint4*>(at)) : zero;
+        wb[k] = row1 && (k == 0 || two) ? __ldg(reinterpret_cast<const uint4*>(at + 8 * p.K)) : zero;
+      }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[warp][q + 8 * (e >> 1)][8 * t + 2 * i + (e & 1)] = acc[t][e];
-  }
-  __syncthreads();
-  for (int e = tid; e < 16 * n; e += kShrinkWarps * 32) {
-    const int r = e / n, m = e - r * n;
-    float v = 0.f;
+      for (int t0 = 0; t0 < 8; t0 += 2) {
+        if (t0 >= tiles) break;
+        uint4 x[2][2];
 #pragma unroll
-    for (int w = 0; w < kShrinkWarps; ++w) v += part[w][r][m];
-    cta[r][m] = v;
-  }
-  cluster.sync();
-  const float sc = p.scale[id];
-  for (int e = rank * kShrinkWarps * 32 + tid; e < 16 * n; e += kShrinkCluster * kShrinkWarps * 32) {
-    const int r = e / n, m = e - r * n;
-    float v = 0.f;
+        for (int t = 0; t < 2; ++t) {
+          const int m = 8 * (t0 + t) + q;
+          const uint16_t* at = p.x + static_cast<int64_t>(list[m < n ? m : 0]) * p.K + 32 * s + 8 * i;
 #pragma unroll
-    for (int c = 0; c < kShrinkCluster; ++c) v += cluster.map_shared_rank(&cta[0][0], c)[r * kMaxTokens + m];
-    if (r0 + r < p.R) p.t[list[m] * p.R + r0 + r] = sc * v;
+          for (int k = 0; k < 2; ++k)
+            x[t][k] = m < n && (k == 0 || two) ? __ldg(reinterpret_cast<const uint4*>(at + 32 * kStride * k)) : zero;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mma_bf16(acc[t0 + t], wa[k].x, wb[k].x, wa[k].y, wb[k].y, x[t][k].x, x[t][k].y);
+            mma_bf16(acc[t0 + t], wa[k].z, wb[k].z, wa[k].w, wb[k].w, x[t][k].z, x[t][k].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (t < tiles) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[warp][q + 8 * (e >> 1)][8 * t + 2 * i + (e & 1)] = acc[t][e];
+      }
+    __syncthreads();
+    for (int e = tid; e < 16 * n; e += kShrinkWarps * 32) {
+      const int m = e >> 4, r = e & 15;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kShrinkWarps; ++w) v += part[w][r][m];
+      sum[m][r] = v;
+    }
+    cluster.sync();
+    const float sc = p.scale[id];
+    for (int e = rank * kShrinkWarps * 32 + tid; e < 16 * n; e += kStride * 32) {
+      const int m = e >> 4, r = e & 15;
+      float v = 0.f;
+#pragma unroll
+      for (int c = 0; c < kShrinkCluster; ++c) v += cluster.map_shared_rank(&sum[0][0], c)[e];
+      if (r0 + r < p.R) p.t[(split * kMaxTokens + list[m]) * p.R + r0 + r] = sc * v;
+    }
+    cluster.sync();                                        // peers keep their sums until all have read
   }
-  cluster.sync();                                        // peers keep their shared memory until all have read
 }
 
 // Y = base + B t.  A thread owns one output column n, a CTA kExpandCols
 // columns and kExpandTokens tokens taken in the order of their adapters, so
-// that a thread reloads its row of B only when the adapter changes.
+// that a thread reloads its row of B only when the adapter changes.  Few registers and
+// many CTAs keep the loads in flight (all loads of four tokens held at once: 12.6 us
+// instead of 9.2 for 64 adapters of rank 16 at 12288 rows, fewer CTAs fit).
 constexpr int kExpandCols = 128, kExpandTokens = 4;
 
 template <int R, typename Out>
 __global__ void __launch_bounds__(kExpandCols) lora_expand_kernel(const LoraArgs p) {
-  __shared__ int ids[kMaxTokens], order[kMaxTokens];
   __shared__ __align__(16) float t[kExpandTokens][R];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tid < kMaxTokens) ids[tid] = adapter_of(p, tid);
-  __syncthreads();
-  if (tid < p.M) {
-    int at = 0;
-    for (int m = 0; m < p.M; ++m) at += ids[m] < ids[tid] || (ids[m] == ids[tid] && m < tid);
-    order[at] = tid;
-  }
-  __syncthreads();
   const int m0 = blockIdx.y * kExpandTokens;
   const int tokens = p.M - m0 < kExpandTokens ? p.M - m0 : kExpandTokens;
-  for (int e = tid; e < tokens * R; e += kExpandCols) {
-    const int j = e / R, m = order[m0 + j];
-    t[j][e - j * R] = ids[m] >= 0 ? p.t[m * R + (e - j * R)] : 0.f;
-  }
+  int2 token[kExpandTokens];                              // (token, adapter)
+#pragma unroll
+  for (int j = 0; j < kExpandTokens; ++j) token[j] = p.sorted[m0 + (j < tokens ? j : 0)];
+#pragma unroll
+  for (int j = 0; j < kExpandTokens; ++j)
+    for (int r = tid; r < R; r += kExpandCols) {
+      float v = 0.f;
+      if (token[j].y >= 0)
+        for (int c = 0; c < p.splits; ++c) v += p.t[(c * kMaxTokens + token[j].x) * R + r];
+      t[j][r] = v;
+    }
   __syncthreads();
   const int64_t n = static_cast<int64_t>(blockIdx.x) * kExpandCols + tid;
   if (n >= p.N) return;
@@ -162,7 +210,7 @@ __global__ void __launch_bounds__(kExpandCols) lora_expand_kernel(const LoraArgs
 #pragma unroll
   for (int j = 0; j < kExpandTokens; ++j) {
     if (j >= tokens) break;
-    const int m = order[m0 + j], id = ids[m];
+    const int m = token[j].x, id = token[j].y;
     float y = p.base[m * p.N + n];
     if (id >= 0) {
       if (id != held) {
@@ -218,6 +266,7 @@ LoraArgs lora_args(const LoraCall& c) {
   p.scale = c.scale;
   p.ids = c.ids;
   p.t = c.t;
+  p.sorted = reinterpret_cast<int2*>(c.t + static_cast<int64_t>(lora_splits(c.K)) * kMaxTokens * c.R);
   p.base = c.base;
   p.y = c.y;
   p.err = c.err;
@@ -226,15 +275,20 @@ LoraArgs lora_args(const LoraCall& c) {
   p.M = c.M;
   p.R = c.R;
   p.count = c.count;
+  p.splits = lora_splits(c.K);
   return p;
 }
 
 }  // namespace
 
-cudaError_t launch_lora_shrink(const LoraCall& c, cudaStream_t s) {
+int lora_splits(int64_t K) { return static_cast<int>(std::clamp<int64_t>(K / kSplitCols, 1, kMaxSplits)); }
+
+cudaError_t launch_lora_shrink(const LoraCall& c, const DeviceInfo& info, cudaStream_t s) {
   const LoraArgs p = lora_args(c);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kShrinkCluster, static_cast<unsigned>((p.R + 15) / 16), static_cast<unsigned>(p.M));
+  // as many clusters as there can be items and as the GPU holds
+  const int clusters = std::min(p.M * ((p.R + 15) / 16) * p.splits, std::max(1, kShrinkPerSm * info.sms / kShrinkCluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kShrinkCluster));
   cfg.blockDim = dim3(kShrinkWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -64,6 +64,8 @@ KvBatch batch_of(const q4nx_kv_batch* b) {
 constexpr int kMaxHeads = 1024;
 constexpr int64_t kMaxStride = int64_t(1) << 40;      // elements between rows: products of it stay in 64 bits
 
+// 32-bit words of the adapters' inner products and of the tokens in their order
+uint64_t lora_t(int64_t cols) { return static_cast<uint64_t>(lora_splits(cols)) * 64 * 128 + 128; }
 bool known_rank(int r) { return r == 8 || r == 16 || r == 32 || r == 64 || r == 128; }
 
 }  // namespace
@@ -132,7 +134,7 @@ int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, co
 
 uint64_t q4nx_gemm_lora_scratch(const q4nx_weight* w, int M) {
   if (w == nullptr || check_grid(w->rows, w->cols) != Q4NX_OK || M < 1 || M > 64) return 0;
-  return 64 * 128 * 4 + static_cast<uint64_t>(M) * static_cast<uint64_t>(w->rows) * 4;
+  return lora_t(w->cols) * 4 + static_cast<uint64_t>(M) * static_cast<uint64_t>(w->rows) * 4;
 }
 
 int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_adapters* ad, const int32_t* ids_dev,
@@ -164,7 +166,7 @@ int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_ad
   c.scale = ad->scale_dev;
   c.ids = ids_dev;
   c.t = static_cast<float*>(scratch_dev);
-  float* base = f32 ? static_cast<float*>(Y_dev) : c.t + 64 * 128;
+  float* base = f32 ? static_cast<float*>(Y_dev) : c.t + lora_t(w->cols);
   c.base = base;
   c.y = Y_dev;
   c.err = static_cast<uint32_t*>(workspace_dev);
@@ -173,7 +175,8 @@ int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_ad
   c.M = M;
   c.R = ad->rank;
   c.count = ad->count;
-  if (launch_lora_shrink(c, s) != cudaSuccess) return Q4NX_E_CUDA;
+  DeviceInfo info;
+  if (device_info(&info) != cudaSuccess || launch_lora_shrink(c, info, s) != cudaSuccess) return Q4NX_E_CUDA;
   if ((st = q4nx_gemm_m64(w, X_dev, M, base, Q4NX_OUT_F32, workspace_dev, workspace_bytes, stream))) return st;
   return from_cuda(launch_lora_expand(c, f32, s));
 }
