@@ -12,8 +12,9 @@
 // warp's 32 thread maxima, j = ceil(top / warps), is reached by at least j
 // elements of that warp, so the smallest such value over the warps is a floor
 // for the CTA's top elements.  Only threads whose own maximum reaches the
-// floor read their elements again (from L2; a few per cent of them), and the
-// elements at or above it, about a hundred, get their ranks by counting.  Rows with
+// floor have their elements read again (from L2, by their whole warp; one thread in
+// ten), and the elements at or above it, about a hundred, get their ranks by
+// counting.  Rows with
 // more than kCand such elements (many equal ones) take `top` rounds of
 // "largest below the previous" instead.
 #include <cooperative_groups.h>
@@ -63,11 +64,18 @@ __device__ __forceinline__ void move_to(Stat& s, float m) {
   s.z *= f;
   s.m = m;
 }
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
-  move_to(a, m);
-  move_to(b, m);
-  return {m, a.z + b.z, a.w + b.w};
+// A warp's statistics joined: moved to the largest maximum, then added.
+__device__ __forceinline__ Stat join_warp(Stat s) {
+  float m = s.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  move_to(s, m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+    s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+  }
+  return s;
 }
 __device__ __forceinline__ void add(Stat& s, float x, float shift) {
   const float d = x - shift;
@@ -114,6 +122,7 @@ struct Row {
 template <bool BF16, typename F>
 __device__ __forceinline__ void for_elements(const Row<BF16>& row, int64_t v0, int64_t v1, int64_t end_elem, F f) {
   constexpr int VE = Row<BF16>::VE;
+#pragma unroll 1
   for (int64_t v = v0 + threadIdx.x; v < v1; v += kThreads) {
     const uint4 u = row.load(v);
 #pragma unroll
@@ -131,7 +140,6 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
   __shared__ uint64_t best[kMaxTop];                   // this CTA's, largest first
   __shared__ uint64_t all[kMaxTop * kMaxCluster];
   __shared__ uint64_t reduce[kWarps];
-  __shared__ Stat cta;
   __shared__ int found;
   __shared__ float final_lse;
   cg::cluster_group cluster = cg::this_cluster();
@@ -181,15 +189,14 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
   // all); a NaN total means a NaN or +inf among them: look again at which
   uint32_t mine = any ? ord_of(big) : 0u;
   if (a.top > 0 && s.z != s.z) for_elements<BF16>(row, v0, v1, end_elem, [&](float x, int64_t) { mine = max(mine, ord_of(x)); });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat t;
-    t.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-    t.z = __shfl_xor_sync(0xffffffffu, s.z, o);
-    t.w = __shfl_xor_sync(0xffffffffu, s.w, o);
-    s = lane & o ? join(t, s) : join(s, t);            // the same order on both sides
-  }
+  s = join_warp(s);
   if (lane == 0) stats[warp] = s;
+  // the token's logit, ahead of its use
+  float given = __int_as_float(0x7fc00000);              // no such token
+  if (rank == 0 && tid == 0 && a.logprob != nullptr) {
+    const int64_t tok = a.tokens[m];
+    if (tok >= 0 && tok < a.V) given = row.at(tok);
+  }
   if (a.top > 0) {
     uint32_t left = mine, kth = 0;
     for (int j = 0; j < (a.top + kWarps - 1) / kWarps; ++j) {
@@ -200,33 +207,53 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
     if (lane == 0) floor_of[warp] = kth;
   }
   if (tid == 0) found = 0;
+  if (tid < kMaxTop) best[tid] = 0;
   __syncthreads();
-  if (warp == 0) {
-    Stat t = lane < kWarps ? stats[lane] : Stat{neg_inf(), 0.f, 0.f};
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) {
-      Stat r;
-      r.m = __shfl_down_sync(0xffffffffu, t.m, o);
-      r.z = __shfl_down_sync(0xffffffffu, t.z, o);
-      r.w = __shfl_down_sync(0xffffffffu, t.w, o);
-      t = join(t, r);
-    }
-    if (lane == 0) cta = t;
-  }
   if (a.top > 0) {
     uint32_t floor = 0xFFFFFFFFu;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) floor = min(floor, floor_of[w]);
-    if (mine >= floor && any) {
-      for_elements<BF16>(row, v0, v1, end_elem, [&](float x, int64_t i) {
-        const uint64_t key = argmax_key(x, static_cast<uint32_t>(i));
-        if (static_cast<uint32_t>(key >> 32) >= floor) {
-          const int at = atomicAdd(&found, 1);
-          if (at < kCand) cand[at] = key;
+    // A warp goes through its lanes that reach the floor, kSources at a time: the
+    // 32 lanes load one's elements together.
+    constexpr int kSources = 4;
+    const float least = value_of(static_cast<uint64_t>(floor) << 32);
+    auto offer = [&](float x, int64_t i) {
+      if (x < least) return;                           // not a NaN
+      const uint64_t key = argmax_key(x, static_cast<uint32_t>(i));
+      if (static_cast<uint32_t>(key >> 32) < floor) return;
+      const int at = atomicAdd(&found, 1);
+      if (at < kCand) cand[at] = key;
+    };
+    uint32_t reach = __ballot_sync(0xffffffffu, any && mine >= floor);
+    if (any && mine >= floor && end_elem >= 0) offer(row.at(end_elem), end_elem);
+#pragma unroll 1
+    while (reach != 0) {
+      uint32_t some = reach;
+#pragma unroll
+      for (int k = 0; k < kSources; ++k) reach &= reach - 1;
+      some &= ~reach;
+#pragma unroll 1
+      for (int64_t l = lane; v0 + warp * 32 + (l - lane) * kThreads < v1; l += 32) {
+        uint4 u[kSources];
+        uint32_t rest = some;
+#pragma unroll
+        for (int k = 0; k < kSources; ++k) {
+          const int64_t v = v0 + warp * 32 + __ffs(rest) - 1 + l * kThreads;
+          if (rest != 0 && v < v1) u[k] = row.load(v);
+          rest &= rest - 1;
         }
-      });
+        rest = some;
+#pragma unroll
+        for (int k = 0; k < kSources; ++k) {
+          const int64_t v = v0 + warp * 32 + __ffs(rest) - 1 + l * kThreads;
+          if (rest != 0 && v < v1) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) offer(Row<BF16>::pick(u[k], e), row.head + v * VE + e);
+          }
+          rest &= rest - 1;
+        }
+      }
     }
-    if (tid < kMaxTop) best[tid] = 0;
     __syncthreads();
     const int n = found;
     if (n <= kCand) {
@@ -258,38 +285,47 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
   }
   cluster.sync();
   if (rank == 0) {
-    if (tid == 0) {
-      Stat t = cta;
-      for (int c = 1; c < C; ++c) t = join(t, *cluster.map_shared_rank(&cta, c));
-      const bool none = t.z == 0.f;                    // every logit is -inf
-      const float log_z = none ? neg_inf() : logf(t.z);
-      const float lse = t.m + log_z;
-      final_lse = lse;
-      if (a.lse != nullptr) a.lse[m] = lse;
-      if (a.entropy != nullptr) a.entropy[m] = none ? 0.f : log_z - t.w / t.z;
-      if (a.logprob != nullptr) {
-        const int64_t tok = a.tokens[m];
-        float lp = __int_as_float(0x7fc00000);         // no such token
-        if (tok >= 0 && tok < a.V) lp = none ? neg_inf() : row.at(tok) - lse;
-        a.logprob[m] = lp;
+    if (warp == 0) {
+      constexpr int kEach = kWarps * kMaxCluster / 32;
+      Stat t[kEach], all_t = {neg_inf(), 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int c = lane + 32 * k;
+        t[k] = c < kWarps * C ? cluster.map_shared_rank(&stats[0], c / kWarps)[c % kWarps] : Stat{neg_inf(), 0.f, 0.f};
+        all_t.m = fmaxf(all_t.m, t[k].m);
       }
-    }
-    if (a.top > 0) {
-      for (int e = tid; e < a.top * C; e += kThreads) {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        move_to(t[k], all_t.m);
+        all_t.z += t[k].z;
+        all_t.w += t[k].w;
+      }
+      all_t = join_warp(all_t);
+      if (lane == 0) {
+        const bool none = all_t.z == 0.f;                // every logit is -inf
+        const float log_z = none ? neg_inf() : logf(all_t.z);
+        const float lse = all_t.m + log_z;
+        final_lse = lse;
+        if (a.lse != nullptr) a.lse[m] = lse;
+        if (a.entropy != nullptr) a.entropy[m] = none ? 0.f : log_z - all_t.w / all_t.z;
+        if (a.logprob != nullptr) a.logprob[m] = none && given == given ? neg_inf() : given - lse;
+      }
+    } else {
+      for (int e = tid - 32; e < a.top * C; e += kThreads - 32) {
         const int c = e / a.top;
         all[e] = cluster.map_shared_rank(&best[0], c)[e - c * a.top];
       }
-      __syncthreads();
-      const int n = a.top * C;
-      if (tid < n) {
-        const uint64_t key = all[tid];
-        int above = 0;
-        for (int o = 0; o < n; ++o) above += all[o] > key;
-        if (key != 0 && above < a.top) {
-          const float lse = final_lse;
-          a.top_idx[m * a.top + above] = argmax_index(key);
-          a.top_lp[m * a.top + above] = lse == neg_inf() ? neg_inf() : value_of(key) - lse;
-        }
+    }
+    __syncthreads();
+    const int n = a.top * C;
+    if (tid < n) {
+      const uint64_t key = all[tid];
+      int above = 0;
+      for (int o = 0; o < n; ++o) above += all[o] > key;
+      if (key != 0 && above < a.top) {
+        const float lse = final_lse;
+        a.top_idx[m * a.top + above] = argmax_index(key);
+        a.top_lp[m * a.top + above] = lse == neg_inf() ? neg_inf() : value_of(key) - lse;
       }
     }
   }
