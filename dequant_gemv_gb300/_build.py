@@ -1,16 +1,21 @@
 """In-tree build of libq4nx.so for sm_103a (nvcc, one -gencode, parallel TUs).
 
 ``python dequant_gemv_gb300/_build.py`` or ``build()`` compiles every
-``csrc/*.cu`` into ``_objs/`` and links ``libq4nx.so`` next to this file.
+``csrc/*.cu`` into ``_objs/`` and links ``libq4nx.so`` next to this file, and
+the native binding of the decode-step operators (``csrc/serving_binding.cpp``,
+g++ against the installed torch's headers) into ``_serving.so``.
 Objects are rebuilt only when a source or header is newer.  No cmake.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +23,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJS = os.path.join(PKG, "_objs")
 LIB = os.path.join(PKG, "libq4nx.so")
+BINDING = os.path.join(PKG, "_serving.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing"]
 
@@ -41,6 +47,22 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_jobs(nvcc: str) -> tuple[list[str], list[str]]:
+    """Commands that compile and link the native binding against the installed torch."""
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+           "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+    gxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    # the object's name holds torch's version: another torch is another build
+    obj = os.path.join(OBJS, f"serving_binding-torch{importlib.metadata.version('torch')}.o")
+    compile_ = [gxx, "-O2", "-std=c++17", "-fPIC", "-fno-strict-aliasing", *[f"-I{d}" for d in inc], "-c",
+                os.path.join(CSRC, "serving_binding.cpp"), "-o", obj]
+    link = [gxx, "-shared", obj, f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda",
+            "-lc10", f"-L{PKG}", "-lq4nx", "-Wl,-rpath,$ORIGIN", "-o"]
+    return compile_, link
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(OBJS, exist_ok=True)
@@ -55,6 +77,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append((src, cmd))
 
+    binding, link = _binding_jobs(nvcc)
+    if _stale(binding[-1], [binding[-3], os.path.join(ROOT, "include", "q4nx.h")]):
+        jobs.append((binding[-3], binding))
+
     def run(job):
         src, cmd = job
         p = subprocess.run(cmd, capture_output=True, text=True)
@@ -68,7 +94,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             if verbose or ptxas_info or rc != 0:
                 sys.stderr.write(f"== {os.path.basename(s)} (rc={rc})\n{out}")
         if failed:
-            raise RuntimeError("nvcc failed on: " + ", ".join(os.path.basename(s) for s, _ in failed))
+            raise RuntimeError("compilation failed on: " + ", ".join(os.path.basename(s) for s, _ in failed))
     objs = [os.path.join(OBJS, os.path.basename(s)[:-3] + ".o") for s in sources]
     if _stale(LIB, objs) or jobs:
         tmp = LIB + f".tmp{os.getpid()}"
@@ -77,6 +103,12 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         if p.returncode != 0:
             raise RuntimeError("link of libq4nx.so failed:\n" + p.stdout + p.stderr)
         os.replace(tmp, LIB)
+    if _stale(BINDING, [binding[-1]]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        p = subprocess.run([*link, tmp], capture_output=True, text=True)
+        if p.returncode != 0:
+            raise RuntimeError("link of _serving.so failed:\n" + p.stdout + p.stderr)
+        os.replace(tmp, BINDING)
     return LIB
 
 
