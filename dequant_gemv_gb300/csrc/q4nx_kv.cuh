@@ -59,17 +59,19 @@ struct KvRequest {
   bool ok;
 };
 
-// Request b with its numbers checked: a length below 0 or beyond the table, or
+// A request with its numbers checked: a length below 0 or beyond the table, or
 // token ranges that do not lie in 0..tokens in order, make it empty (ok false).
-__device__ __forceinline__ KvRequest kv_request(const KvBatch& kb, int page_blocks, int b) {
+__device__ __forceinline__ KvRequest kv_checked(const KvBatch& kb, int page_blocks, int64_t q0, int64_t q1, int64_t L) {
   KvRequest r;
-  const int64_t q0 = kb.q_start[b], q1 = kb.q_start[b + 1], L = kb.lens[b];
   const int64_t cap = static_cast<int64_t>(kb.table_cols) * page_blocks * kKvBlock;
   r.ok = q0 >= 0 && q1 >= q0 && q1 <= kb.tokens && L >= 0 && L <= cap;
   r.q0 = r.ok ? q0 : 0;
   r.T = r.ok ? q1 - q0 : 0;
   r.L = r.ok ? L : 0;
   return r;
+}
+__device__ __forceinline__ KvRequest kv_request(const KvBatch& kb, int page_blocks, int b) {
+  return kv_checked(kb, page_blocks, kb.q_start[b], kb.q_start[b + 1], kb.lens[b]);
 }
 
 // Block `blk` (16 positions) of request b and kv head h, or NULL where the
@@ -91,16 +93,24 @@ __device__ __forceinline__ int kv_v_byte(int D, int t, int mt, int r) {  // byte
   return 8 * D + ((mt >> 2) * 32 + lane) * 16 + (mt & 3) * 4 + (t >> 3) + 2 * (t & 1);
 }
 
-// The request that holds token `tok` of the call (binary search over q_start),
-// or -1 where the ranges are not in order.
-__device__ __forceinline__ int kv_find_request(const KvBatch& kb, int64_t tok) {
-  int lo = 0, hi = kb.batch;                       // q_start[lo] <= tok < q_start[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (kb.q_start[mid] <= tok) lo = mid;
-    else hi = mid;
+// The request that holds token `tok` of the call (b), or -1 where there is none;
+// by a whole warp, in one round trip to memory for 32 requests (a binary
+// search takes one for each of its steps).
+__device__ __forceinline__ KvRequest kv_locate(const KvBatch& kb, int page_blocks, int64_t tok, int& b) {
+  const int lane = threadIdx.x & 31;
+  b = -1;
+  for (int j0 = 0; j0 < kb.batch; j0 += 32) {
+    const int j = j0 + lane;
+    int32_t q0 = 0, q1 = 0, L = 0;
+    if (j < kb.batch) q0 = kb.q_start[j], q1 = kb.q_start[j + 1], L = kb.lens[j];
+    const uint32_t here = __ballot_sync(0xffffffffu, q0 <= tok && tok < q1);
+    if (here == 0) continue;
+    const int src = __ffs(here) - 1;
+    b = j0 + src;
+    return kv_checked(kb, page_blocks, __shfl_sync(0xffffffffu, q0, src), __shfl_sync(0xffffffffu, q1, src),
+                      __shfl_sync(0xffffffffu, L, src));
   }
-  return (kb.q_start[lo] <= tok && tok < kb.q_start[lo + 1]) ? lo : -1;
+  return KvRequest{0, 0, 0, false};
 }
 
 }  // namespace q4nx
