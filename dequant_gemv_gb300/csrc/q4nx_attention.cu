@@ -9,11 +9,11 @@
 // AND makes two), queries as fp16 scaled by a power of two per row (bf16 has
 // 8 significant bits, so nothing is lost above 2^-39 of the row's largest), and
 // the scales meet the products in binary32:
-//   q.k   = sum_g sk_g * (q_g.ck_g - 8*Q_g) + mk_g * Q_g,  Q_g = sum of q over g
+//   q.k   = sum_g sk_g * (q_g.ck_g) + sk_g * (-8*Q_g) + mk_g * Q_g,  Q_g = sum of q over g
 //   out_g = sum_j (p sv_g) (cv - 8) + sum_j p mv_g
-// -8*Q_g is the matrix product's initial accumulator; mk_g*Q_g is a matrix
-// product with Q_g as three bf16 parts (24 bits), sum_j p mv_g one with p as
-// two (16 bits).  The values' codes are centred before their product (fp16
+// The two terms with Q_g are matrix products with it as three bf16 parts (24
+// bits; as the products' initial accumulator -8*Q_g cost four moves each),
+// sum_j p mv_g is one with p as two (16 bits).  The values' codes are centred before their product (fp16
 // 1024 + c, less 1032): sums over thousands of tokens stay near their result.
 // p*sv is rounded to fp16 (2^-11 of itself; a power of two per row, which
 // follows the largest p*sv seen, keeps it in range); bf16 values would cost
@@ -38,7 +38,7 @@
 // between CTAs by the CTA that posts last, in the order of the CTAs, so that the
 // result does not depend on timing.  (With all warps of a CTA on one unit at
 // a time every unit cost the CTA 4 us of waiting and joining: 71 us instead
-// of XX for 48 requests of 600 to 6000 tokens, 8 kv heads.)
+// of 58 for 48 requests of 600 to 6000 tokens, 8 kv heads.)
 #include "q4nx_kernels.h"
 #include "q4nx_kv.cuh"
 
@@ -259,8 +259,8 @@ template <int D, int NT>
 struct State {
   static constexpr int NG = D / 32;
   uint32_t qb[NT][NG][4];        // q as B operands: [group][k-step of 16: b0 b1], times 2^(14 - e) of its row
-  float2 q8[NT][NG];             // -8 * Q_g, in the products' unit: 2^(-10 - e)
-  uint32_t qs[NT][(NG + 3) / 4][2];   // Q_g of row lane/4 in three bf16 parts, g = 4*half + i
+  // Q_g and -8 * Q_g of row lane/4 in three bf16 parts, g = 4*half + i, in the products' unit 2^(-10 - e)
+  uint32_t qs[2][NT][(NG + 3) / 4][2];
   float2 cr[NT];                 // softmax scale * log2(e) * 2^(10 + e)
   float o[NT][D / 16][4];        // [channels 16mt + lane/4 (+8, times 16)][rows 2i, 2i+1], times fs
   float corr[NT][4];             // sum of p*mid, group lane/4, rows 2i, 2i+1 (then two unused)
@@ -311,7 +311,6 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, const Piece<8 * NT>& u
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       s *= 0x1p-24f;
       sum[g] = s;
-      st.q8[t][g] = make_float2(-8.f * __shfl_sync(0xffffffffu, s, 8 * i), -8.f * __shfl_sync(0xffffffffu, s, 8 * i + 4));
     }
 #pragma unroll
     for (int hf = 0; hf < (NG + 3) / 4; ++hf) {
@@ -321,8 +320,10 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, const Piece<8 * NT>& u
         if (g == 4 * hf + i) s = sum[g];
       const float hi = __bfloat162float(__float2bfloat16_rn(s));
       const float mid = __bfloat162float(__float2bfloat16_rn(s - hi));
-      st.qs[t][hf][0] = pack_bf16x2(hi, mid);
-      st.qs[t][hf][1] = pack_bf16x2((s - hi) - mid, 0.f);
+      st.qs[0][t][hf][0] = pack_bf16x2(hi, mid);
+      st.qs[0][t][hf][1] = pack_bf16x2((s - hi) - mid, 0.f);
+      st.qs[1][t][hf][0] = pack_bf16x2(-8.f * hi, -8.f * mid);
+      st.qs[1][t][hf][1] = pack_bf16x2(-8.f * ((s - hi) - mid), 0.f);
     }
   }
 }
@@ -387,16 +388,19 @@ __device__ __forceinline__ void block_step(State<D, NT>& st, uint32_t blk0, bool
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const uint32_t blk = blk0 + n * BB;
-    // mid * Q
+    // mid * Q - 8 * scale * Q
 #pragma unroll
     for (int hf = 0; hf < NH; ++hf) {
       const int g = NG < 4 ? (i & (NG - 1)) : 4 * hf + i;
-      const uint32_t z0 = lds_u16(blk + 17 * D + (tk * NG + g) * 2) * 0x10001u;
-      const uint32_t z1 = lds_u16(blk + 17 * D + ((tk + 8) * NG + g) * 2) * 0x10001u;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (hf == 0) mma<false>(s[n][t], z0, z1, z0, z1, st.qs[t][hf][0], st.qs[t][hf][1], 0.f, 0.f, 0.f, 0.f);
-        else mma_add<false>(s[n][t], z0, z1, z0, z1, st.qs[t][hf][0], st.qs[t][hf][1]);
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t z0 = lds_u16(blk + (17 - k) * D + (tk * NG + g) * 2) * 0x10001u;
+        const uint32_t z1 = lds_u16(blk + (17 - k) * D + ((tk + 8) * NG + g) * 2) * 0x10001u;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (hf == 0 && k == 0) mma<false>(s[n][t], z0, z1, z0, z1, st.qs[k][t][hf][0], st.qs[k][t][hf][1], 0.f, 0.f, 0.f, 0.f);
+          else mma_add<false>(s[n][t], z0, z1, z0, z1, st.qs[k][t][hf][0], st.qs[k][t][hf][1]);
+        }
       }
     }
 #pragma unroll
@@ -417,8 +421,7 @@ __device__ __forceinline__ void block_step(State<D, NT>& st, uint32_t blk0, bool
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float acc[4];
-          mma<true>(acc, x0 & kLo, x1 & kLo, x0 & kHi, x1 & kHi, st.qb[t][g][0], st.qb[t][g][1], st.q8[t][g].x, st.q8[t][g].y,
-                    st.q8[t][g].x, st.q8[t][g].y);
+          mma<true>(acc, x0 & kLo, x1 & kLo, x0 & kHi, x1 & kHi, st.qb[t][g][0], st.qb[t][g][1], 0.f, 0.f, 0.f, 0.f);
           mma_add<true>(acc, y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi, st.qb[t][g][2], st.qb[t][g][3]);
           const float2 a = ffma2(both(k0), make_float2(acc[0], acc[1]), make_float2(s[n][t][0], s[n][t][1]));
           const float2 b = ffma2(both(k1), make_float2(acc[2], acc[3]), make_float2(s[n][t][2], s[n][t][3]));
