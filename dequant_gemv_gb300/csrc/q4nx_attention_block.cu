@@ -1,0 +1,689 @@
+// q4nx_attention_block.cu -- attention of many query rows (prompt blocks) over
+// the 4-bit cache, on the tcgen05 tensor cores.
+//
+//   S = q k^T (128 rows x 64 tokens),  p = exp2(S * scale * log2 e - ref),
+//   O += p v,  l += sum p;  out = O / l
+// with one running reference per row, moved only when a logit passes it by 2^8.
+//
+// Where the kernel for few rows keeps the codes exact and applies the groups'
+// scales to the sums, here a key or value x = (code - 8) * scale + mid enters as
+// two bf16 numbers, x = hi + lo within 2^-17 of itself (one alone, 2^-9, would
+// move the row's log-sum by more than binary32 does), and so does p:
+//   S = q k_hi + q k_lo          (q is bf16)
+//   O = p_hi v_hi + p_lo v_hi + p_hi v_lo
+// 28 tcgen05.mma (M = 128, K = 16) per 64 tokens at 128 channels, accumulated in
+// binary32 in TMEM.
+//
+// Sixteen warps, one CTA per SM: a loader (bulk copies of the cache's blocks), the
+// MMA issuer, four softmax warps (a thread is a row: its logits come from TMEM, its
+// p go back there as the A operand of the second product) and eight decoding
+// warps (codes to bf16 pairs in shared memory, 128-byte swizzle: keys as rows of
+// channels, values as rows of tokens).  S, p, keys and values have two buffers:
+// the tensor cores form S of a step while the softmax warps work on the one before.
+//
+// Bound: instruction issue of the decoding and softmax warps (about 5500 per
+// 64 tokens x 128 rows, 2200 cycles against 1350 of the products).
+//
+// A CTA's steps (64 tokens) are a range of all units' steps; a unit cut between
+// CTAs leaves its parts in the workspace, with a record of whose they are, for
+// a second kernel that joins them over the whole GPU (a part is 64 KB).
+#include <cuda_fp16.h>
+
+#include "q4nx_attention.cuh"
+
+namespace q4nx {
+
+namespace {
+
+constexpr int kRows = 128, kSB = 4, kTok = kSB * kKvBlock;      // rows of a unit, blocks and tokens of a step
+constexpr int kThreads = 512, kDecodeWarps = 8, kRawStages = 4;
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpSoft0 = 4, kWarpDecode0 = 8;
+constexpr uint32_t kTmemCols = 512;
+
+template <int D>
+struct Layout {
+  static constexpr int NBX = D / 64;
+  static constexpr int kKeys = 2 * NBX * 8192;                  // hi boxes (64 tokens x 64 channels), then lo
+  static constexpr int kValues = 2 * D * 128;                   // hi rows (D x 64 tokens), then lo
+  static constexpr int kRaw = kSB * kv_block_bytes(D);
+  static constexpr int kValuesAt = 2 * kKeys, kRawAt = kValuesAt + 2 * kValues, kControlAt = kRawAt + kRawStages * kRaw;
+  // TMEM columns
+  static constexpr uint32_t kQ = 0, kS = D / 2, kP = kS + 2 * kTok, kO = kP + 2 * kTok;
+  static_assert(kO + D <= kTmemCols, "TMEM budget");
+  static_assert(kControlAt % 128 == 0 && kValuesAt % 1024 == 0, "swizzled regions");
+};
+
+struct Control {
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t q_ready, drain;
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag;
+  volatile uint32_t odd_any[2];
+  uint32_t odd[2][8][2];                            // tokens kept as NaN: [stage][group][64 tokens]
+  int64_t begin, end;
+  int64_t prefix[kKvMaxBatch + 1], cost[kKvMaxBatch + 1];
+};
+template <int D>
+constexpr int kSmemBytes = Layout<D>::kControlAt + sizeof(Control) + 1024;
+
+// ---- PTX ----
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// K-major operand, 128-byte swizzle: rows of 128 B, 8-row groups 1024 B apart
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | static_cast<uint64_t>(1) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+         static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+// D fp32, A (TMEM) and B (shared memory) bf16, both K-major, M = 128, N = n
+__host__ __device__ constexpr uint32_t idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((kRows >> 4) << 24);
+}
+// one product of K = 16, by one thread
+__device__ __forceinline__ void mma16(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+// completes the loads before it: their registers pass through, so that no use is moved ahead of the wait
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
+
+// Bounded wait that also ends when another warp has given up; for a whole warp.
+__device__ __forceinline__ bool wait(Control& c, uint64_t* bar, uint32_t parity, uint32_t* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(ok = mbar_try_wait_sleep(bar, parity, 1000000u))) {
+      if (c.abort_flag) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        c.abort_flag = 1;
+        atomicOr(err, kErrTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The positions that some row of a unit sees, [first, last], and those of its rows.
+struct Span {
+  int64_t first, last;
+  int rows;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Unit& u) {
+  Span s;
+  const int64_t base = u.rq.L - u.rq.T, row0 = u.rg * kRows, left = u.rq.T * a.group - row0;
+  s.rows = static_cast<int>(left < kRows ? left : kRows);
+  const int64_t p0 = base + quot(row0, a.group), p1 = base + quot(row0 + s.rows - 1, a.group);
+  s.first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+  s.last = p1 < u.rq.L ? p1 : u.rq.L - 1;
+  return s;
+}
+
+// A CTA's range, piece by piece (a piece: its part of one unit), the same for
+// every warp: steps that no row sees are left out by all of them.
+struct Walk {
+  Unit u;
+  Span s;
+  int n, end;               // the CTA's next step, the end of the piece
+  int64_t step;             // the request's step of n
+};
+__device__ __forceinline__ void next_piece(const AttnArgs& a, const Plan& pl, const Control& c, Walk& w, int steps) {
+  w.u = find_unit<kSB, kRows>(a, pl, c.begin + w.n);
+  w.s = span_of(a, w.u);
+  const int64_t end = w.u.start + w.u.n - c.begin;
+  w.end = static_cast<int>(end < steps ? end : steps);
+  w.step = w.u.first + (c.begin + w.n - w.u.start);
+}
+__device__ __forceinline__ bool needed(const Walk& w) { return w.step * kTok <= w.s.last && (w.step + 1) * kTok > w.s.first; }
+
+// x, y as bf16 pairs hi + lo
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - bf_lo(hi), y - bf_hi(hi));
+}
+// the four pairs of centred codes of a word; the second and fourth times 16
+__device__ __forceinline__ void centred(uint32_t w, float2 (&c)[4]) {
+  const uint32_t y = w >> 8;
+  const uint32_t h[4] = {hadd2(lop3_and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u), hadd2(lop3_and_or(w, 0x00F000F0u, 0x64006400u), 0xE480E480u),
+                         hadd2(lop3_and_or(y, 0x000F000Fu, 0x64006400u), 0xE408E408u), hadd2(lop3_and_or(y, 0x00F000F0u, 0x64006400u), 0xE480E480u)};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+}
+
+// Keys of 8 tokens (block b, half h) of a step: token row 16b + 8h + lane/4,
+// channels 32g + 8i .. of every group, into the hi and lo boxes.
+template <int D>
+__device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, int h, int64_t tok0, const Span& span) {
+  constexpr int NG = D / 32, NBX = D / 64;
+  const int lane = threadIdx.x & 31, i = lane & 3, t = 8 * h + (lane >> 2), row = 16 * b + t;
+  const uint32_t blk = raw + b * kv_block_bytes(D);
+  uint32_t w[NG], sc[NG / 2], md[NG / 2];
+  lds_words<NG>(w, blk + (t * 4 + i) * (4 * NG));
+  lds_words<NG / 2>(sc, blk + 16 * D + t * (2 * NG));
+  lds_words<NG / 2>(md, blk + 17 * D + t * (2 * NG));
+  const bool seen = tok0 + row >= span.first && tok0 + row <= span.last;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    float s = g & 1 ? bf_hi(sc[g >> 1]) : bf_lo(sc[g >> 1]), m = g & 1 ? bf_hi(md[g >> 1]) : bf_lo(md[g >> 1]);
+    if (!seen) s = m = 0.f;                                     // it may hold anything
+    float2 c[4];
+    centred(w[g], c);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = j & 1 ? 0.0625f * s : s;
+      split(fmaf(c[j].x, f, m), fmaf(c[j].y, f, m), hi[j], lo[j]);
+    }
+    const uint32_t at = keys + (g >> 1) * 8192 + row * 128 + (((4 * (g & 1) + i) ^ (row & 7)) << 4);
+    sts128(at, hi);
+    sts128(at + NBX * 8192, lo);
+  }
+}
+
+// Values of a block's 64 channels 64*quad .. : words of channels d = 16mt +
+// lane/4 and d + 8, tokens 2i, 2i+1, 2i+8, 2i+9, into the hi and lo rows d.
+template <int D>
+__device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t raw, uint32_t values, int b, int quad, int64_t tok0,
+                                              const Span& span) {
+  constexpr int NG = D / 32;
+  const int lane = threadIdx.x & 31, i = lane & 3, q = lane >> 2;
+  const uint32_t blk = raw + b * kv_block_bytes(D);
+  uint32_t w[4];
+  lds_words<4>(w, blk + 8 * D + (quad * 32 + lane) * 16);
+#pragma unroll
+  for (int gg = 0; gg < 2; ++gg) {
+    const int g = 2 * quad + gg;
+    float s[4], m[4];                                           // tokens 2i, 2i+1, 2i+8, 2i+9
+    uint32_t md[2][1];
+    lds_words<1>(md[0], blk + 19 * D + g * 32 + 4 * i);
+    lds_words<1>(md[1], blk + 19 * D + g * 32 + 4 * i + 16);
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = 2 * i + (k & 1) + 8 * (k >> 1);
+      const uint32_t bits = lds_u16(blk + 18 * D + (t * NG + g) * 2);
+      s[k] = bf16_bits_to_f32(bits);
+      m[k] = k & 1 ? bf_hi(md[k >> 1][0]) : bf_lo(md[k >> 1][0]);
+      const int64_t tok = tok0 + 16 * b + t;
+      const bool seen = tok >= span.first && tok <= span.last, bad = (bits & 0x7F80u) == 0x7F80u;
+      if (!seen || bad) s[k] = m[k] = 0.f;                      // 0 times it has to be 0: a NaN reaches its rows through `odd`
+      if (seen && bad) {
+        odd = true;
+        if (q == 0) atomicOr(&c.odd[stage][g][(16 * b + t) >> 5], 1u << ((16 * b + t) & 31));
+      }
+    }
+    if (odd && q == 0) c.odd_any[stage] = 1;
+#pragma unroll
+    for (int mm = 0; mm < 2; ++mm) {
+      float2 x[4];
+      centred(w[2 * gg + mm], x);
+      const int d = 16 * (2 * g + mm) + q;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                             // j & 1: channel d + 8, times 16; j >> 1: tokens + 8
+        const int k = 2 * (j >> 1), r = d + 8 * (j & 1);
+        const float f = j & 1 ? 0.0625f : 1.f;
+        uint32_t hi, lo;
+        split(fmaf(x[j].x, s[k] * f, m[k]), fmaf(x[j].y, s[k + 1] * f, m[k + 1]), hi, lo);
+        const uint32_t at = values + r * 128 + (((2 * b + (j >> 1)) ^ (r & 7)) << 4) + 4 * i;
+        sts32(at, hi);
+        sts32(at + D * 128, lo);
+      }
+    }
+  }
+}
+
+template <int D, typename Out>
+__global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const AttnArgs a) {
+  using Y = Layout<D>;
+  constexpr int NG = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Control& c = *reinterpret_cast<Control*>(smem + Y::kControlAt);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < kRawStages; ++s) mbar_init(&c.raw_full[s], 1), mbar_init(&c.raw_empty[s], kDecodeWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&c.k_full[s], kDecodeWarps), mbar_init(&c.k_empty[s], 1);
+      mbar_init(&c.v_full[s], kDecodeWarps), mbar_init(&c.v_empty[s], 2);
+      mbar_init(&c.s_full[s], 1), mbar_init(&c.s_empty[s], 4);
+      mbar_init(&c.p_full[s], 4), mbar_init(&c.pv_done[s], 1);
+      c.odd_any[s] = 0;
+      for (int g = 0; g < 8; ++g) c.odd[s][g][0] = c.odd[s][g][1] = 0;
+    }
+    mbar_init(&c.q_ready, 4), mbar_init(&c.drain, 1);
+    c.abort_flag = 0;
+    fence_barrier_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) a.joined[blockIdx.x].parts = 0;
+  const Plan pl = make_plan<kSB, kRows>(a, c.prefix, c.cost);
+  if (pl.total == 0 || blockIdx.x >= pl.ctas) return;
+  if (tid < 2) (tid ? c.end : c.begin) = bound<kSB, kRows>(a, pl, blockIdx.x + tid);
+  __syncthreads();
+  if (c.begin >= c.end) return;
+  const int steps = static_cast<int>(c.end - c.begin);
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem_base)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem_base;
+
+  Walk w;
+  w.n = w.end = 0;
+  int j = 0;                                                     // steps taken: buffers and phases go by it
+  if (warp == kWarpLoad) {
+    // ---- blocks of the cache into the raw ring; lane k < 4 copies a step's block k ----
+    bool ok = true;
+    while (w.n < steps && ok) {
+      next_piece(a, pl, c, w, steps);
+      for (; w.n < w.end; ++w.n, ++w.step) {
+        if (!needed(w)) continue;
+        const int r = j % kRawStages;
+        const uint8_t* src = nullptr;
+        const int64_t blk = w.step * kSB + lane;
+        if (lane < kSB && blk * kKvBlock < w.u.rq.L) {
+          src = kv_block_ptr(a.pool, a.kb, D, w.u.b, w.u.h, blk);
+          if (src == nullptr) atomicOr(a.err, kErrIndex);
+        }
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, src != nullptr)) * kv_block_bytes(D);
+        if (!(ok = wait(c, &c.raw_empty[r], ((j / kRawStages) & 1) ^ 1, a.err))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[r], bytes);
+        __syncwarp();
+        if (src != nullptr) bulk_g2s(smem + Y::kRawAt + r * Y::kRaw + lane * kv_block_bytes(D), src, kv_block_bytes(D), &c.raw_full[r]);
+        ++j;
+      }
+    }
+    for (int t = j > kRawStages ? j - kRawStages : 0; t < j; ++t)     // copies still under way land first
+      mbar_wait_bounded(&c.raw_full[t % kRawStages], (t / kRawStages) & 1);
+  } else if (warp == kWarpMma) {
+    // ---- products ----
+    auto values = [&](int k, bool first) {                           // O (+)= p v of step k
+      const int b = k & 1;
+      if (!wait(c, &c.p_full[b], (k >> 1) & 1, a.err) || !wait(c, &c.v_full[b], (k >> 1) & 1, a.err)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t v = sw128_desc(base + Y::kValuesAt + b * Y::kValues);
+        const uint32_t p = tmem + Y::kP + b * kTok;
+#pragma unroll
+        for (int part = 0; part < 3; ++part)                         // p_hi v_hi, p_lo v_hi, p_hi v_lo
+#pragma unroll
+          for (int x = 0; x < kTok / 16; ++x)
+            mma16(tmem + Y::kO, p + (part == 1 ? kTok / 2 : 0) + 8 * x, v + (part == 2 ? D * 128 / 16 : 0) + 2 * x, idesc(D),
+                  !(first && part == 0 && x == 0));
+        commit(&c.pv_done[b]);
+        commit(&c.v_empty[b]);
+        if (c.odd_any[b]) {                                          // the softmax warps have read it
+          c.odd_any[b] = 0;
+          for (int g = 0; g < NG; ++g) c.odd[b][g][0] = c.odd[b][g][1] = 0;
+        }
+        arrive(&c.v_empty[b]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int pieces = 0;
+    while (w.n < steps && ok) {
+      next_piece(a, pl, c, w, steps);
+      int begun = -1;                                                // first step of the piece
+      for (; w.n < w.end && ok; ++w.n, ++w.step) {
+        if (!needed(w)) continue;
+        const int b = j & 1;
+        if (begun < 0 && !(ok = wait(c, &c.q_ready, pieces & 1, a.err))) break;
+        if (!(ok = wait(c, &c.k_full[b], (j >> 1) & 1, a.err) && wait(c, &c.s_empty[b], ((j >> 1) & 1) ^ 1, a.err))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t k = sw128_desc(base + b * Y::kKeys);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+              mma16(tmem + Y::kS + b * kTok, tmem + Y::kQ + 8 * x, k + (part * Y::NBX + x / 4) * 512 + 2 * (x % 4), idesc(kTok),
+                    !(part == 0 && x == 0));
+          commit(&c.s_full[b]);
+          commit(&c.k_empty[b]);
+        }
+        __syncwarp();
+        if (begun < 0) begun = j;
+        else ok = values(j - 1, j - 1 == begun);                     // while S of this step is formed
+        ++j;
+      }
+      if (ok && begun >= 0) ok = values(j - 1, j - 1 == begun), ++pieces;
+    }
+    if (lane == 0) commit(&c.drain);                                 // every product issued so far has completed
+    __syncwarp();
+    mbar_wait_bounded(&c.drain, 0, 100000000ull);
+  } else if (warp >= kWarpDecode0) {
+    // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
+    const int d = warp - kWarpDecode0, blk = d >> 1, half = d & 1;
+    bool ok = true;
+    while (w.n < steps && ok) {
+      next_piece(a, pl, c, w, steps);
+      for (; w.n < w.end; ++w.n, ++w.step) {
+        if (!needed(w)) continue;
+        const int b = j & 1, r = j % kRawStages;
+        const uint32_t raw = base + Y::kRawAt + r * Y::kRaw, free_phase = ((j >> 1) & 1) ^ 1;
+        if (!(ok = wait(c, &c.raw_full[r], (j / kRawStages) & 1, a.err) && wait(c, &c.k_empty[b], free_phase, a.err))) break;
+        decode_keys<D>(raw, base + b * Y::kKeys, blk, half, w.step * kTok, w.s);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive(&c.k_full[b]);
+        if (!(ok = wait(c, &c.v_empty[b], free_phase, a.err))) break;
+        if (half < D / 64) decode_values<D>(c, b, raw, base + Y::kValuesAt + b * Y::kValues, blk, half, w.step * kTok, w.s);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          arrive(&c.v_full[b]);
+          arrive(&c.raw_empty[r]);
+        }
+        ++j;
+      }
+    }
+  } else if (warp >= kWarpSoft0) {
+    // ---- softmax: a thread is a row ----
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const float none = -__int_as_float(0x7f800000);
+    bool ok = true;
+    while (w.n < steps && ok) {
+      const int64_t x0 = c.begin + w.n;
+      next_piece(a, pl, c, w, steps);
+      const int64_t r = w.u.rg * kRows + row, tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
+      const bool have = row < w.s.rows;
+      const int64_t pos = w.u.rq.L - w.u.rq.T + tq;
+      const int64_t hi = have ? (pos < w.u.rq.L ? pos : w.u.rq.L - 1) : -1;                 // the row sees lo < position <= hi
+      const int64_t lo = a.window > 0 && pos - a.window > -1 ? pos - a.window : -1;
+      // the query row into TMEM (bf16 pairs, a column each); the piece before has no products left that read it
+      const uint4* q = reinterpret_cast<const uint4*>(a.q + (w.u.rq.q0 + (have ? tq : 0)) * a.q_stride + (have ? head : 0) * D);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t v[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 t = have ? __ldg(q + 8 * h + k) : make_uint4(0, 0, 0, 0);
+          v[4 * k] = t.x, v[4 * k + 1] = t.y, v[4 * k + 2] = t.z, v[4 * k + 3] = t.w;
+        }
+        tmem_store(lanes + Y::kQ + 32 * h, v);
+      }
+      tmem_wait_store();
+      tc_fence_before();
+      __syncwarp();
+      int begun = -1;
+      float ref = kRefNone, l = 0.f;
+      uint32_t odd = 0;                                             // groups in which the row has seen a NaN
+      for (; w.n < w.end; ++w.n, ++w.step) {
+        if (!needed(w)) continue;
+        const int b = j & 1;
+        if (begun < 0 && lane == 0) arrive(&c.q_ready);
+        if (!(ok = wait(c, &c.s_full[b], (j >> 1) & 1, a.err))) break;
+        tc_fence_after();
+        uint32_t s0[32], s1[32];
+        tmem_load(lanes + Y::kS + b * kTok, s0);
+        tmem_load(lanes + Y::kS + b * kTok + 32, s1);
+        tmem_wait_load(s0);
+        tmem_wait_load(s1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(&c.s_empty[b]);
+        const int64_t t0 = w.step * kTok;
+        const int from = static_cast<int>(lo - t0 + 1 > 0 ? (lo - t0 + 1 < kTok ? lo - t0 + 1 : kTok) : 0);      // sees from <= k < to
+        const int to = static_cast<int>(hi - t0 + 1 < kTok ? (hi - t0 + 1 > 0 ? hi - t0 + 1 : 0) : kTok);
+        if (__any_sync(0xffffffffu, from > 0 || to < kTok)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (k < from || k >= to) s0[k] = __float_as_uint(none);
+            if (k + 32 < from || k + 32 >= to) s1[k] = __float_as_uint(none);
+          }
+        }
+        float top = none;
+        // the row's largest logit; where the scale is negative the smallest product
+        const float c2 = a.scale_log2;
+        // masked entries are -inf as products and have to be -inf as logits
+        if (c2 > 0.f) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) top = fmaxf(top, fmaxf(__uint_as_float(s0[k]), __uint_as_float(s1[k])));
+          top *= c2;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float x = __uint_as_float(s0[k]) == none ? none : __uint_as_float(s0[k]) * c2;
+            const float y = __uint_as_float(s1[k]) == none ? none : __uint_as_float(s1[k]) * c2;
+            s0[k] = __float_as_uint(x), s1[k] = __float_as_uint(y);
+            top = fmaxf(top, fmaxf(x, y));
+          }
+        }
+        const float mul = c2 > 0.f ? c2 : 1.f;
+        // the values of this step are decoded: what was odd among them is known
+        if (!(ok = wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
+        if (c.odd_any[b]) {
+          for (int g = 0; g < NG; ++g)
+            for (int k = from; k < to; ++k)
+              if (c.odd[b][g][k >> 5] >> (k & 31) & 1) odd |= 1u << g;
+        }
+        // p's place: the product of two steps before has read it
+        if (!(ok = wait(c, &c.pv_done[b], ((j >> 1) & 1) ^ 1, a.err))) break;
+        const bool move = top > ref + 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+          const float now = move ? top : ref, f = ex2(ref - now);
+          ref = now;
+          l *= f;
+          if (begun >= 0) {                                          // O, once the step before is in it
+            if (!(ok = wait(c, &c.pv_done[b ^ 1], ((j - 1) >> 1) & 1, a.err))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+              uint32_t o[32];
+              tmem_load(lanes + Y::kO + 32 * h, o);
+              tmem_wait_load(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_store(lanes + Y::kO + 32 * h, o);
+            }
+            tmem_wait_store();
+          }
+        }
+        uint32_t p_hi[32], p_lo[32];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float x = ex2(fmaf(__uint_as_float(s0[2 * k]), mul, -ref)), y = ex2(fmaf(__uint_as_float(s0[2 * k + 1]), mul, -ref));
+          l += x + y;
+          split(x, y, p_hi[k], p_lo[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float x = ex2(fmaf(__uint_as_float(s1[2 * k]), mul, -ref)), y = ex2(fmaf(__uint_as_float(s1[2 * k + 1]), mul, -ref));
+          l += x + y;
+          split(x, y, p_hi[16 + k], p_lo[16 + k]);
+        }
+        tmem_store(lanes + Y::kP + b * kTok, p_hi);
+        tmem_store(lanes + Y::kP + b * kTok + kTok / 2, p_lo);
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(&c.p_full[b]);
+        if (begun < 0) begun = j;
+        ++j;
+      }
+      if (!ok) break;
+      if (begun >= 0 && !(ok = wait(c, &c.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.err))) break;
+      tc_fence_after();
+      // O to the output, or as a part to the workspace
+      const bool whole = x0 == w.u.start && w.end == w.u.start + w.u.n - c.begin, first = w.u.start >= c.begin;
+      float* part = a.partial + static_cast<int64_t>(2 * blockIdx.x + (first ? 1 : 0)) * kRows * (D + 2);
+      const int64_t at = (w.u.rq.q0 + tq) * a.heads + head;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int h = 0; h < D / 32; ++h) {
+        uint32_t o[32];
+        if (begun >= 0) {
+          tmem_load(lanes + Y::kO + 32 * h, o);
+          tmem_wait_load(o);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (begun < 0 || l == 0.f) o[k] = 0;
+        if (odd >> h & 1)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0x7fc00000u;
+        if (have && whole) {
+          if constexpr (sizeof(Out) == 4) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + 32 * h + k) =
+                  make_float4(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv, __uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + 32 * h + k) =
+                  make_uint4(pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
+                             pack_bf16x2(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
+                             pack_bf16x2(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
+                             pack_bf16x2(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+          }
+        } else if (have) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<uint4*>(part + row * D + 32 * h + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+      tc_fence_before();
+      if (have && whole && a.lse != nullptr) a.lse[at] = log_total(ref, l);
+      if (have && !whole) *(reinterpret_cast<float2*>(part + kRows * D) + row) = make_float2(ref, l);
+      if (!whole && first && row == 0) {
+        // this CTA has the unit's first part: the others are those of the next CTAs up to the unit's end
+        const int c1 = share_of(pl, w.u.cost + kUnitCost + w.u.n - kCutSteps);
+        a.joined[blockIdx.x] = {w.u.rq.q0, w.u.rg * kRows, w.u.h, w.s.rows, c1 - static_cast<int>(blockIdx.x) + 1, 0};
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// The parts of units cut between CTAs: a warp per row, lanes along the channels.
+constexpr int kJoinWarps = 8;
+
+template <int D, typename Out>
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgs a) {
+  constexpr int VPL = D / 32, kBatch = 12;
+  constexpr int64_t kPitch = kRows * (D + 2);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Joined u = a.joined[blockIdx.x];
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (u.parts == 0 || r >= u.rows) return;
+  auto part = [&](int c) { return a.partial + (2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * kPitch; };
+  float m = kRefNone, l = 0.f, o[VPL] = {};
+  for (int c = lane; c < u.parts; c += 32) m = fmaxf(m, __ldcg(part(c) + kRows * D + 2 * r));
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+#pragma unroll 1
+  for (int c = 0; c < u.parts; c += kBatch) {
+    float2 ml[kBatch], v[kBatch][VPL / 2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float* from = part(c + k < u.parts ? c + k : c);
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(from + kRows * D) + r);
+#pragma unroll
+      for (int x = 0; x < VPL / 2; ++x) v[k][x] = __ldcg(reinterpret_cast<const float2*>(from + r * D + VPL * lane) + x);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (c + k < u.parts) {
+        const float f = ex2(ml[k].x - m);
+        l = fmaf(f, ml[k].y, l);
+#pragma unroll
+        for (int x = 0; x < VPL; ++x) o[x] = fmaf(f, x & 1 ? v[k][x / 2].y : v[k][x / 2].x, o[x]);
+      }
+  }
+  const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int x = 0; x < VPL; ++x) put<Out>(a, at * D + VPL * lane + x, l == 0.f ? 0.f : o[x] * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[at] = log_total(m, l);
+}
+
+template <int D, typename Out>
+cudaError_t launch_block_variant(const AttnArgs& a, int grid, cudaStream_t s) {
+  static_assert(kSmemBytes<D> <= 232448, "shared memory per CTA");
+  const void* f = reinterpret_cast<const void*>(attention_block_kernel<D, Out>);
+  cudaError_t e = set_max_dynamic_smem(f);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes<D>;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attention_block_kernel<D, Out>, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, Out>, a);
+}
+
+}  // namespace
+
+uint64_t attention_block_bytes(int D) { return static_cast<uint64_t>(kKvMaxCtas) * kRows * (D + 2) * 4; }
+
+cudaError_t launch_attention_block(int D, const AttnArgs& a, int out_f32, const DeviceInfo& info, cudaStream_t s) {
+  const int grid = info.sms < kKvMaxCtas / 2 ? info.sms : kKvMaxCtas / 2;      // two parts each
+  switch (D) {
+    case 64: return out_f32 ? launch_block_variant<64, float>(a, grid, s) : launch_block_variant<64, uint16_t>(a, grid, s);
+    case 128: return out_f32 ? launch_block_variant<128, float>(a, grid, s) : launch_block_variant<128, uint16_t>(a, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace q4nx
