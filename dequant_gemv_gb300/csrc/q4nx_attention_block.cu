@@ -119,6 +119,13 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -195,23 +202,19 @@ __device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, 
   constexpr int NG = D / 32, NBX = D / 64;
   const int lane = threadIdx.x & 31, i = lane & 3, t = 8 * h + (lane >> 2), row = 16 * b + t;
   const uint32_t blk = raw + b * kv_block_bytes(D);
-  uint32_t w[NG], sc[NG / 2], md[NG / 2];
-  lds_words<NG>(w, blk + (t * 4 + i) * (4 * NG));
-  lds_words<NG / 2>(sc, blk + 16 * D + t * (2 * NG));
-  lds_words<NG / 2>(md, blk + 17 * D + t * (2 * NG));
   const bool seen = tok0 + row >= span.first && tok0 + row <= span.last;
-#pragma unroll
+#pragma unroll 1
   for (int g = 0; g < NG; ++g) {
-    float s = g & 1 ? bf_hi(sc[g >> 1]) : bf_lo(sc[g >> 1]), m = g & 1 ? bf_hi(md[g >> 1]) : bf_lo(md[g >> 1]);
+    uint32_t w[1];
+    lds_words<1>(w, blk + (t * 4 + i) * (4 * NG) + 4 * g);
+    float s = bf16_bits_to_f32(lds_u16(blk + 16 * D + (t * NG + g) * 2)), m = bf16_bits_to_f32(lds_u16(blk + 17 * D + (t * NG + g) * 2));
     if (!seen) s = m = 0.f;                                     // it may hold anything
+    const float s16 = 0.0625f * s;
     float2 c[4];
-    centred(w[g], c);
+    centred(w[0], c);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float f = j & 1 ? 0.0625f * s : s;
-      split(fmaf(c[j].x, f, m), fmaf(c[j].y, f, m), hi[j], lo[j]);
-    }
+    for (int j = 0; j < 4; ++j) split(fmaf(c[j].x, j & 1 ? s16 : s, m), fmaf(c[j].y, j & 1 ? s16 : s, m), hi[j], lo[j]);
     const uint32_t at = keys + (g >> 1) * 8192 + row * 128 + (((4 * (g & 1) + i) ^ (row & 7)) << 4);
     sts128(at, hi);
     sts128(at + NBX * 8192, lo);
@@ -226,15 +229,15 @@ __device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t ra
   constexpr int NG = D / 32;
   const int lane = threadIdx.x & 31, i = lane & 3, q = lane >> 2;
   const uint32_t blk = raw + b * kv_block_bytes(D);
-  uint32_t w[4];
-  lds_words<4>(w, blk + 8 * D + (quad * 32 + lane) * 16);
-#pragma unroll
+  const bool all = tok0 >= span.first && tok0 + kTok - 1 <= span.last;      // some row sees each token of the step
+#pragma unroll 1
   for (int gg = 0; gg < 2; ++gg) {
     const int g = 2 * quad + gg;
-    float s[4], m[4];                                           // tokens 2i, 2i+1, 2i+8, 2i+9
-    uint32_t md[2][1];
+    uint32_t w[2], md[2][1];
+    lds_words<2>(w, blk + 8 * D + (quad * 32 + lane) * 16 + 8 * gg);
     lds_words<1>(md[0], blk + 19 * D + g * 32 + 4 * i);
     lds_words<1>(md[1], blk + 19 * D + g * 32 + 4 * i + 16);
+    float s[4], m[4];                                           // tokens 2i, 2i+1, 2i+8, 2i+9
     bool odd = false;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -242,19 +245,27 @@ __device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t ra
       const uint32_t bits = lds_u16(blk + 18 * D + (t * NG + g) * 2);
       s[k] = bf16_bits_to_f32(bits);
       m[k] = k & 1 ? bf_hi(md[k >> 1][0]) : bf_lo(md[k >> 1][0]);
-      const int64_t tok = tok0 + 16 * b + t;
-      const bool seen = tok >= span.first && tok <= span.last, bad = (bits & 0x7F80u) == 0x7F80u;
-      if (!seen || bad) s[k] = m[k] = 0.f;                      // 0 times it has to be 0: a NaN reaches its rows through `odd`
-      if (seen && bad) {
-        odd = true;
-        if (q == 0) atomicOr(&c.odd[stage][g][(16 * b + t) >> 5], 1u << ((16 * b + t) & 31));
+      odd |= (bits & 0x7F80u) == 0x7F80u;
+    }
+    // 0 times a token that a row does not see has to be 0: those that no row
+    // sees may hold anything, and a NaN reaches the rows that do see it through `odd`
+    if (__any_sync(0xffffffffu, odd) || !all) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = 16 * b + 2 * i + (k & 1) + 8 * (k >> 1);
+        const int64_t tok = tok0 + t;
+        const bool seen = tok >= span.first && tok <= span.last, bad = !(fabsf(s[k]) < __int_as_float(0x7f800000));
+        if (!seen || bad) s[k] = m[k] = 0.f;
+        if (seen && bad && q == 0) {
+          atomicOr(&c.odd[stage][g][t >> 5], 1u << (t & 31));
+          c.odd_any[stage] = 1;
+        }
       }
     }
-    if (odd && q == 0) c.odd_any[stage] = 1;
 #pragma unroll
     for (int mm = 0; mm < 2; ++mm) {
       float2 x[4];
-      centred(w[2 * gg + mm], x);
+      centred(w[mm], x);
       const int d = 16 * (2 * g + mm) + q;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {                             // j & 1: channel d + 8, times 16; j >> 1: tokens + 8
@@ -427,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     // ---- softmax: a thread is a row ----
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const float none = -__int_as_float(0x7f800000);
+    const float none = -__int_as_float(0x7f800000), c2 = a.scale_log2;
     bool ok = true;
     while (w.n < steps && ok) {
       const int64_t x0 = c.begin + w.n;
@@ -461,48 +472,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (begun < 0 && lane == 0) arrive(&c.q_ready);
         if (!(ok = wait(c, &c.s_full[b], (j >> 1) & 1, a.err))) break;
         tc_fence_after();
-        uint32_t s0[32], s1[32];
-        tmem_load(lanes + Y::kS + b * kTok, s0);
-        tmem_load(lanes + Y::kS + b * kTok + 32, s1);
-        tmem_wait_load(s0);
-        tmem_wait_load(s1);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(&c.s_empty[b]);
         const int64_t t0 = w.step * kTok;
         const int from = static_cast<int>(lo - t0 + 1 > 0 ? (lo - t0 + 1 < kTok ? lo - t0 + 1 : kTok) : 0);      // sees from <= k < to
         const int to = static_cast<int>(hi - t0 + 1 < kTok ? (hi - t0 + 1 > 0 ? hi - t0 + 1 : 0) : kTok);
-        if (__any_sync(0xffffffffu, from > 0 || to < kTok)) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (k < from || k >= to) s0[k] = __float_as_uint(none);
-            if (k + 32 < from || k + 32 >= to) s1[k] = __float_as_uint(none);
-          }
-        }
+        const bool part = __any_sync(0xffffffffu, from > 0 || to < kTok);
+        // Two passes over S, 32 columns at a time and rolled: straight code for 64
+        // columns of several roles does not fit the instruction cache (103 us instead of XX).
         float top = none;
-        // the row's largest logit; where the scale is negative the smallest product
-        const float c2 = a.scale_log2;
-        // masked entries are -inf as products and have to be -inf as logits
-        if (c2 > 0.f) {
+#pragma unroll 1
+        for (int h = 0; h < kTok; h += 32) {
+          uint32_t x[32];
+          tmem_load(lanes + Y::kS + b * kTok + h, x);
+          tmem_wait_load(x);
+          if (part || c2 <= 0.f) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) top = fmaxf(top, fmaxf(__uint_as_float(s0[k]), __uint_as_float(s1[k])));
-          top *= c2;
-        } else {
+            for (int k = 0; k < 32; ++k) {
+              const float y = k + h < from || k + h >= to ? none : __uint_as_float(x[k]) * c2;
+              top = fmaxf(top, y);
+            }
+          } else {
+            float m[4] = {none, none, none, none};
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float x = __uint_as_float(s0[k]) == none ? none : __uint_as_float(s0[k]) * c2;
-            const float y = __uint_as_float(s1[k]) == none ? none : __uint_as_float(s1[k]) * c2;
-            s0[k] = __float_as_uint(x), s1[k] = __float_as_uint(y);
-            top = fmaxf(top, fmaxf(x, y));
+            for (int k = 0; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(x[k]));
+            top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c2);
           }
-        }
-        const float mul = c2 > 0.f ? c2 : 1.f;
-        // the values of this step are decoded: what was odd among them is known
-        if (!(ok = wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
-        if (c.odd_any[b]) {
-          for (int g = 0; g < NG; ++g)
-            for (int k = from; k < to; ++k)
-              if (c.odd[b][g][k >> 5] >> (k & 31) & 1) odd |= 1u << g;
         }
         // p's place: the product of two steps before has read it
         if (!(ok = wait(c, &c.pv_done[b], ((j >> 1) & 1) ^ 1, a.err))) break;
@@ -526,23 +519,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
             tmem_wait_store();
           }
         }
-        uint32_t p_hi[32], p_lo[32];
+#pragma unroll 1
+        for (int h = 0; h < kTok; h += 32) {
+          uint32_t x[32], p_hi[16], p_lo[16];
+          tmem_load(lanes + Y::kS + b * kTok + h, x);
+          tmem_wait_load(x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float x = ex2(fmaf(__uint_as_float(s0[2 * k]), mul, -ref)), y = ex2(fmaf(__uint_as_float(s0[2 * k + 1]), mul, -ref));
-          l += x + y;
-          split(x, y, p_hi[k], p_lo[k]);
-        }
+          for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), c2, -ref));
+          if (part) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float x = ex2(fmaf(__uint_as_float(s1[2 * k]), mul, -ref)), y = ex2(fmaf(__uint_as_float(s1[2 * k + 1]), mul, -ref));
-          l += x + y;
-          split(x, y, p_hi[16 + k], p_lo[16 + k]);
+            for (int k = 0; k < 32; ++k)
+              if (k + h < from || k + h >= to) x[k] = __float_as_uint(none);
+          }
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float y0 = ex2(__uint_as_float(x[2 * k])), y1 = ex2(__uint_as_float(x[2 * k + 1]));
+            sum[0] += y0;
+            sum[1] += y1;
+            split(y0, y1, p_hi[k], p_lo[k]);
+          }
+          l += sum[0] + sum[1];
+          tmem_store16(lanes + Y::kP + b * kTok + h / 2, p_hi);
+          tmem_store16(lanes + Y::kP + b * kTok + kTok / 2 + h / 2, p_lo);
         }
-        tmem_store(lanes + Y::kP + b * kTok, p_hi);
-        tmem_store(lanes + Y::kP + b * kTok + kTok / 2, p_lo);
         tmem_wait_store();
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(&c.s_empty[b]);
+        // the values of this step are decoded: what was odd among them is known
+        if (!(ok = wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
+        if (c.odd_any[b]) {
+          for (int g = 0; g < NG; ++g)
+            for (int k = from; k < to; ++k)
+              if (c.odd[b][g][k >> 5] >> (k & 31) & 1) odd |= 1u << g;
+        }
         __syncwarp();
         if (lane == 0) arrive(&c.p_full[b]);
         if (begun < 0) begun = j;
