@@ -201,23 +201,29 @@ template <int D>
 __device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, int h, int64_t tok0, const Span& span) {
   constexpr int NG = D / 32, NBX = D / 64;
   const int lane = threadIdx.x & 31, i = lane & 3, t = 8 * h + (lane >> 2), row = 16 * b + t;
-  const uint32_t blk = raw + b * kv_block_bytes(D);
+  const uint32_t blk = raw + b * kv_block_bytes(D), words = blk + (t * 4 + i) * (4 * NG), scales = blk + 16 * D + t * (2 * NG);
   const bool seen = tok0 + row >= span.first && tok0 + row <= span.last;
+  // chunk 4*(g & 1) + i of 16 bytes, swizzled by the row: group g + 1 flips bit 2
+  const uint32_t at = keys + row * 128 + ((i ^ (row & 7)) << 4);
 #pragma unroll 1
-  for (int g = 0; g < NG; ++g) {
-    uint32_t w[1];
-    lds_words<1>(w, blk + (t * 4 + i) * (4 * NG) + 4 * g);
-    float s = bf16_bits_to_f32(lds_u16(blk + 16 * D + (t * NG + g) * 2)), m = bf16_bits_to_f32(lds_u16(blk + 17 * D + (t * NG + g) * 2));
-    if (!seen) s = m = 0.f;                                     // it may hold anything
-    const float s16 = 0.0625f * s;
-    float2 c[4];
-    centred(w[0], c);
-    uint32_t hi[4], lo[4];
+  for (int g2 = 0; g2 < NG / 2; ++g2) {
+    uint32_t w[2], sc[1], md[1];
+    lds_words<2>(w, words + 8 * g2);
+    lds_words<1>(sc, scales + 4 * g2);
+    lds_words<1>(md, scales + D + 4 * g2);
+    if (!seen) sc[0] = md[0] = 0;                               // it may hold anything
 #pragma unroll
-    for (int j = 0; j < 4; ++j) split(fmaf(c[j].x, j & 1 ? s16 : s, m), fmaf(c[j].y, j & 1 ? s16 : s, m), hi[j], lo[j]);
-    const uint32_t at = keys + (g >> 1) * 8192 + row * 128 + (((4 * (g & 1) + i) ^ (row & 7)) << 4);
-    sts128(at, hi);
-    sts128(at + NBX * 8192, lo);
+    for (int e = 0; e < 2; ++e) {
+      const float s = e ? bf_hi(sc[0]) : bf_lo(sc[0]), m = e ? bf_hi(md[0]) : bf_lo(md[0]), s16 = 0.0625f * s;
+      float2 c[4];
+      centred(w[e], c);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split(fmaf(c[j].x, j & 1 ? s16 : s, m), fmaf(c[j].y, j & 1 ? s16 : s, m), hi[j], lo[j]);
+      const uint32_t to = (at ^ (e << 6)) + g2 * 8192;
+      sts128(to, hi);
+      sts128(to + NBX * 8192, lo);
+    }
   }
 }
 
@@ -230,52 +236,57 @@ __device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t ra
   const int lane = threadIdx.x & 31, i = lane & 3, q = lane >> 2;
   const uint32_t blk = raw + b * kv_block_bytes(D);
   const bool all = tok0 >= span.first && tok0 + kTok - 1 <= span.last;      // some row sees each token of the step
+  // row d = 16 * tile + q (+ 8), chunks 2b and 2b + 1 of it, swizzled by q
+  const uint32_t at = values + q * 128 + 4 * i, at0 = at + (((2 * b) ^ q) << 4), at1 = at + (((2 * b + 1) ^ q) << 4);
 #pragma unroll 1
   for (int gg = 0; gg < 2; ++gg) {
     const int g = 2 * quad + gg;
-    uint32_t w[2], md[2][1];
+    uint32_t w[2], md[2][1], bits[4];
     lds_words<2>(w, blk + 8 * D + (quad * 32 + lane) * 16 + 8 * gg);
     lds_words<1>(md[0], blk + 19 * D + g * 32 + 4 * i);
     lds_words<1>(md[1], blk + 19 * D + g * 32 + 4 * i + 16);
-    float s[4], m[4];                                           // tokens 2i, 2i+1, 2i+8, 2i+9
-    bool odd = false;
+    const uint32_t scales = blk + 18 * D + (2 * i * NG + g) * 2;            // tokens 2i, 2i+1, 2i+8, 2i+9
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = 2 * i + (k & 1) + 8 * (k >> 1);
-      const uint32_t bits = lds_u16(blk + 18 * D + (t * NG + g) * 2);
-      s[k] = bf16_bits_to_f32(bits);
-      m[k] = k & 1 ? bf_hi(md[k >> 1][0]) : bf_lo(md[k >> 1][0]);
-      odd |= (bits & 0x7F80u) == 0x7F80u;
-    }
+    for (int k = 0; k < 4; ++k) bits[k] = lds_u16(scales + ((k & 1) + 8 * (k >> 1)) * (2 * NG));
+    const bool odd = max(max(bits[0], bits[1]), max(bits[2], bits[3])) >= 0x7F80u;
     // 0 times a token that a row does not see has to be 0: those that no row
-    // sees may hold anything, and a NaN reaches the rows that do see it through `odd`
+    // sees may hold anything, and a NaN reaches the rows that do see it through c.odd
     if (__any_sync(0xffffffffu, odd) || !all) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int t = 16 * b + 2 * i + (k & 1) + 8 * (k >> 1);
         const int64_t tok = tok0 + t;
-        const bool seen = tok >= span.first && tok <= span.last, bad = !(fabsf(s[k]) < __int_as_float(0x7f800000));
-        if (!seen || bad) s[k] = m[k] = 0.f;
+        const bool seen = tok >= span.first && tok <= span.last, bad = (bits[k] & 0x7F80u) == 0x7F80u;
+        if (!seen || bad) {
+          bits[k] = 0;
+          md[k >> 1][0] &= k & 1 ? 0xFFFFu : 0xFFFF0000u;
+        }
         if (seen && bad && q == 0) {
           atomicOr(&c.odd[stage][g][t >> 5], 1u << (t & 31));
           c.odd_any[stage] = 1;
         }
       }
     }
+    float s[2][4];                                              // and a sixteenth, for the codes that come as 16c
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s[0][k] = bf16_bits_to_f32(bits[k]);
+      s[1][k] = 0.0625f * s[0][k];
+    }
+    const float m[4] = {bf_lo(md[0][0]), bf_hi(md[0][0]), bf_lo(md[1][0]), bf_hi(md[1][0])};
 #pragma unroll
     for (int mm = 0; mm < 2; ++mm) {
       float2 x[4];
       centred(w[mm], x);
-      const int d = 16 * (2 * g + mm) + q;
+      const uint32_t tile = (2 * g + mm) * 2048;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {                             // j & 1: channel d + 8, times 16; j >> 1: tokens + 8
-        const int k = 2 * (j >> 1), r = d + 8 * (j & 1);
-        const float f = j & 1 ? 0.0625f : 1.f;
+      for (int j = 0; j < 4; ++j) {                             // j & 1: channel d + 8; j >> 1: tokens + 8
+        const int k = 2 * (j >> 1);
         uint32_t hi, lo;
-        split(fmaf(x[j].x, s[k] * f, m[k]), fmaf(x[j].y, s[k + 1] * f, m[k + 1]), hi, lo);
-        const uint32_t at = values + r * 128 + (((2 * b + (j >> 1)) ^ (r & 7)) << 4) + 4 * i;
-        sts32(at, hi);
-        sts32(at + D * 128, lo);
+        split(fmaf(x[j].x, s[j & 1][k], m[k]), fmaf(x[j].y, s[j & 1][k + 1], m[k + 1]), hi, lo);
+        const uint32_t to = (j >> 1 ? at1 : at0) + tile + (j & 1) * 1024;
+        sts32(to, hi);
+        sts32(to + D * 128, lo);
       }
     }
   }
@@ -477,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         const int to = static_cast<int>(hi - t0 + 1 < kTok ? (hi - t0 + 1 > 0 ? hi - t0 + 1 : 0) : kTok);
         const bool part = __any_sync(0xffffffffu, from > 0 || to < kTok);
         // Two passes over S, 32 columns at a time and rolled: straight code for 64
-        // columns of several roles does not fit the instruction cache (103 us instead of XX).
+        // columns of several roles does not fit the instruction cache (103 us instead of 75).
         float top = none;
 #pragma unroll 1
         for (int h = 0; h < kTok; h += 32) {
