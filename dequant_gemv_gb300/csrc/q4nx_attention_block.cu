@@ -83,15 +83,26 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t idesc(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((kRows >> 4) << 24);
 }
-// one product of K = 16, by one thread
-__device__ __forceinline__ void mma16(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// four products of K = 16 (64 columns of A, 128 bytes of B's rows), issued by one
+// elected lane of a converged warp
+template <uint32_t kId>
+__device__ __forceinline__ void mma64(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 ra;\n\t.reg .b64 rb;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, 1, 1;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+      "add.u32 ra, %1, 8;\n\tadd.u64 rb, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t"
+      "add.u32 ra, %1, 16;\n\tadd.u64 rb, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t"
+      "add.u32 ra, %1, 24;\n\tadd.u64 rb, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(accumulate), "n"(kId)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
@@ -362,22 +373,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     for (int t = j > kRawStages ? j - kRawStages : 0; t < j; ++t)     // copies still under way land first
       mbar_wait_bounded(&c.raw_full[t % kRawStages], (t / kRawStages) & 1);
   } else if (warp == kWarpMma) {
-    // ---- products ----
+    // ---- products; the whole warp runs the loop and its operands are broadcast, so
+    // that they sit in uniform registers: issued from a single-lane branch the 28
+    // products of a step took 3200 cycles instead of 1800 ----
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     auto values = [&](int k, bool first) {                           // O (+)= p v of step k
       const int b = k & 1;
       if (!wait(c, &c.p_full[b], (k >> 1) & 1, a.err) || !wait(c, &c.v_full[b], (k >> 1) & 1, a.err)) return false;
       tc_fence_after();
+      const int ub = __shfl_sync(0xffffffffu, b, 0);
+      const uint64_t v = sw128_desc(base + Y::kValuesAt + ub * Y::kValues);
+      const uint32_t p = tm + Y::kP + ub * kTok;
+#pragma unroll
+      for (int part = 0; part < 3; ++part)                           // p_hi v_hi, p_lo v_hi, p_hi v_lo
+        mma64<idesc(D)>(tm + Y::kO, p + (part == 1 ? kTok / 2 : 0), v + (part == 2 ? D * 128 / 16 : 0), !(first && part == 0));
+      commit(&c.pv_done[ub]);
+      commit(&c.v_empty[ub]);
       if (lane == 0) {
-        const uint64_t v = sw128_desc(base + Y::kValuesAt + b * Y::kValues);
-        const uint32_t p = tmem + Y::kP + b * kTok;
-#pragma unroll
-        for (int part = 0; part < 3; ++part)                         // p_hi v_hi, p_lo v_hi, p_hi v_lo
-#pragma unroll
-          for (int x = 0; x < kTok / 16; ++x)
-            mma16(tmem + Y::kO, p + (part == 1 ? kTok / 2 : 0) + 8 * x, v + (part == 2 ? D * 128 / 16 : 0) + 2 * x, idesc(D),
-                  !(first && part == 0 && x == 0));
-        commit(&c.pv_done[b]);
-        commit(&c.v_empty[b]);
         if (c.odd_any[b]) {                                          // the softmax warps have read it
           c.odd_any[b] = 0;
           for (int g = 0; g < NG; ++g) c.odd[b][g][0] = c.odd[b][g][1] = 0;
@@ -398,26 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (begun < 0 && !(ok = wait(c, &c.q_ready, pieces & 1, a.err))) break;
         if (!(ok = wait(c, &c.k_full[b], (j >> 1) & 1, a.err) && wait(c, &c.s_empty[b], ((j >> 1) & 1) ^ 1, a.err))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t k = sw128_desc(base + b * Y::kKeys);
+        const int ub = __shfl_sync(0xffffffffu, b, 0);
+        const uint64_t k = sw128_desc(base + ub * Y::kKeys);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-              mma16(tmem + Y::kS + b * kTok, tmem + Y::kQ + 8 * x, k + (part * Y::NBX + x / 4) * 512 + 2 * (x % 4), idesc(kTok),
-                    !(part == 0 && x == 0));
-          commit(&c.s_full[b]);
-          commit(&c.k_empty[b]);
-        }
-        __syncwarp();
+        for (int x = 0; x < 2 * Y::NBX; ++x)                         // boxes of 64 channels, those of hi, then of lo
+          mma64<idesc(kTok)>(tm + Y::kS + ub * kTok, tm + Y::kQ + 32 * (x % Y::NBX), k + x * 512, x > 0);
+        commit(&c.s_full[ub]);
+        commit(&c.k_empty[ub]);
         if (begun < 0) begun = j;
         else ok = values(j - 1, j - 1 == begun);                     // while S of this step is formed
         ++j;
       }
       if (ok && begun >= 0) ok = values(j - 1, j - 1 == begun), ++pieces;
     }
-    if (lane == 0) commit(&c.drain);                                 // every product issued so far has completed
-    __syncwarp();
+    commit(&c.drain);                                                // every product issued so far has completed
     mbar_wait_bounded(&c.drain, 0, 100000000ull);
   } else if (warp >= kWarpDecode0) {
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
