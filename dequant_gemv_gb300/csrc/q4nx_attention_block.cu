@@ -35,9 +35,13 @@ namespace q4nx {
 
 namespace {
 
-constexpr int kRows = 128, kSB = 4, kTok = kSB * kKvBlock;      // rows of a unit, blocks and tokens of a step
-constexpr int kThreads = 512, kDecodeWarps = 8, kRawStages = 4;
-constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpSoft0 = 4, kWarpDecode0 = 8;
+constexpr int kTile = 128, kRows = 2 * kTile;                   // rows of a tile (TMEM lanes), of a unit
+constexpr int kSB = 4, kTok = kSB * kKvBlock;                   // blocks and tokens of a step
+constexpr int kThreads = 640, kDecodeWarps = 8, kRawStages = 4;
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpSoft0 = 4, kWarpDecode0 = 12;
+// registers per thread: 96 at launch, shared out anew (4, 8 and 8 warps)
+constexpr int kRegsRest = 64, kRegsSoft = 128, kRegsDecode = 80;
+static_assert(4 * kRegsRest + 8 * kRegsSoft + 8 * kRegsDecode <= kThreads / 32 * 96, "the split draws on the launch's registers");
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -47,17 +51,17 @@ struct Layout {
   static constexpr int kValues = 2 * D * 128;                   // hi rows (D x 64 tokens), then lo
   static constexpr int kRaw = kSB * kv_block_bytes(D);
   static constexpr int kValuesAt = 2 * kKeys, kRawAt = kValuesAt + 2 * kValues, kControlAt = kRawAt + kRawStages * kRaw;
-  // TMEM columns
-  static constexpr uint32_t kQ = 0, kS = D / 2, kP = kS + 2 * kTok, kO = kP + 2 * kTok;
-  static_assert(kO + D <= kTmemCols, "TMEM budget");
+  // TMEM columns of a tile; p takes the place of S, 32 columns (32 tokens) at a time: 16 of p_hi, 16 of p_lo
+  static constexpr uint32_t kQ = 0, kS = D / 2, kO = kS + kTok, kCols = kTmemCols / 2;
+  static_assert(kO + D <= kCols, "TMEM budget");
   static_assert(kControlAt % 128 == 0 && kValuesAt % 1024 == 0, "swizzled regions");
 };
 
 struct Control {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_ready, drain;
+  uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];  // of a tile
+  uint64_t drain;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
   volatile uint32_t odd_any[2];
@@ -81,21 +85,21 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 }
 // D fp32, A (TMEM) and B (shared memory) bf16, both K-major, M = 128, N = n
 __host__ __device__ constexpr uint32_t idesc(int n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((kRows >> 4) << 24);
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((kTile >> 4) << 24);
 }
-// four products of K = 16 (64 columns of A, 128 bytes of B's rows), issued by one
-// elected lane of a converged warp
-template <uint32_t kId>
+// four products of K = 16 (A at columns a, a + A1, .., 128 bytes of B's rows),
+// issued by one elected lane of a converged warp
+template <uint32_t kId, int A1, int A2, int A3>
 __device__ __forceinline__ void mma64(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred e, p, t;\n\t.reg .b32 ra;\n\t.reg .b64 rb;\n\t"
       "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, 1, 1;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
-      "add.u32 ra, %1, 8;\n\tadd.u64 rb, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t"
-      "add.u32 ra, %1, 16;\n\tadd.u64 rb, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t"
-      "add.u32 ra, %1, 24;\n\tadd.u64 rb, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(accumulate), "n"(kId)
+      "add.u32 ra, %1, %5;\n\tadd.u64 rb, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t"
+      "add.u32 ra, %1, %6;\n\tadd.u64 rb, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t"
+      "add.u32 ra, %1, %7;\n\tadd.u64 rb, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], rb, %4, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(accumulate), "n"(kId), "n"(A1), "n"(A2), "n"(A3)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -165,10 +169,11 @@ struct Span {
   int64_t first, last;
   int rows;
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, const Unit& u) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Unit& u, int from, int most) {     // its rows from .. from + most - 1
   Span s;
-  const int64_t base = u.rq.L - u.rq.T, row0 = u.rg * kRows, left = u.rq.T * a.group - row0;
-  s.rows = static_cast<int>(left < kRows ? left : kRows);
+  const int64_t base = u.rq.L - u.rq.T, row0 = u.rg * kRows + from, left = u.rq.T * a.group - row0;
+  s.rows = static_cast<int>(left < most ? left : most);
+  if (s.rows <= 0) return {0, -1, 0};
   const int64_t p0 = base + quot(row0, a.group), p1 = base + quot(row0 + s.rows - 1, a.group);
   s.first = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
   s.last = p1 < u.rq.L ? p1 : u.rq.L - 1;
@@ -185,12 +190,12 @@ struct Walk {
 };
 __device__ __forceinline__ void next_piece(const AttnArgs& a, const Plan& pl, const Control& c, Walk& w, int steps) {
   w.u = find_unit<kSB, kRows>(a, pl, c.begin + w.n);
-  w.s = span_of(a, w.u);
+  w.s = span_of(a, w.u, 0, kRows);
   const int64_t end = w.u.start + w.u.n - c.begin;
   w.end = static_cast<int>(end < steps ? end : steps);
   w.step = w.u.first + (c.begin + w.n - w.u.start);
 }
-__device__ __forceinline__ bool needed(const Walk& w) { return w.step * kTok <= w.s.last && (w.step + 1) * kTok > w.s.first; }
+__device__ __forceinline__ bool needed(const Walk& w, const Span& s) { return w.step * kTok <= s.last && (w.step + 1) * kTok > s.first; }
 
 // x, y as bf16 pairs hi + lo
 __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -317,12 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.k_full[s], kDecodeWarps), mbar_init(&c.k_empty[s], 1);
       mbar_init(&c.v_full[s], kDecodeWarps), mbar_init(&c.v_empty[s], 2);
-      mbar_init(&c.s_full[s], 1), mbar_init(&c.s_empty[s], 4);
-      mbar_init(&c.p_full[s], 4), mbar_init(&c.pv_done[s], 1);
+      mbar_init(&c.q_ready[s], 4), mbar_init(&c.s_full[s], 1);
+      mbar_init(&c.p_full[s], 4), mbar_init(&c.o_full[s], 1);
       c.odd_any[s] = 0;
       for (int g = 0; g < 8; ++g) c.odd[s][g][0] = c.odd[s][g][1] = 0;
     }
-    mbar_init(&c.q_ready, 4), mbar_init(&c.drain, 1);
+    mbar_init(&c.drain, 1);
     c.abort_flag = 0;
     fence_barrier_init();
   }
@@ -348,13 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   Walk w;
   w.n = w.end = 0;
   int j = 0;                                                     // steps taken: buffers and phases go by it
+  if (warp < kWarpSoft0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   if (warp == kWarpLoad) {
     // ---- blocks of the cache into the raw ring; lane k < 4 copies a step's block k ----
     bool ok = true;
     while (w.n < steps && ok) {
       next_piece(a, pl, c, w, steps);
       for (; w.n < w.end; ++w.n, ++w.step) {
-        if (!needed(w)) continue;
+        if (!needed(w, w.s)) continue;
         const int r = j % kRawStages;
         const uint8_t* src = nullptr;
         const int64_t blk = w.step * kSB + lane;
@@ -375,64 +381,81 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   } else if (warp == kWarpMma) {
     // ---- products; the whole warp runs the loop and its operands are broadcast, so
     // that they sit in uniform registers: issued from a single-lane branch the 28
-    // products of a step took 3200 cycles instead of 1800 ----
+    // products of a tile and step took 3200 cycles instead of 1800 ----
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    auto values = [&](int k, bool first) {                           // O (+)= p v of step k
-      const int b = k & 1;
-      if (!wait(c, &c.p_full[b], (k >> 1) & 1, a.err) || !wait(c, &c.v_full[b], (k >> 1) & 1, a.err)) return false;
-      tc_fence_after();
-      const int ub = __shfl_sync(0xffffffffu, b, 0);
-      const uint64_t v = sw128_desc(base + Y::kValuesAt + ub * Y::kValues);
-      const uint32_t p = tm + Y::kP + ub * kTok;
-#pragma unroll
-      for (int part = 0; part < 3; ++part)                           // p_hi v_hi, p_lo v_hi, p_hi v_lo
-        mma64<idesc(D)>(tm + Y::kO, p + (part == 1 ? kTok / 2 : 0), v + (part == 2 ? D * 128 / 16 : 0), !(first && part == 0));
-      commit(&c.pv_done[ub]);
-      commit(&c.v_empty[ub]);
-      if (lane == 0) {
-        if (c.odd_any[b]) {                                          // the softmax warps have read it
-          c.odd_any[b] = 0;
-          for (int g = 0; g < NG; ++g) c.odd[b][g][0] = c.odd[b][g][1] = 0;
-        }
-        arrive(&c.v_empty[b]);
-      }
-      __syncwarp();
-      return true;
-    };
+    uint32_t begun = 0, pending = 0, open = 0;                       // a bit per tile: phases of q_ready and s_full; p v to come; S formed in this piece
+    uint32_t turn = 0;
     bool ok = true;
-    int pieces = 0;
     while (w.n < steps && ok) {
       next_piece(a, pl, c, w, steps);
-      int begun = -1;                                                // first step of the piece
-      for (; w.n < w.end && ok; ++w.n, ++w.step) {
-        if (!needed(w)) continue;
-        const int b = j & 1;
-        if (begun < 0 && !(ok = wait(c, &c.q_ready, pieces & 1, a.err))) break;
-        if (!(ok = wait(c, &c.k_full[b], (j >> 1) & 1, a.err) && wait(c, &c.s_empty[b], ((j >> 1) & 1) ^ 1, a.err))) break;
-        tc_fence_after();
-        const int ub = __shfl_sync(0xffffffffu, b, 0);
-        const uint64_t k = sw128_desc(base + ub * Y::kKeys);
+      const Span s0 = span_of(a, w.u, 0, kTile), s1 = span_of(a, w.u, kTile, kTile);
+      uint32_t fresh = 0;                                            // nothing in O yet
+      bool before = false;                                           // the piece has had a step
+      for (bool more = true; more && ok;) {
+        while (w.n < w.end && !needed(w, w.s)) ++w.n, ++w.step;
+        more = w.n < w.end;
+        const int b = __shfl_sync(0xffffffffu, j & 1, 0);
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+          const uint32_t bit = 1u << t, cols = __shfl_sync(0xffffffffu, tm + t * Y::kCols, 0);
+          if (pending & bit) {                                       // O (+)= p v of the step before, while the other tile's p are formed
+            if (!(ok = wait(c, &c.p_full[t], turn >> t & 1 ^ 1, a.err) && wait(c, &c.v_full[b ^ 1], ((j - 1) >> 1) & 1, a.err))) break;
+            tc_fence_after();
+            const uint64_t v = sw128_desc(base + Y::kValuesAt + (b ^ 1) * Y::kValues);
+            const uint32_t p = cols + Y::kS, o = cols + Y::kO, add = __shfl_sync(0xffffffffu, fresh & bit ? 0 : 1, 0);
+            mma64<idesc(D), 8, 32, 40>(o, p, v, add);                // p_hi v_hi
+            mma64<idesc(D), 8, 32, 40>(o, p + 16, v, 1);             // p_lo v_hi
+            mma64<idesc(D), 8, 32, 40>(o, p, v + D * 128 / 16, 1);   // p_hi v_lo
+            pending ^= bit, fresh &= ~bit;
+          }
+          if (!more) {
+            if (open & bit) commit(&c.o_full[t]);
+          } else if (needed(w, t ? s1 : s0)) {
+            if (!(open & bit)) {
+              if (!(ok = wait(c, &c.q_ready[t], begun >> t & 1, a.err))) break;
+              open |= bit, fresh |= bit, begun ^= bit;
+            }
+            if (!(ok = wait(c, &c.k_full[b], (j >> 1) & 1, a.err))) break;
+            tc_fence_after();
+            const uint64_t k = sw128_desc(base + b * Y::kKeys);
 #pragma unroll
-        for (int x = 0; x < 2 * Y::NBX; ++x)                         // boxes of 64 channels, those of hi, then of lo
-          mma64<idesc(kTok)>(tm + Y::kS + ub * kTok, tm + Y::kQ + 32 * (x % Y::NBX), k + x * 512, x > 0);
-        commit(&c.s_full[ub]);
-        commit(&c.k_empty[ub]);
-        if (begun < 0) begun = j;
-        else ok = values(j - 1, j - 1 == begun);                     // while S of this step is formed
-        ++j;
+            for (int x = 0; x < 2 * Y::NBX; ++x)                     // boxes of 64 channels, those of hi, then of lo
+              mma64<idesc(kTok), 8, 16, 24>(cols + Y::kS, cols + Y::kQ + 32 * (x % Y::NBX), k + x * 512, x > 0);
+            commit(&c.s_full[t]);
+            pending ^= bit, turn ^= bit;
+          }
+        }
+        if (!ok) break;
+        if (before) {                                                // the step before is done with: its values' place
+          commit(&c.v_empty[b ^ 1]);
+          if (lane == 0) {
+            if (c.odd_any[b ^ 1]) {                                  // the softmax warps have read it
+              c.odd_any[b ^ 1] = 0;
+              for (int g = 0; g < NG; ++g) c.odd[b ^ 1][g][0] = c.odd[b ^ 1][g][1] = 0;
+            }
+            arrive(&c.v_empty[b ^ 1]);
+          }
+          __syncwarp();
+        }
+        if (more) {
+          commit(&c.k_empty[b]);
+          before = true;
+          ++j, ++w.n, ++w.step;
+        }
       }
-      if (ok && begun >= 0) ok = values(j - 1, j - 1 == begun), ++pieces;
+      open = 0;
     }
     commit(&c.drain);                                                // every product issued so far has completed
     mbar_wait_bounded(&c.drain, 0, 100000000ull);
   } else if (warp >= kWarpDecode0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
     const int d = warp - kWarpDecode0, blk = d >> 1, half = d & 1;
     bool ok = true;
     while (w.n < steps && ok) {
       next_piece(a, pl, c, w, steps);
       for (; w.n < w.end; ++w.n, ++w.step) {
-        if (!needed(w)) continue;
+        if (!needed(w, w.s)) continue;
         const int b = j & 1, r = j % kRawStages;
         const uint32_t raw = base + Y::kRawAt + r * Y::kRaw, free_phase = ((j >> 1) & 1) ^ 1;
         if (!(ok = wait(c, &c.raw_full[r], (j / kRawStages) & 1, a.err) && wait(c, &c.k_empty[b], free_phase, a.err))) break;
@@ -452,14 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       }
     }
   } else if (warp >= kWarpSoft0) {
-    // ---- softmax: a thread is a row ----
-    const int row = 32 * (warp & 3) + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    // ---- softmax, four warps a tile: a thread is a row ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int t = (warp - kWarpSoft0) >> 2, row = kTile * t + 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + t * Y::kCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    int turn = 0;                                                    // steps of the tile
+    int piece = 0;
     const float none = -__int_as_float(0x7f800000), c2 = a.scale_log2;
     bool ok = true;
     while (w.n < steps && ok) {
       const int64_t x0 = c.begin + w.n;
       next_piece(a, pl, c, w, steps);
+      const Span own = span_of(a, w.u, kTile * t, kTile);
       const int64_t r = w.u.rg * kRows + row, tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
       const bool have = row < w.s.rows;
       const int64_t pos = w.u.rq.L - w.u.rq.T + tq;
@@ -480,14 +507,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       tmem_wait_store();
       tc_fence_before();
       __syncwarp();
-      int begun = -1;
+      bool begun = false;
       float ref = kRefNone, l = 0.f;
       uint32_t odd = 0;                                             // groups in which the row has seen a NaN
       for (; w.n < w.end; ++w.n, ++w.step) {
-        if (!needed(w)) continue;
-        const int b = j & 1;
-        if (begun < 0 && lane == 0) arrive(&c.q_ready);
-        if (!(ok = wait(c, &c.s_full[b], (j >> 1) & 1, a.err))) break;
+        if (!needed(w, w.s)) continue;
+        const int b = j & 1, jv = j >> 1;
+        ++j;
+        if (!needed(w, own)) continue;
+        if (!begun && lane == 0) arrive(&c.q_ready[t]);
+        if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err))) break;
         tc_fence_after();
         const int64_t t0 = w.step * kTok;
         const int from = static_cast<int>(lo - t0 + 1 > 0 ? (lo - t0 + 1 < kTok ? lo - t0 + 1 : kTok) : 0);      // sees from <= k < to
@@ -499,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
 #pragma unroll 1
         for (int h = 0; h < kTok; h += 32) {
           uint32_t x[32];
-          tmem_load(lanes + Y::kS + b * kTok + h, x);
+          tmem_load(lanes + Y::kS + h, x);
           tmem_wait_load(x);
           if (part || c2 <= 0.f) {
 #pragma unroll
@@ -514,16 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
             top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c2);
           }
         }
-        // p's place: the product of two steps before has read it
-        if (!(ok = wait(c, &c.pv_done[b], ((j >> 1) & 1) ^ 1, a.err))) break;
         const bool move = top > ref + 8.f;
         if (__any_sync(0xffffffffu, move)) {
           const float now = move ? top : ref, f = ex2(ref - now);
           ref = now;
           l *= f;
-          if (begun >= 0) {                                          // O, once the step before is in it
-            if (!(ok = wait(c, &c.pv_done[b ^ 1], ((j - 1) >> 1) & 1, a.err))) break;
-            tc_fence_after();
+          if (begun) {                                               // O: the products before S are in it
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
               uint32_t o[32];
@@ -539,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
 #pragma unroll 1
         for (int h = 0; h < kTok; h += 32) {
           uint32_t x[32], p_hi[16], p_lo[16];
-          tmem_load(lanes + Y::kS + b * kTok + h, x);
+          tmem_load(lanes + Y::kS + h, x);
           tmem_wait_load(x);
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), c2, -ref));
@@ -557,27 +582,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
             split(y0, y1, p_hi[k], p_lo[k]);
           }
           l += sum[0] + sum[1];
-          tmem_store16(lanes + Y::kP + b * kTok + h / 2, p_hi);
-          tmem_store16(lanes + Y::kP + b * kTok + kTok / 2 + h / 2, p_lo);
+          tmem_store16(lanes + Y::kS + h, p_hi);
+          tmem_store16(lanes + Y::kS + h + 16, p_lo);
         }
         tmem_wait_store();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive(&c.s_empty[b]);
         // the values of this step are decoded: what was odd among them is known
-        if (!(ok = wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
+        if (!(ok = wait(c, &c.v_full[b], jv & 1, a.err))) break;
         if (c.odd_any[b]) {
           for (int g = 0; g < NG; ++g)
             for (int k = from; k < to; ++k)
               if (c.odd[b][g][k >> 5] >> (k & 31) & 1) odd |= 1u << g;
         }
         __syncwarp();
-        if (lane == 0) arrive(&c.p_full[b]);
-        if (begun < 0) begun = j;
-        ++j;
+        if (lane == 0) arrive(&c.p_full[t]);
+        begun = true;
       }
       if (!ok) break;
-      if (begun >= 0 && !(ok = wait(c, &c.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.err))) break;
+      if (begun && !(ok = wait(c, &c.o_full[t], piece++ & 1, a.err))) break;
       tc_fence_after();
       // O to the output, or as a part to the workspace
       const bool whole = x0 == w.u.start && w.end == w.u.start + w.u.n - c.begin, first = w.u.start >= c.begin;
@@ -587,13 +610,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
 #pragma unroll 1
       for (int h = 0; h < D / 32; ++h) {
         uint32_t o[32];
-        if (begun >= 0) {
+        if (begun) {
           tmem_load(lanes + Y::kO + 32 * h, o);
           tmem_wait_load(o);
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          if (begun < 0 || l == 0.f) o[k] = 0;
+          if (!begun || l == 0.f) o[k] = 0;
         if (odd >> h & 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0x7fc00000u;
