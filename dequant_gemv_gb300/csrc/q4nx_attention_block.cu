@@ -64,8 +64,8 @@ struct Control {
   uint64_t drain;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
-  volatile uint32_t odd_any[2];
-  uint32_t odd[2][8][2];                            // tokens kept as NaN: [stage][group][64 tokens]
+  volatile int odd_any[2];                          // the last step (from 1 on) with a value kept as NaN, by stage
+  volatile int odd[2][4][kTok];                     // that of a group's token
   int64_t begin, end;
   int64_t prefix[kKvMaxBatch + 1], cost[kKvMaxBatch + 1];
 };
@@ -148,8 +148,10 @@ __device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&v)[4]) {
 __device__ __forceinline__ void sts32(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 
 // Bounded wait that also ends when another warp has given up; for a whole warp.
+// The first wait sleeps without a look at the timer, whose read would lie between
+// the phase's end and the warp's next step.
 __device__ __forceinline__ bool wait(Control& c, uint64_t* bar, uint32_t parity, uint32_t* err) {
-  bool ok = mbar_try_wait(bar, parity);
+  bool ok = mbar_try_wait_sleep(bar, parity, 20000u);
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
     while (!(ok = mbar_try_wait_sleep(bar, parity, 1000000u))) {
@@ -182,25 +184,37 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Unit& u, int fr
 
 // A CTA's range, piece by piece (a piece: its part of one unit), the same for
 // every warp: steps that no row sees are left out by all of them.
+struct Range {
+  int lo, hi;
+};
 struct Walk {
   Unit u;
   Span s;
-  int n, end;               // the CTA's next step, the end of the piece
-  int64_t step;             // the request's step of n
+  int at, end;              // the CTA's steps of the piece
+  int64_t step0;            // the request's step of the CTA's step 0
+  Range r;                  // those that some row sees
 };
+__device__ __forceinline__ Range range_of(const Walk& w, const Span& s) {
+  if (s.last < s.first) return {w.at, w.at};
+  const int64_t lo = s.first / kTok - w.step0, hi = s.last / kTok + 1 - w.step0;
+  const Range r = {lo > w.at ? static_cast<int>(lo < w.end ? lo : w.end) : w.at, hi < w.end ? static_cast<int>(hi > w.at ? hi : w.at) : w.end};
+  return r;
+}
 __device__ __forceinline__ void next_piece(const AttnArgs& a, const Plan& pl, const Control& c, Walk& w, int steps) {
-  w.u = find_unit<kSB, kRows>(a, pl, c.begin + w.n);
+  w.at = w.end;
+  w.u = find_unit<kSB, kRows>(a, pl, c.begin + w.at);
   w.s = span_of(a, w.u, 0, kRows);
   const int64_t end = w.u.start + w.u.n - c.begin;
   w.end = static_cast<int>(end < steps ? end : steps);
-  w.step = w.u.first + (c.begin + w.n - w.u.start);
+  w.step0 = w.u.first + (c.begin - w.u.start);
+  w.r = range_of(w, w.s);
 }
-__device__ __forceinline__ bool needed(const Walk& w, const Span& s) { return w.step * kTok <= s.last && (w.step + 1) * kTok > s.first; }
 
 // x, y as bf16 pairs hi + lo
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf_lo(hi), y - bf_hi(hi));
+__device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  const float2 rest = ffma2(make_float2(bf_lo(hi), bf_hi(hi)), both(-1.f), x);
+  lo = pack_bf16x2(rest.x, rest.y);
 }
 // the four pairs of centred codes of a word; the second and fourth times 16
 __device__ __forceinline__ void centred(uint32_t w, float2 (&c)[4]) {
@@ -235,7 +249,7 @@ __device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, 
       centred(w[e], c);
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split(fmaf(c[j].x, j & 1 ? s16 : s, m), fmaf(c[j].y, j & 1 ? s16 : s, m), hi[j], lo[j]);
+      for (int j = 0; j < 4; ++j) split(ffma2(c[j], both(j & 1 ? s16 : s), both(m)), hi[j], lo[j]);
       const uint32_t to = (at ^ (e << 6)) + g2 * 8192;
       sts128(to, hi);
       sts128(to + NBX * 8192, lo);
@@ -246,7 +260,7 @@ __device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, 
 // Values of a block's 64 channels 64*quad .. : words of channels d = 16mt +
 // lane/4 and d + 8, tokens 2i, 2i+1, 2i+8, 2i+9, into the hi and lo rows d.
 template <int D>
-__device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t raw, uint32_t values, int b, int quad, int64_t tok0,
+__device__ __forceinline__ void decode_values(Control& c, int j, uint32_t raw, uint32_t values, int b, int quad, int64_t tok0,
                                               const Span& span) {
   constexpr int NG = D / 32;
   const int lane = threadIdx.x & 31, i = lane & 3, q = lane >> 2;
@@ -278,18 +292,18 @@ __device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t ra
           md[k >> 1][0] &= k & 1 ? 0xFFFFu : 0xFFFF0000u;
         }
         if (seen && bad && q == 0) {
-          atomicOr(&c.odd[stage][g][t >> 5], 1u << (t & 31));
-          c.odd_any[stage] = 1;
+          c.odd[j & 1][g][t] = j + 1;
+          c.odd_any[j & 1] = j + 1;
         }
       }
     }
-    float s[2][4];                                              // and a sixteenth, for the codes that come as 16c
+    float2 s[2][2], m[2];                                       // and a sixteenth, for the codes that come as 16c
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s[0][k] = bf16_bits_to_f32(bits[k]);
-      s[1][k] = 0.0625f * s[0][k];
+    for (int k = 0; k < 2; ++k) {
+      s[0][k] = make_float2(bf16_bits_to_f32(bits[2 * k]), bf16_bits_to_f32(bits[2 * k + 1]));
+      s[1][k] = mul2(s[0][k], both(0.0625f));
+      m[k] = make_float2(bf_lo(md[k][0]), bf_hi(md[k][0]));
     }
-    const float m[4] = {bf_lo(md[0][0]), bf_hi(md[0][0]), bf_lo(md[1][0]), bf_hi(md[1][0])};
 #pragma unroll
     for (int mm = 0; mm < 2; ++mm) {
       float2 x[4];
@@ -297,9 +311,8 @@ __device__ __forceinline__ void decode_values(Control& c, int stage, uint32_t ra
       const uint32_t tile = (2 * g + mm) * 2048;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {                             // j & 1: channel d + 8; j >> 1: tokens + 8
-        const int k = 2 * (j >> 1);
         uint32_t hi, lo;
-        split(fmaf(x[j].x, s[j & 1][k], m[k]), fmaf(x[j].y, s[j & 1][k + 1], m[k + 1]), hi, lo);
+        split(ffma2(x[j], s[j & 1][j >> 1], m[j >> 1]), hi, lo);
         const uint32_t to = (j >> 1 ? at1 : at0) + tile + (j & 1) * 1024;
         sts32(to, hi);
         sts32(to + D * 128, lo);
@@ -317,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   Control& c = *reinterpret_cast<Control*>(smem + Y::kControlAt);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int k = tid; k < 2 * 4 * kTok; k += kThreads) c.odd[0][0][k] = 0;
   if (tid == 0) {
     for (int s = 0; s < kRawStages; ++s) mbar_init(&c.raw_full[s], 1), mbar_init(&c.raw_empty[s], kDecodeWarps);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.k_full[s], kDecodeWarps), mbar_init(&c.k_empty[s], 1);
-      mbar_init(&c.v_full[s], kDecodeWarps), mbar_init(&c.v_empty[s], 2);
+      mbar_init(&c.v_full[s], kDecodeWarps), mbar_init(&c.v_empty[s], 1);
       mbar_init(&c.q_ready[s], 4), mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], 4), mbar_init(&c.o_full[s], 1);
       c.odd_any[s] = 0;
-      for (int g = 0; g < 8; ++g) c.odd[s][g][0] = c.odd[s][g][1] = 0;
     }
     mbar_init(&c.drain, 1);
     c.abort_flag = 0;
@@ -351,19 +364,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   const uint32_t tmem = c.tmem_base;
 
   Walk w;
-  w.n = w.end = 0;
+  w.end = 0;
   int j = 0;                                                     // steps taken: buffers and phases go by it
   if (warp < kWarpSoft0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   if (warp == kWarpLoad) {
     // ---- blocks of the cache into the raw ring; lane k < 4 copies a step's block k ----
     bool ok = true;
-    while (w.n < steps && ok) {
+    while (w.end < steps && ok) {
       next_piece(a, pl, c, w, steps);
-      for (; w.n < w.end; ++w.n, ++w.step) {
-        if (!needed(w, w.s)) continue;
+      for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int r = j % kRawStages;
         const uint8_t* src = nullptr;
-        const int64_t blk = w.step * kSB + lane;
+        const int64_t blk = (w.step0 + n) * kSB + lane;
         if (lane < kSB && blk * kKvBlock < w.u.rq.L) {
           src = kv_block_ptr(a.pool, a.kb, D, w.u.b, w.u.h, blk);
           if (src == nullptr) atomicOr(a.err, kErrIndex);
@@ -386,36 +398,36 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     uint32_t begun = 0, pending = 0, open = 0;                       // a bit per tile: phases of q_ready and s_full; p v to come; S formed in this piece
     uint32_t turn = 0;
     bool ok = true;
-    while (w.n < steps && ok) {
+    while (w.end < steps && ok) {
       next_piece(a, pl, c, w, steps);
-      const Span s0 = span_of(a, w.u, 0, kTile), s1 = span_of(a, w.u, kTile, kTile);
+      const Range r0 = range_of(w, span_of(a, w.u, 0, kTile)), r1 = range_of(w, span_of(a, w.u, kTile, kTile));
       uint32_t fresh = 0;                                            // nothing in O yet
-      bool before = false;                                           // the piece has had a step
-      for (bool more = true; more && ok;) {
-        while (w.n < w.end && !needed(w, w.s)) ++w.n, ++w.step;
-        more = w.n < w.end;
+      for (int n = w.r.lo; n <= w.r.hi && ok; ++n) {                 // and once more for the last p v
+        const bool more = n < w.r.hi;
+        bool keys = false;                                           // they are there
         const int b = __shfl_sync(0xffffffffu, j & 1, 0);
 #pragma unroll 1
         for (int t = 0; t < 2 && ok; ++t) {
           const uint32_t bit = 1u << t, cols = __shfl_sync(0xffffffffu, tm + t * Y::kCols, 0);
           if (pending & bit) {                                       // O (+)= p v of the step before, while the other tile's p are formed
-            if (!(ok = wait(c, &c.p_full[t], turn >> t & 1 ^ 1, a.err) && wait(c, &c.v_full[b ^ 1], ((j - 1) >> 1) & 1, a.err))) break;
+            if (!(ok = wait(c, &c.p_full[t], (turn >> t & 1) ^ 1, a.err))) break;      // whose warps have waited for v_full
             tc_fence_after();
             const uint64_t v = sw128_desc(base + Y::kValuesAt + (b ^ 1) * Y::kValues);
-            const uint32_t p = cols + Y::kS, o = cols + Y::kO, add = __shfl_sync(0xffffffffu, fresh & bit ? 0 : 1, 0);
-            mma64<idesc(D), 8, 32, 40>(o, p, v, add);                // p_hi v_hi
+            const uint32_t p = cols + Y::kS, o = cols + Y::kO;
+            mma64<idesc(D), 8, 32, 40>(o, p, v, !(fresh & bit));     // p_hi v_hi
             mma64<idesc(D), 8, 32, 40>(o, p + 16, v, 1);             // p_lo v_hi
             mma64<idesc(D), 8, 32, 40>(o, p, v + D * 128 / 16, 1);   // p_hi v_lo
             pending ^= bit, fresh &= ~bit;
           }
+          if (t == 1 && n > w.r.lo) commit(&c.v_empty[b ^ 1]);       // the step before is done with: its values' place
           if (!more) {
             if (open & bit) commit(&c.o_full[t]);
-          } else if (needed(w, t ? s1 : s0)) {
+          } else if (n >= (t ? r1.lo : r0.lo) && n < (t ? r1.hi : r0.hi)) {
             if (!(open & bit)) {
               if (!(ok = wait(c, &c.q_ready[t], begun >> t & 1, a.err))) break;
               open |= bit, fresh |= bit, begun ^= bit;
             }
-            if (!(ok = wait(c, &c.k_full[b], (j >> 1) & 1, a.err))) break;
+            if (!keys && !(ok = keys = wait(c, &c.k_full[b], (j >> 1) & 1, a.err))) break;
             tc_fence_after();
             const uint64_t k = sw128_desc(base + b * Y::kKeys);
 #pragma unroll
@@ -426,21 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           }
         }
         if (!ok) break;
-        if (before) {                                                // the step before is done with: its values' place
-          commit(&c.v_empty[b ^ 1]);
-          if (lane == 0) {
-            if (c.odd_any[b ^ 1]) {                                  // the softmax warps have read it
-              c.odd_any[b ^ 1] = 0;
-              for (int g = 0; g < NG; ++g) c.odd[b ^ 1][g][0] = c.odd[b ^ 1][g][1] = 0;
-            }
-            arrive(&c.v_empty[b ^ 1]);
-          }
-          __syncwarp();
-        }
         if (more) {
           commit(&c.k_empty[b]);
-          before = true;
-          ++j, ++w.n, ++w.step;
+          ++j;
         }
       }
       open = 0;
@@ -452,19 +452,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
     const int d = warp - kWarpDecode0, blk = d >> 1, half = d & 1;
     bool ok = true;
-    while (w.n < steps && ok) {
+    while (w.end < steps && ok) {
       next_piece(a, pl, c, w, steps);
-      for (; w.n < w.end; ++w.n, ++w.step) {
-        if (!needed(w, w.s)) continue;
+      for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int b = j & 1, r = j % kRawStages;
+        const int64_t t0 = (w.step0 + n) * kTok;
         const uint32_t raw = base + Y::kRawAt + r * Y::kRaw, free_phase = ((j >> 1) & 1) ^ 1;
         if (!(ok = wait(c, &c.raw_full[r], (j / kRawStages) & 1, a.err) && wait(c, &c.k_empty[b], free_phase, a.err))) break;
-        decode_keys<D>(raw, base + b * Y::kKeys, blk, half, w.step * kTok, w.s);
+        decode_keys<D>(raw, base + b * Y::kKeys, blk, half, t0, w.s);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) arrive(&c.k_full[b]);
         if (!(ok = wait(c, &c.v_empty[b], free_phase, a.err))) break;
-        if (half < D / 64) decode_values<D>(c, b, raw, base + Y::kValuesAt + b * Y::kValues, blk, half, w.step * kTok, w.s);
+        if (half < D / 64) decode_values<D>(c, j, raw, base + Y::kValuesAt + b * Y::kValues, blk, half, t0, w.s);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -483,24 +483,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     int piece = 0;
     const float none = -__int_as_float(0x7f800000), c2 = a.scale_log2;
     bool ok = true;
-    while (w.n < steps && ok) {
-      const int64_t x0 = c.begin + w.n;
+    while (w.end < steps && ok) {
       next_piece(a, pl, c, w, steps);
-      const Span own = span_of(a, w.u, kTile * t, kTile);
-      const int64_t r = w.u.rg * kRows + row, tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
-      const bool have = row < w.s.rows;
+      const int64_t x0 = c.begin + w.at, row0 = w.u.rg * kRows, left = w.u.rq.T * a.group - row0;
+      const bool have = row < w.s.rows;                              // those that have none take the last, and keep nothing of it
+      const int64_t r = row0 + (row < left ? row : left - 1), tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
       const int64_t pos = w.u.rq.L - w.u.rq.T + tq;
-      const int64_t hi = have ? (pos < w.u.rq.L ? pos : w.u.rq.L - 1) : -1;                 // the row sees lo < position <= hi
+      const int64_t hi = pos < w.u.rq.L ? pos : w.u.rq.L - 1;                               // the row sees lo < position <= hi
       const int64_t lo = a.window > 0 && pos - a.window > -1 ? pos - a.window : -1;
+      // the positions that all rows of the warp see; later rows see from and to later ones
+      const int64_t all_lo = __shfl_sync(0xffffffffu, lo, 31), all_hi = __shfl_sync(0xffffffffu, hi, 0);
+      const Range own = range_of(w, span_of(a, w.u, kTile * t, kTile));
       // the query row into TMEM (bf16 pairs, a column each); the piece before has no products left that read it
-      const uint4* q = reinterpret_cast<const uint4*>(a.q + (w.u.rq.q0 + (have ? tq : 0)) * a.q_stride + (have ? head : 0) * D);
+      const uint4* q = reinterpret_cast<const uint4*>(a.q + (w.u.rq.q0 + tq) * a.q_stride + head * D);
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint32_t v[32];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint4 t = have ? __ldg(q + 8 * h + k) : make_uint4(0, 0, 0, 0);
-          v[4 * k] = t.x, v[4 * k + 1] = t.y, v[4 * k + 2] = t.z, v[4 * k + 3] = t.w;
+          const uint4 x = __ldg(q + 8 * h + k);
+          v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = x.z, v[4 * k + 3] = x.w;
         }
         tmem_store(lanes + Y::kQ + 32 * h, v);
       }
@@ -510,18 +512,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       bool begun = false;
       float ref = kRefNone, l = 0.f;
       uint32_t odd = 0;                                             // groups in which the row has seen a NaN
-      for (; w.n < w.end; ++w.n, ++w.step) {
-        if (!needed(w, w.s)) continue;
-        const int b = j & 1, jv = j >> 1;
-        ++j;
-        if (!needed(w, own)) continue;
+      j += own.lo - w.r.lo;
+      for (int n = own.lo; n < own.hi; ++n, ++j) {
+        const int b = j & 1;
         if (!begun && lane == 0) arrive(&c.q_ready[t]);
+        const int64_t t0 = (w.step0 + n) * kTok;
+        const bool part = t0 <= all_lo || t0 + kTok - 1 > all_hi;
+        int from = 0, to = kTok;                                    // sees from <= k < to
+        if (part) {
+          from = static_cast<int>(lo - t0 + 1 > 0 ? (lo - t0 + 1 < kTok ? lo - t0 + 1 : kTok) : 0);
+          to = static_cast<int>(hi - t0 + 1 < kTok ? (hi - t0 + 1 > 0 ? hi - t0 + 1 : 0) : kTok);
+        }
+        // the values of this step, decoded by the time of S: what is odd among them
+        if (!(ok = wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
+        if (c.odd_any[b] == j + 1) {
+          for (int g = 0; g < NG; ++g)
+            for (int k = from; k < to; ++k)
+              if (c.odd[b][g][k] == j + 1) odd |= 1u << g;
+        }
+        __syncwarp();
         if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err))) break;
         tc_fence_after();
-        const int64_t t0 = w.step * kTok;
-        const int from = static_cast<int>(lo - t0 + 1 > 0 ? (lo - t0 + 1 < kTok ? lo - t0 + 1 : kTok) : 0);      // sees from <= k < to
-        const int to = static_cast<int>(hi - t0 + 1 < kTok ? (hi - t0 + 1 > 0 ? hi - t0 + 1 : 0) : kTok);
-        const bool part = __any_sync(0xffffffffu, from > 0 || to < kTok);
         // Two passes over S, 32 columns at a time and rolled: straight code for 64
         // columns of several roles does not fit the instruction cache (103 us instead of 75).
         float top = none;
@@ -539,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           } else {
             float m[4] = {none, none, none, none};
 #pragma unroll
-            for (int k = 0; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(x[k]));
+            for (int k = 0; k < 32; k += 2)
+              m[k / 2 & 3] = fmaxf(m[k / 2 & 3], fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
             top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c2);
           }
         }
@@ -566,40 +578,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           uint32_t x[32], p_hi[16], p_lo[16];
           tmem_load(lanes + Y::kS + h, x);
           tmem_wait_load(x);
+          float2 sum = both(0.f), y[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), c2, -ref));
+          for (int k = 0; k < 16; ++k)
+            y[k] = ffma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), both(c2), both(-ref));
           if (part) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k + h < from || k + h >= to) x[k] = __float_as_uint(none);
+            for (int k = 0; k < 16; ++k) {
+              if (2 * k + h < from || 2 * k + h >= to) y[k].x = none;
+              if (2 * k + 1 + h < from || 2 * k + 1 + h >= to) y[k].y = none;
+            }
           }
-          float sum[2] = {0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float y0 = ex2(__uint_as_float(x[2 * k])), y1 = ex2(__uint_as_float(x[2 * k + 1]));
-            sum[0] += y0;
-            sum[1] += y1;
-            split(y0, y1, p_hi[k], p_lo[k]);
+            y[k] = ex2(y[k]);
+            sum = fadd2(sum, y[k]);
+            split(y[k], p_hi[k], p_lo[k]);
           }
-          l += sum[0] + sum[1];
+          l += sum.x + sum.y;
           tmem_store16(lanes + Y::kS + h, p_hi);
           tmem_store16(lanes + Y::kS + h + 16, p_lo);
         }
         tmem_wait_store();
         tc_fence_before();
         __syncwarp();
-        // the values of this step are decoded: what was odd among them is known
-        if (!(ok = wait(c, &c.v_full[b], jv & 1, a.err))) break;
-        if (c.odd_any[b]) {
-          for (int g = 0; g < NG; ++g)
-            for (int k = from; k < to; ++k)
-              if (c.odd[b][g][k >> 5] >> (k & 31) & 1) odd |= 1u << g;
-        }
-        __syncwarp();
         if (lane == 0) arrive(&c.p_full[t]);
         begun = true;
       }
       if (!ok) break;
+      j += w.r.hi - own.hi;
       if (begun && !(ok = wait(c, &c.o_full[t], piece++ & 1, a.err))) break;
       tc_fence_after();
       // O to the output, or as a part to the workspace
