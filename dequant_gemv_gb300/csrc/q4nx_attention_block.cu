@@ -40,7 +40,7 @@ constexpr int kSB = 4, kTok = kSB * kKvBlock;                   // blocks and to
 constexpr int kThreads = 640, kDecodeWarps = 8, kRawStages = 4;
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpSoft0 = 4, kWarpDecode0 = 12;
 // registers per thread: 96 at launch, shared out anew (4, 8 and 8 warps)
-constexpr int kRegsRest = 64, kRegsSoft = 128, kRegsDecode = 80;
+constexpr int kRegsRest = 64, kRegsSoft = 144, kRegsDecode = 64;
 static_assert(4 * kRegsRest + 8 * kRegsSoft + 8 * kRegsDecode <= kThreads / 32 * 96, "the split draws on the launch's registers");
 constexpr uint32_t kTmemCols = 512;
 
@@ -123,6 +123,16 @@ __device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+// with its wait
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
@@ -533,27 +543,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         __syncwarp();
         if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err))) break;
         tc_fence_after();
-        // Two passes over S, 32 columns at a time and rolled: straight code for 64
-        // columns of several roles does not fit the instruction cache (103 us instead of 75).
-        float top = none;
-#pragma unroll 1
-        for (int h = 0; h < kTok; h += 32) {
-          uint32_t x[32];
-          tmem_load(lanes + Y::kS + h, x);
-          tmem_wait_load(x);
-          if (part || c2 <= 0.f) {
+        uint32_t x[2][32];
+        tmem_load(lanes + Y::kS, x[0]);
+        tmem_load(lanes + Y::kS + 32, x[1]);
+        tmem_wait_load(x[0]);
+        tmem_wait_load(x[1]);
+        float top = none, mul = c2;
+        if (part || c2 <= 0.f) {
+          mul = 1.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float y = k + h < from || k + h >= to ? none : __uint_as_float(x[k]) * c2;
+              const float y = k + 32 * h < from || k + 32 * h >= to ? none : __uint_as_float(x[h][k]) * c2;
+              x[h][k] = __float_as_uint(y);
               top = fmaxf(top, y);
             }
-          } else {
-            float m[4] = {none, none, none, none};
+        } else {
+          float m[4] = {none, none, none, none};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int k = 0; k < 32; k += 2)
-              m[k / 2 & 3] = fmaxf(m[k / 2 & 3], fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-            top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c2);
-          }
+              m[k / 2 & 3] = fmaxf(m[k / 2 & 3], fmaxf(__uint_as_float(x[h][k]), __uint_as_float(x[h][k + 1])));
+          top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c2;
         }
         const bool move = top > ref + 8.f;
         if (__any_sync(0xffffffffu, move)) {
@@ -562,42 +575,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           l *= f;
           if (begun) {                                               // O: the products before S are in it
 #pragma unroll 1
-            for (int h = 0; h < D / 32; ++h) {
-              uint32_t o[32];
-              tmem_load(lanes + Y::kO + 32 * h, o);
-              tmem_wait_load(o);
+            for (int h = 0; h < D / 16; ++h) {
+              uint32_t o[16];
+              tmem_load16(lanes + Y::kO + 16 * h, o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_store(lanes + Y::kO + 32 * h, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_store16(lanes + Y::kO + 16 * h, o);
             }
             tmem_wait_store();
           }
         }
-#pragma unroll 1
-        for (int h = 0; h < kTok; h += 32) {
-          uint32_t x[32], p_hi[16], p_lo[16];
-          tmem_load(lanes + Y::kS + h, x);
-          tmem_wait_load(x);
-          float2 sum = both(0.f), y[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            y[k] = ffma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), both(c2), both(-ref));
-          if (part) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              if (2 * k + h < from || 2 * k + h >= to) y[k].x = none;
-              if (2 * k + 1 + h < from || 2 * k + 1 + h >= to) y[k].y = none;
-            }
-          }
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p_hi[16], p_lo[16];
+          float2 sum = both(0.f);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            y[k] = ex2(y[k]);
-            sum = fadd2(sum, y[k]);
-            split(y[k], p_hi[k], p_lo[k]);
+            const float2 y = ex2(ffma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])), both(mul), both(-ref)));
+            sum = fadd2(sum, y);
+            split(y, p_hi[k], p_lo[k]);
           }
           l += sum.x + sum.y;
-          tmem_store16(lanes + Y::kS + h, p_hi);
-          tmem_store16(lanes + Y::kS + h + 16, p_lo);
+          tmem_store16(lanes + Y::kS + 32 * h, p_hi);
+          tmem_store16(lanes + Y::kS + 32 * h + 16, p_lo);
         }
         tmem_wait_store();
         tc_fence_before();
