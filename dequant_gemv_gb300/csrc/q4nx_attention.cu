@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
   // the CTAs with a part of a unit: those whose shares begin where it may be cut, and the one before
   if (tid < 2 && edge[tid] >= 0) {
     const Cut& u = sm.cut[edge[tid]];
-    const int c0 = share_of(pl, u.cost + kUnitCost + kCutSteps - 1), c1 = share_of(pl, u.cost + kUnitCost + u.n - kCutSteps);
+    const int c0 = share_of(pl, u.cost + kUnitCost + cut_steps<RB> - 1), c1 = share_of(pl, u.cost + kUnitCost + u.n - cut_steps<RB>);
     // release: the CTA's parts, stored before the barrier, come first; acquire: the last one sees the others'
     uint32_t count;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(count) : "l"(a.counters + c0) : "memory");

@@ -9,7 +9,10 @@ namespace q4nx {
 
 constexpr float kRefNone = -3.0e38f;             // reference of a row that has seen nothing
 constexpr int kUnitCost = 4;                     // what a unit costs besides its steps, in steps
-constexpr int kCutSteps = 4;                     // a unit is cut between CTAs only this far from its ends
+// a unit is cut between CTAs only so many steps from its ends; a step of the
+// kernel for many rows takes 2 us, and up to so many come on top of a CTA's share
+template <int RB>
+constexpr int cut_steps = RB < 128 ? 4 : 2;
 constexpr int kMinCost = kUnitCost + 2;          // less is not worth a CTA
 
 // A unit that a CTA began and others ended, for the kernel that joins its parts.
@@ -172,7 +175,7 @@ __device__ int64_t bound(const AttnArgs& a, const Plan& pl, int c) {
   const int64_t x = q * c + (c < rest ? c : rest);
   const Unit u = find_unit<SB, RB>(a, pl, x, true);
   const int64_t in = x - u.cost - kUnitCost;
-  return u.start + (in < kCutSteps && in < u.n - kCutSteps + 1 ? 0 : in > u.n - kCutSteps ? u.n : in);
+  return u.start + (in < cut_steps<RB> && in < u.n - cut_steps<RB> + 1 ? 0 : in > u.n - cut_steps<RB> ? u.n : in);
 }
 // The CTA whose share of the costs holds x.
 __device__ __forceinline__ int share_of(const Plan& pl, int64_t x) {

@@ -363,6 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   __syncthreads();
   if (c.begin >= c.end) return;
   const int steps = static_cast<int>(c.end - c.begin);
+  Walk w;                                                        // the first piece, in code that all warps share
+  w.end = 0;
+  next_piece(a, pl, c, w, steps);
   if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem_base)), "r"(kTmemCols)
                  : "memory");
@@ -373,15 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   tc_fence_after();
   const uint32_t tmem = c.tmem_base;
 
-  Walk w;
-  w.end = 0;
   int j = 0;                                                     // steps taken: buffers and phases go by it
   if (warp < kWarpSoft0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   if (warp == kWarpLoad) {
     // ---- blocks of the cache into the raw ring; lane k < 4 copies a step's block k ----
     bool ok = true;
-    while (w.end < steps && ok) {
-      next_piece(a, pl, c, w, steps);
+    for (; ok; next_piece(a, pl, c, w, steps)) {
       for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int r = j % kRawStages;
         const uint8_t* src = nullptr;
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (src != nullptr) bulk_g2s(smem + Y::kRawAt + r * Y::kRaw + lane * kv_block_bytes(D), src, kv_block_bytes(D), &c.raw_full[r]);
         ++j;
       }
+      if (w.end >= steps) break;
     }
     for (int t = j > kRawStages ? j - kRawStages : 0; t < j; ++t)     // copies still under way land first
       mbar_wait_bounded(&c.raw_full[t % kRawStages], (t / kRawStages) & 1);
@@ -408,8 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     uint32_t begun = 0, pending = 0, open = 0;                       // a bit per tile: phases of q_ready and s_full; p v to come; S formed in this piece
     uint32_t turn = 0;
     bool ok = true;
-    while (w.end < steps && ok) {
-      next_piece(a, pl, c, w, steps);
+    for (; ok; next_piece(a, pl, c, w, steps)) {
       const Range r0 = range_of(w, span_of(a, w.u, 0, kTile)), r1 = range_of(w, span_of(a, w.u, kTile, kTile));
       uint32_t fresh = 0;                                            // nothing in O yet
       for (int n = w.r.lo; n <= w.r.hi && ok; ++n) {                 // and once more for the last p v
@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         }
       }
       open = 0;
+      if (w.end >= steps) break;
     }
     commit(&c.drain);                                                // every product issued so far has completed
     mbar_wait_bounded(&c.drain, 0, 100000000ull);
@@ -462,8 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
     const int d = warp - kWarpDecode0, blk = d >> 1, half = d & 1;
     bool ok = true;
-    while (w.end < steps && ok) {
-      next_piece(a, pl, c, w, steps);
+    for (; ok; next_piece(a, pl, c, w, steps)) {
       for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int b = j & 1, r = j % kRawStages;
         const int64_t t0 = (w.step0 + n) * kTok;
@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         }
         ++j;
       }
+      if (w.end >= steps) break;
     }
   } else if (warp >= kWarpSoft0) {
     // ---- softmax, four warps a tile: a thread is a row ----
@@ -493,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     int piece = 0;
     const float none = -__int_as_float(0x7f800000), c2 = a.scale_log2;
     bool ok = true;
-    while (w.end < steps && ok) {
-      next_piece(a, pl, c, w, steps);
+    for (; ok; next_piece(a, pl, c, w, steps)) {
       const int64_t x0 = c.begin + w.at, row0 = w.u.rg * kRows, left = w.u.rq.T * a.group - row0;
       const bool have = row < w.s.rows;                              // those that have none take the last, and keep nothing of it
       const int64_t r = row0 + (row < left ? row : left - 1), tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
@@ -644,8 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           }
         } else if (have) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<uint4*>(part + row * D + 32 * h + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 32; k += 4)                             // [D / 4][row][4]: a warp's rows side by side
+            *reinterpret_cast<uint4*>(part + ((8 * h + k / 4) * kRows + row) * 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
       tc_fence_before();
@@ -653,9 +653,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       if (have && !whole) *(reinterpret_cast<float2*>(part + kRows * D) + row) = make_float2(ref, l);
       if (!whole && first && row == 0) {
         // this CTA has the unit's first part: the others are those of the next CTAs up to the unit's end
-        const int c1 = share_of(pl, w.u.cost + kUnitCost + w.u.n - kCutSteps);
+        const int c1 = share_of(pl, w.u.cost + kUnitCost + w.u.n - cut_steps<kRows>);
         a.joined[blockIdx.x] = {w.u.rq.q0, w.u.rg * kRows, w.u.h, w.s.rows, c1 - static_cast<int>(blockIdx.x) + 1, 0};
       }
+      if (w.end >= steps) break;
     }
   }
   tc_fence_before();
@@ -665,46 +666,53 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-// The parts of units cut between CTAs: a warp per row, lanes along the channels.
+// The parts of units cut between CTAs: a thread per row and four channels, lanes
+// along the rows, as the parts lie.
 constexpr int kJoinWarps = 8;
 
 template <int D, typename Out>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgs a) {
-  constexpr int VPL = D / 32, kBatch = 12;
+  constexpr int kBatch = 10;
   constexpr int64_t kPitch = kRows * (D + 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Joined u = a.joined[blockIdx.x];
-  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int slot = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), r = slot % (kRows / 32) * 32 + (threadIdx.x & 31), c4 = slot / (kRows / 32);
   if (u.parts == 0 || r >= u.rows) return;
   auto part = [&](int c) { return a.partial + (2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * kPitch; };
-  float m = kRefNone, l = 0.f, o[VPL] = {};
-  for (int c = lane; c < u.parts; c += 32) m = fmaxf(m, __ldcg(part(c) + kRows * D + 2 * r));
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float m = kRefNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int c = 0; c < u.parts; c += kBatch) {
-    float2 ml[kBatch], v[kBatch][VPL / 2];
+    float2 ml[kBatch];
+    float4 v[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const float* from = part(c + k < u.parts ? c + k : c);
       ml[k] = __ldcg(reinterpret_cast<const float2*>(from + kRows * D) + r);
-#pragma unroll
-      for (int x = 0; x < VPL / 2; ++x) v[k][x] = __ldcg(reinterpret_cast<const float2*>(from + r * D + VPL * lane) + x);
+      v[k] = __ldcg(reinterpret_cast<const float4*>(from) + c4 * kRows + r);
     }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);           // a part taken twice changes no maximum
+    const float f0 = ex2(m - top);
+    m = top, l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (c + k < u.parts) {
         const float f = ex2(ml[k].x - m);
         l = fmaf(f, ml[k].y, l);
-#pragma unroll
-        for (int x = 0; x < VPL; ++x) o[x] = fmaf(f, x & 1 ? v[k][x / 2].y : v[k][x / 2].x, o[x]);
+        o.x = fmaf(f, v[k].x, o.x), o.y = fmaf(f, v[k].y, o.y), o.z = fmaf(f, v[k].z, o.z), o.w = fmaf(f, v[k].w, o.w);
       }
   }
   const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
   const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int x = 0; x < VPL; ++x) put<Out>(a, at * D + VPL * lane + x, l == 0.f ? 0.f : o[x] * inv);
-  if (lane == 0 && a.lse != nullptr) a.lse[at] = log_total(m, l);
+  if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (sizeof(Out) == 4)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + 4 * c4) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * c4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (c4 == 0 && a.lse != nullptr) a.lse[at] = log_total(m, l);
 }
 
 template <int D, typename Out>
@@ -725,7 +733,7 @@ cudaError_t launch_block_variant(const AttnArgs& a, int grid, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attention_block_kernel<D, Out>, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / kJoinWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 32 * (D / 4) / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, Out>, a);
