@@ -47,7 +47,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kManyRows = 64;                    // from so many query rows per request on, the tensor-core kernel
+// From so many query rows per request on, the tensor-core kernel.  It costs the same
+// up to 128 rows, this one a pass for each 16: one request of 16384 tokens, 8 kv
+// heads of 128 channels: 64 rows 47 (here) and 49 us (there), 68 rows 53 and 49,
+// 256 rows 115 and 57; 16 requests of 4096: 64 rows 119 and 137, 68 rows 143 and
+// 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125.
+constexpr int kManyRows = 65;
 // 16-token blocks of one step (a ring stage), and stages of a warp's ring
 __host__ __device__ constexpr int step_blocks(int D) { return D == 256 ? 1 : 2; }
 __host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 2 : 4; }

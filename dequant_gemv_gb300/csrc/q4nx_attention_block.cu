@@ -1,7 +1,7 @@
 // q4nx_attention_block.cu -- attention of many query rows (prompt blocks) over
 // the 4-bit cache, on the tcgen05 tensor cores.
 //
-//   S = q k^T (128 rows x 64 tokens),  p = exp2(S * scale * log2 e - ref),
+//   S = q k^T (256 rows x 64 tokens),  p = exp2(S * scale * log2 e - ref),
 //   O += p v,  l += sum p;  out = O / l
 // with one running reference per row, moved only when a logit passes it by 2^8.
 //
@@ -11,22 +11,32 @@
 // move the row's log-sum by more than binary32 does), and so does p:
 //   S = q k_hi + q k_lo          (q is bf16)
 //   O = p_hi v_hi + p_lo v_hi + p_hi v_lo
-// 28 tcgen05.mma (M = 128, K = 16) per 64 tokens at 128 channels, accumulated in
-// binary32 in TMEM.
+// 28 tcgen05.mma (M = 128, K = 16) per 128 rows and 64 tokens at 128 channels,
+// accumulated in binary32 in TMEM.
 //
-// Sixteen warps, one CTA per SM: a loader (bulk copies of the cache's blocks), the
-// MMA issuer, four softmax warps (a thread is a row: its logits come from TMEM, its
-// p go back there as the A operand of the second product) and eight decoding
-// warps (codes to bf16 pairs in shared memory, 128-byte swizzle: keys as rows of
-// channels, values as rows of tokens).  S, p, keys and values have two buffers:
-// the tensor cores form S of a step while the softmax warps work on the one before.
+// Twenty warps, one CTA per SM: a loader (bulk copies of the cache's blocks), the
+// MMA issuer, eight softmax warps (a thread is a row: its logits come from TMEM,
+// its p take their place there, as the A operand of the second product) and eight
+// decoding warps (codes to bf16 pairs in shared memory, 128-byte swizzle: keys as
+// rows of channels, values as rows of tokens; two buffers each).  A unit is two
+// tiles of 128 rows that share what is decoded: while the softmax of one is under
+// way, the products of the other are.  With one tile per CTA (S in two buffers)
+// decoding was half the work: 70 us instead of 52 for 64 tokens x 32 heads over
+// 16384 positions, 8 kv heads of 128 channels, 40 us of it in the loop (14 steps).
 //
-// Bound: instruction issue of the decoding and softmax warps (about 5500 per
-// 64 tokens x 128 rows, 2200 cycles against 1350 of the products).
+// Bound: the turns that a tile takes in a step of 2.1 us: softmax 1.0, the issue and
+// run of its products 0.9, the hand-over 0.2.  The products alone need 1.1 us for
+// both tiles (tensor pipe 37% busy), and the warps issue 0.6 instructions a cycle
+// and scheduler, so that neither is full: the next thing would be S in two buffers
+// beside two tiles, for which TMEM (512 columns) has no room with q in it.  The
+// start takes 8.6 us: plan, the first blocks' arrival, cold code.
+// What else was tried: two issuing warps, one for each tile: they fall into step
+// and leave the tensor cores idle together, 58 us instead of 52; the keys' wait
+// before the weights': 53; both products as rolled loops: 55.
 //
 // A CTA's steps (64 tokens) are a range of all units' steps; a unit cut between
 // CTAs leaves its parts in the workspace, with a record of whose they are, for
-// a second kernel that joins them over the whole GPU (a part is 64 KB).
+// a second kernel that joins them over the whole GPU (a part is 128 KB).
 #include <cuda_fp16.h>
 
 #include "q4nx_attention.cuh"
@@ -543,6 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         __syncwarp();
         if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err))) break;
         tc_fence_after();
+        // the row's 64 logits stay in registers between maximum and weights: read again
+        // for the second pass they cost 64.5 us instead of 62
         uint32_t x[2][32];
         tmem_load(lanes + Y::kS, x[0]);
         tmem_load(lanes + Y::kS + 32, x[1]);

@@ -319,6 +319,84 @@ def test_attention_nan_stays_where_it_is_seen(q):
     assert np.isfinite(got[:3]).all() and np.isfinite(got[3, :, :32]).all() and np.isnan(got[3, :, 32:]).all()
 
 
+# Many rows per request (more than 64 on average, 64 or 128 channels) go to a kernel
+# of 256-row units of two tiles, on the tensor cores; 256 channels stay where they are.
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,new,window", [(4, 100, 0), (3, 50, 0), (1, 129, 70), (3, 100, 70), (16, 33, 1), (5, 60, 64), (1, 300, 257)])
+def test_attention_many_rows(q, dim, group, new, window):
+    lens = [new, new + 1, max(1, new - 30), 333, 1025]     # the third has rows before its first position
+    c = Case(q, lens, [new] * len(lens), 2, dim, 48, seed=new + group).fill().append_new()
+    for dt in ("f32", "bf16"):
+        qx, out, lse, scale = attend(c, 2 * group, window=window, out_dtype=dt)
+        check(c, qx, out, lse, scale, window, 2 * group)
+
+
+def test_attention_many_rows_of_some_requests(q):
+    # the average decides: requests of 600 rows, of one token, of none, and an empty cache
+    c = Case(q, [40, 0, 3, 9000, 1, 700], [0, 2, 7, 3, 1, 300], 2, 128, 64).fill().append_new()
+    qx, out, lse, scale = attend(c, 4)
+    check(c, qx, out, lse, scale, 0, 4)
+    again = attend(Same(c, qx), 4)
+    assert torch.equal(out, again[1]) and torch.equal(lse, again[2])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_many_rows_nan_stays_where_it_is_seen(q, dim):
+    c = Case(q, [400, 90], [200, 70], 1, dim, 16)
+    c.k[0][300, 0, 3] = np.nan                            # seen by the tokens from position 300 on
+    c.v[0][260, 0, 40] = np.inf                           # from position 260 on, in one group
+    c.fill().append_new()
+    qx, out, lse, scale = attend(c, 2)
+    got, l = out.cpu().numpy(), lse.cpu().numpy()
+    assert np.isfinite(l[:100]).all() and np.isnan(l[100:200]).all() and np.isnan(got[100:200]).all()
+    assert np.isfinite(got[:60]).all() and np.isfinite(got[200:]).all() and np.isfinite(l[200:]).all()
+    assert np.isfinite(got[60:100, :, :32]).all() and np.isnan(got[60:100, :, 32:64]).all() and np.isfinite(got[60:100, :, 64:]).all()
+    # a window past them: those rows are finite again, and right
+    qx, out, lse, scale = attend(c, 2, window=20)
+    got = out.cpu().numpy()
+    assert np.isfinite(got[120:]).all() and np.isfinite(got[80:100]).all() and np.isfinite(lse.cpu().numpy()[120:]).all()
+
+
+def test_attention_many_rows_sharp_and_scaled_values(q):
+    c = Case(q, [700, 90], [130, 70], 2, 128, 64)
+    for b in range(2):
+        f = np.exp2(c.rng.integers(-20, 21, size=(c.lens[b], c.kv, 1))).astype(np.float32)
+        c.v[b] = _bf16(c.v[b] * f)
+        c.k[b] = _bf16(c.k[b] * np.exp2(c.rng.integers(-3, 3, size=(c.lens[b], c.kv, 1))).astype(np.float32))
+    c.fill().append_new()
+    for scale in (0.5, -0.3, 1e-3, 0.0):
+        qx, out, lse, scale = attend(c, 4, scale=scale)
+        y, l, A = exact(c, qx, scale, 0, 4)
+        # as for few rows; a key is kept to 2^-17 of itself
+        got = out.float().cpu().numpy().astype(np.float64)
+        big = abs(scale) * max(np.abs(qx).sum(-1).max() * np.abs(np.concatenate(c.k)).max(), 1.0)
+        tol = (2.0 ** -11 + 2.0 ** -13 + 2 * 2.0 ** -16 * big) * A
+        assert np.all(np.abs(got - y) <= tol)
+        assert np.all(np.abs(lse.cpu().numpy() - l) <= 2.0 ** -13 + 2.0 ** -16 * big)
+
+
+def test_attention_many_rows_in_a_graph_and_bad_indexes(q):
+    c = Case(q, [300, 200], [80, 90], 2, 128, 64).fill().append_new()
+    qx, out, lse, scale = attend(c, 4)
+    qt, out2 = dev(qx), torch.zeros_like(out)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.q4nx_kv_attention(c.cache, qt, c.start, c.tlens, c.table, out=out2, out_dtype="f32", ws=ws)
+    for _ in range(3):
+        g.replay()
+    assert torch.equal(out, out2)
+    for i, x in (((0, 1), 10 ** 6), ((1, 0), -1)):
+        table = c.table.clone()
+        table[i] = x
+        q.q4nx_kv_attention(c.cache, qt, c.start, c.tlens, table, ws=ws)
+        with pytest.raises(q.Q4NXError) as e:
+            q.q4nx_check(ws)
+        assert e.value.status == q.Q4NX_E_INDEX
+    g.replay()
+    assert torch.equal(out, out2)
+
+
 def test_attention_on_another_stream_and_in_a_graph(q):
     c = Case(q, [300, 20], [1, 1], 2, 128, 64).fill().append_new()
     qx, out, lse, scale = attend(c, 4)
