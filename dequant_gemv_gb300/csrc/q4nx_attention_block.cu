@@ -22,7 +22,7 @@
 // tiles of 128 rows that share what is decoded: while the softmax of one is under
 // way, the products of the other are.  With one tile per CTA (S in two buffers)
 // decoding was half the work: 70 us instead of 52 for 64 tokens x 32 heads over
-// 16384 positions, 8 kv heads of 128 channels, 40 us of it in the loop (14 steps).
+// 16384 positions, 8 kv heads of 128 channels, 30 us of it in the loop (14 steps).
 //
 // Bound: the turns that a tile takes in a step of 2.1 us: softmax 1.0, the issue and
 // run of its products 0.9, the hand-over 0.2.  The products alone need 1.1 us for

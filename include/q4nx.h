@@ -296,8 +296,10 @@ int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k
  * A row that sees nothing (a position below 0) gives zeros and -Inf.  NaN and
  * infinities in positions that a row does not see do not reach it.  Rows of
  * tokens of no request are not written.
- * Accuracy: the cached values enter exactly, sums are binary32; each weight
- * p_j times a value scale is rounded to fp16 (2^-12 of itself).
+ * Accuracy: sums are binary32.  Up to 64 query rows (tokens x heads per kv head)
+ * per request on average, and at 256 channels, the cached values enter exactly
+ * and each weight p_j times a value scale is rounded to fp16 (2^-11 of itself);
+ * above, cached values and weights enter as pairs of bf16 (2^-17 of themselves).
  * Deterministic: partial sums are joined in a fixed order. */
 int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
                       int heads, float scale, int64_t window, void* out_dev, int out_dtype, float* lse_dev,
