@@ -11,8 +11,8 @@
 // Two append kernels: few tokens per request take a warp per (token, kv head),
 // all lanes on one token's channels; prompts take a warp per (16-token block,
 // kv head, keys or values, 64 channels), which owns them during the launch and writes whole
-// sectors (a token's value codes are one byte in each of 64 words: 3350 tokens of
-// 8 heads by the first kernel 19.5 us, by the second 13.4).  Bound: bytes (4 in, 0.625
+// sectors (a token's value codes are one byte in each of 64 words: 3351 tokens of
+// 8 heads by the first kernel 16.1 us, by the second 10.7).  Bound: bytes (4 in, 0.625
 // out per value), and the quantisation's arithmetic close behind.
 #include "q4nx_kernels.h"
 #include "q4nx_kv.cuh"
@@ -22,6 +22,7 @@ namespace q4nx {
 namespace {
 
 constexpr int kKvWarps = 8;      // warps per CTA of the append and read kernels
+constexpr int64_t kFullItems = 6144;   // (token, head) pairs from which on larger items pay: below, too few warps have work
 
 // clamp(rint((x - m) / s), -8, 7) + 8 with the quotient correctly rounded; `inv` is
 // about 1 / s.  The product with it is within 2^-21 of the quotient, relative,
@@ -320,8 +321,12 @@ cudaError_t launch(void (*f)(P...), unsigned grid, unsigned block, size_t smem, 
 
 cudaError_t launch_kv_append(int D, const KvPool& p, const KvBatch& kb, const void* k, const void* v, int64_t stride,
                              uint32_t* err, cudaStream_t s) {
-  // prompts (8 tokens per request and more on average) by blocks: a request's tokens lie in T/16 + 2 at most
-  const bool blocks = kb.tokens >= static_cast<int64_t>(8) * kb.batch;
+  // Prompts (64 tokens per request and more on average) by blocks, where there are
+  // enough of them to fill the GPU: a warp has 16 times the work.  8 heads of 128, by
+  // tokens and by blocks: 1 x 512 tokens 4.0 and 4.5 us, 16 x 64 6.2 and 6.3, 1 x 1024
+  // 6.5 and 5.4, 16 x 128 10.5 and 7.7, 1 x 4096 18.7 and 12.0; 2 heads of 64, 3 x 1117: 4.8 and 4.3.
+  // A request's tokens lie in T/16 + 2 blocks at most.
+  const bool blocks = kb.tokens >= static_cast<int64_t>(64) * kb.batch && kb.tokens * p.kv_heads >= kFullItems;
   const int64_t items = (blocks ? (kb.tokens / kKvBlock + 2 * kb.batch) * (D / 32) : kb.tokens) * p.kv_heads;
   const int64_t grid = (items + kKvWarps - 1) / kKvWarps;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
@@ -357,7 +362,9 @@ cudaError_t launch_read(const KvPool& p, const KvBatch& kb, void* k, void* v, in
 
 cudaError_t launch_kv_read(int D, const KvPool& p, const KvBatch& kb, void* k, void* v, int out_f32, uint32_t* err,
                            cudaStream_t s) {
-  const bool four = kb.tokens * p.kv_heads >= 8192;
+  // four heads a warp share the look-ups where there are enough: 8 heads of 128, one and
+  // four: 512 tokens 3.0 and 3.2 us, 1024 4.2 and 3.5, 4096 12.2 and 8.2
+  const bool four = kb.tokens * p.kv_heads >= kFullItems;
   switch (D) {
     case 64: return four ? launch_read<64, 4>(p, kb, k, v, out_f32, err, s) : launch_read<64, 1>(p, kb, k, v, out_f32, err, s);
     case 128: return four ? launch_read<128, 4>(p, kb, k, v, out_f32, err, s) : launch_read<128, 1>(p, kb, k, v, out_f32, err, s);

@@ -9,9 +9,10 @@
 // keeps the entropy free of cancellation).
 //
 // Top alternatives without a second pass over memory: the j-th largest of a
-// warp's 32 thread maxima, j = ceil(top / warps), is reached by at least j
-// elements of that warp, so the smallest such value over the warps is a floor
-// for the CTA's top elements.  Only threads whose own maximum reaches the
+// warp's 32 thread maxima is reached by at least j elements of that warp, so the
+// smallest such value over W warps, j = ceil(top / W), is a floor for the CTA's
+// top elements.  W counts the warps whose threads have elements (of the last one at
+// least half): a floor made by a nearly empty warp lets everything through.  Only threads whose own maximum reaches the
 // floor have their elements read again (from L2, by their whole warp; one thread in
 // ten), and the elements at or above it, about a hundred, get their ranks by
 // counting.  Rows with
@@ -197,9 +198,12 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
     const int64_t tok = a.tokens[m];
     if (tok >= 0 && tok < a.V) given = row.at(tok);
   }
+  const int live = static_cast<int>(v1 - v0 < kThreads ? v1 - v0 : kThreads), full = live / 32;
+  const bool part = live % 32 >= 16 && live % 32 >= (a.top + full) / (full + 1);
+  const int used = part ? full + 1 : full;             // 0: every element is a candidate, some hundred at most
   if (a.top > 0) {
     uint32_t left = mine, kth = 0;
-    for (int j = 0; j < (a.top + kWarps - 1) / kWarps; ++j) {
+    for (int j = 0; used > 0 && j < (a.top + used - 1) / used; ++j) {
       kth = __reduce_max_sync(0xffffffffu, left);
       const uint32_t who = __ballot_sync(0xffffffffu, left == kth);
       if (lane == __ffs(who) - 1) left = 0;
@@ -210,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
   if (tid < kMaxTop) best[tid] = 0;
   __syncthreads();
   if (a.top > 0) {
-    uint32_t floor = 0xFFFFFFFFu;
+    uint32_t floor = used > 0 ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) floor = min(floor, floor_of[w]);
+    for (int w = 0; w < kWarps; ++w) floor = min(floor, w < used ? floor_of[w] : floor);
     // A warp goes through its lanes that reach the floor, kSources at a time: the
     // 32 lanes load one's elements together.
     constexpr int kSources = 4;
@@ -226,6 +230,14 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
     };
     uint32_t reach = __ballot_sync(0xffffffffu, any && mine >= floor);
     if (any && mine >= floor && end_elem >= 0) offer(row.at(end_elem), end_elem);
+    if (live < kThreads) {                             // a load each: by the lanes themselves (60 rows of 15456 bf16, top 32: 10 instead of 62 us)
+      if (reach >> lane & 1 && tid < live) {
+        const uint4 u = row.load(v0 + tid);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) offer(Row<BF16>::pick(u, e), row.head + (v0 + tid) * VE + e);
+      }
+      reach = 0;
+    }
 #pragma unroll 1
     while (reach != 0) {
       uint32_t some = reach;
@@ -346,9 +358,11 @@ cudaError_t launch_logprobs(const LogprobsCall& c, const DeviceInfo& info, cudaS
   a.top_idx = c.top_idx;
   a.top_lp = c.top_lp;
   a.top = c.top;
-  // as many CTAs a row as keep all rows' CTAs (two per SM) on the GPU at once
+  // As many CTAs a row as keep all rows' CTAs (two per SM) on the GPU at once (cold L2): 64 rows
+  // of 151936 by 4 CTAs each 22, by 8 31, by 1 29 us; one row by 8 14, by 1 25.  The
+  // last places take no whole cluster of 4 or 8: 38 rows by 8 19 us, by 4 14; 76 by 4 20, by 2 15.5.
   int cluster = kMaxCluster;
-  while (cluster > 1 && static_cast<int64_t>(c.M) * cluster > 2 * info.sms) cluster /= 2;
+  while (cluster > 1 && static_cast<int64_t>(c.M) * cluster > 2 * info.sms - (cluster > 2 ? 2 * cluster : 0)) cluster /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(c.M));
   cfg.blockDim = dim3(kThreads);

@@ -79,6 +79,15 @@ def test_matches(q, dtype, M, V):
             check(q, t, [int(i) for i in rng.integers(0, V, M)], top)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [30 * 4, 33 * 8, 65 * 4, 483 * 8, 481 * 16, 514 * 4, 496 * 32])
+def test_rows_that_fill_the_last_warps_in_part(q, V, dtype):
+    for M in (1, 60, 320):
+        t = draw(M, V, dtype, seed=3)
+        for top in (17, 32):
+            check(q, t, [(7 * m) % V for m in range(M)], top)
+
+
 @pytest.mark.parametrize("M", [1, 5, 100, 400])
 def test_ties_and_masked_entries(q, M):
     g = torch.Generator(device=DEV).manual_seed(M)
