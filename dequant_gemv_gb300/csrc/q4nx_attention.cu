@@ -91,6 +91,7 @@ struct Smem {
   float2 ml[2 * kWarps][RB];
   float2 total[2 * kWarps][RB];                       // those of the CTA's parts of the unit together
   int64_t prefix[kKvMaxBatch + 1], cost[kKvMaxBatch + 1];
+  int longest[32];
   int64_t begin, end;
   int stopped, joins[2];
 };
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
   if (tid == 0) sm.stopped = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const Plan pl = make_plan<step_blocks(D), RB>(a, sm.prefix, sm.cost);
+  const Plan pl = make_plan<step_blocks(D), RB>(a, sm.prefix, sm.cost, sm.longest);
   if (pl.total == 0 || blockIdx.x >= pl.ctas) return;
   if (tid < 2) (tid ? sm.end : sm.begin) = bound<step_blocks(D), RB>(a, pl, blockIdx.x + tid);
   __syncthreads();

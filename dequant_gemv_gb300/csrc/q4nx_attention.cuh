@@ -13,7 +13,15 @@ constexpr int kUnitCost = 4;                     // what a unit costs besides it
 // kernel for many rows takes 2 us, and up to so many come on top of a CTA's share
 template <int RB>
 constexpr int cut_steps = RB < 128 ? 4 : 2;
-constexpr int kMinCost = kUnitCost + 2;          // less is not worth a CTA
+// A CTA's least share.  The parts of a unit are joined by one CTA (few rows), so that a
+// unit of n steps is cut into 1.7 sqrt(n) parts at most, where joining takes as long as
+// they do: one request of 51015 tokens, one kv head of 128 channels (n = 1594) by 266
+// CTAs 31 us, by 80 20, by 40 21; 2 kv heads of 32768 by 304 26, by 103 19, by 51 22.
+constexpr int kMinCost = kUnitCost + 2;
+__device__ __forceinline__ int least_share(int longest) {
+  const int x = static_cast<int>(0.6f * sqrtf(static_cast<float>(longest)));
+  return x > kMinCost ? x : kMinCost;
+}
 
 // A unit that a CTA began and others ended, for the kernel that joins its parts.
 struct Joined {
@@ -198,19 +206,25 @@ __device__ __forceinline__ float log_total(float m, float l) {
 }
 
 // The plan of the call's units, by all threads of a CTA: prefix and cost are
-// [batch + 1] in shared memory.
+// [batch + 1] and longest is [32] in shared memory.
 template <int SB, int RB>
-__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, int64_t* cost) {
+__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, int64_t* cost, int* longest) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) prefix[0] = cost[0] = 0;
   // the requests' steps and costs, and their prefix sums
   const int B = a.kb.batch;
+  int most = 0;
   for (int b = tid; b < B; b += blockDim.x) {
     const KvRequest rq = kv_request(a.kb, a.pool.page_blocks, b);
     if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
     const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(rq, a.window);
     prefix[b + 1] = units * n;
     cost[b + 1] = units * (n + kUnitCost);
+    if (units > 0) most = max(most, static_cast<int>(n < (1 << 30) ? n : 1 << 30));
+  }
+  if constexpr (RB < 128) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) longest[warp] = most;
   }
   __syncthreads();
   if (warp < 2) {
@@ -233,7 +247,8 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, in
   pl.cost = cost;
   pl.batch = B;
   pl.total = cost[B];
-  const int64_t want = pl.total / kMinCost;
+  int64_t want = pl.total / kMinCost;
+  if constexpr (RB < 128) want = quot(pl.total, least_share(__reduce_max_sync(0xffffffffu, lane < blockDim.x / 32 ? longest[lane] : 0)));
   pl.ctas = want < 1 ? 1 : want < gridDim.x ? static_cast<int>(want) : gridDim.x;
   return pl;
 }

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) a.joined[blockIdx.x].parts = 0;
-  const Plan pl = make_plan<kSB, kRows>(a, c.prefix, c.cost);
+  const Plan pl = make_plan<kSB, kRows>(a, c.prefix, c.cost, nullptr);
   if (pl.total == 0 || blockIdx.x >= pl.ctas) return;
   if (tid < 2) (tid ? c.end : c.begin) = bound<kSB, kRows>(a, pl, blockIdx.x + tid);
   __syncthreads();
