@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_blocks_kernel(KvPool 
 
 // One warp per (token, HEADS kv heads), which share its look-ups; lane l writes
 // channels VPL*l ..  Four heads a warp where that still leaves warps for all SMs
-// (3349 tokens of 8 heads: 10 us, 13 with one), one where latency counts (48 tokens: 5 us, 7 with four).
+// (3351 tokens of 8 heads: 7.1 us, 10.5 with one), one where latency counts (16 tokens: 2.1 us, 3.0 with four).
 template <int D, int HEADS, typename Out>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_read_kernel(KvPool pool, KvBatch kb, Out* __restrict__ ko,
                                                                Out* __restrict__ vo, uint32_t* err) {
