@@ -890,7 +890,7 @@ cudaError_t launch_attention(int D, const KvPool& pool, const KvBatch& kb, const
   a.heads = heads;
   a.group = heads / pool.kv_heads;
   a.scale_log2 = scale * 1.44269504088896f;
-  a.window = window;
+  a.window = window > INT32_MAX ? 0 : window;          // positions have 31 bits: it hides nothing, and differences with it stay in 64
   a.out = out;
   a.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

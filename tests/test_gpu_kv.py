@@ -245,6 +245,16 @@ def test_attention_window(q, dim, window, new):
     check(c, qx, out, lse, scale, window, 6)
 
 
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 63 - 1])
+@pytest.mark.parametrize("new", [9, 100])
+def test_attention_window_beyond_every_length(q, window, new):
+    # a window that hides nothing, rows before the first position among them
+    c = Case(q, [1, 3, 500], [new, new, new], 2, 128, 16, seed=new).fill().append_new()
+    qx, out, lse, scale = attend(c, 8, window=window)
+    check(c, qx, out, lse, scale, 0, 8)
+    q.q4nx_check(device=DEV)
+
+
 def test_attention_mixed_empty_and_short_requests(q):
     # no tokens in the call; an empty cache; rows before the first position; one long split request
     c = Case(q, [40, 0, 3, 9000, 1, 64], [0, 2, 7, 3, 1, 64], 2, 128, 64).fill().append_new()
