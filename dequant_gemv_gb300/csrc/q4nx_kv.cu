@@ -56,7 +56,10 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(KvPool pool, K
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kKvWarps + warp;
   const int64_t tok = item / pool.kv_heads;
   const int h = static_cast<int>(item - tok * pool.kv_heads);
-  if (tok >= kb.tokens) return;
+  if (tok >= kb.tokens) {
+    if (tok == kb.tokens && h == 0) kv_report(kb, pool.page_blocks, err);
+    return;
+  }
   uint32_t raw[2][VPL / 2];                                     // the values, ahead of the look-ups
 #pragma unroll
   for (int which = 0; which < 2; ++which)
@@ -131,6 +134,9 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(KvPool pool, K
   }
 }
 
+// A request's tokens lie in T/16 + 2 blocks at most.
+__host__ __device__ __forceinline__ int64_t most_blocks(const KvBatch& kb) { return kb.tokens / kKvBlock + 2 * kb.batch; }
+
 // One warp per (16-token block that the call writes, kv head, keys or values,
 // pair of groups): lane 2t + e holds one group of token t, so that no lane
 // needs another's extremes.  Keys' words are stored as they come; values' bytes, 512
@@ -147,12 +153,15 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_blocks_kernel(KvPool 
   const int which = static_cast<int>(item % NG) / (NG / 2), pair = static_cast<int>(item % (NG / 2));
   int64_t left = item / NG / pool.kv_heads;                     // the call's block, counted over its requests
   const int h = static_cast<int>(item / NG - left * pool.kv_heads);
+  if (left >= most_blocks(kb)) {
+    if (left == most_blocks(kb) && item % (NG * pool.kv_heads) == 0) kv_report(kb, pool.page_blocks, err);
+    return;
+  }
   // the request: 32 at a time, their block counts added up across the lanes
   int b = -1;
   KvRequest rq = {};
   for (int b0 = 0; b0 < kb.batch && b < 0; b0 += 32) {
     const KvRequest r = b0 + lane < kb.batch ? kv_request(kb, pool.page_blocks, b0 + lane) : KvRequest{0, 0, 0, true};
-    if (!r.ok && item == 0) atomicOr(err, kErrIndex);
     const int64_t from = r.L > r.T ? r.L - r.T : 0;             // tokens at positions below 0 are not kept
     const int64_t n = r.T > 0 && r.L > from ? (r.L - 1) / kKvBlock - from / kKvBlock + 1 : 0;
     int64_t end = n;
@@ -254,7 +263,10 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_read_kernel(KvPool pool, KvB
   const int quads = (pool.kv_heads + HEADS - 1) / HEADS;
   const int64_t tok = item / quads;
   const int h0 = static_cast<int>(item - tok * quads) * HEADS;
-  if (tok >= kb.tokens) return;
+  if (tok >= kb.tokens) {
+    if (tok == kb.tokens && h0 == 0) kv_report(kb, pool.page_blocks, err);
+    return;
+  }
   int b;
   const KvRequest rq = kv_locate(kb, pool.page_blocks, tok, b);
   const uint8_t* blk0 = nullptr;                                // of head h0
@@ -325,10 +337,9 @@ cudaError_t launch_kv_append(int D, const KvPool& p, const KvBatch& kb, const vo
   // enough of them to fill the GPU: a warp has 16 times the work.  8 heads of 128, by
   // tokens and by blocks: 1 x 512 tokens 4.0 and 4.5 us, 16 x 64 6.2 and 6.3, 1 x 1024
   // 6.5 and 5.4, 16 x 128 10.5 and 7.7, 1 x 4096 18.7 and 12.0; 2 heads of 64, 3 x 1117: 4.8 and 4.3.
-  // A request's tokens lie in T/16 + 2 blocks at most.
   const bool blocks = kb.tokens >= static_cast<int64_t>(64) * kb.batch && kb.tokens * p.kv_heads >= kFullItems;
-  const int64_t items = (blocks ? (kb.tokens / kKvBlock + 2 * kb.batch) * (D / 32) : kb.tokens) * p.kv_heads;
-  const int64_t grid = (items + kKvWarps - 1) / kKvWarps;
+  const int64_t items = (blocks ? most_blocks(kb) * (D / 32) : kb.tokens) * p.kv_heads;
+  const int64_t grid = items / kKvWarps + 1;              // and a warp that reports what is out of range
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const uint16_t *kk = static_cast<const uint16_t*>(k), *vv = static_cast<const uint16_t*>(v);
   const unsigned g = static_cast<unsigned>(grid), n = kKvWarps * 32;
@@ -350,7 +361,7 @@ namespace {
 
 template <int D, int HEADS>
 cudaError_t launch_read(const KvPool& p, const KvBatch& kb, void* k, void* v, int out_f32, uint32_t* err, cudaStream_t s) {
-  const int64_t grid = (kb.tokens * ((p.kv_heads + HEADS - 1) / HEADS) + kKvWarps - 1) / kKvWarps;
+  const int64_t grid = kb.tokens * ((p.kv_heads + HEADS - 1) / HEADS) / kKvWarps + 1;      // and a warp that reports
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(grid), n = kKvWarps * 32;
   return out_f32 ? launch(kv_read_kernel<D, HEADS, float>, g, n, 0, s, p, kb, static_cast<float*>(k), static_cast<float*>(v), err)

@@ -74,6 +74,14 @@ __device__ __forceinline__ KvRequest kv_request(const KvBatch& kb, int page_bloc
   return kv_checked(kb, page_blocks, kb.q_start[b], kb.q_start[b + 1], kb.lens[b]);
 }
 
+// Reports the requests that kv_checked refuses; by a whole warp.  Many of them have
+// no tokens that a warp of the append or read kernels would come by, so that a warp
+// beyond those with work looks at all of them.
+__device__ __forceinline__ void kv_report(const KvBatch& kb, int page_blocks, uint32_t* err) {
+  for (int b = threadIdx.x & 31; b < kb.batch; b += 32)
+    if (!kv_request(kb, page_blocks, b).ok) atomicOr(err, kErrIndex);
+}
+
 // Block `blk` (16 positions) of request b and kv head h, or NULL where the
 // table names no page of the pool.
 __device__ __forceinline__ uint8_t* kv_block_ptr(const KvPool& p, const KvBatch& kb, int D, int b, int h, int64_t blk) {

@@ -475,6 +475,30 @@ def test_bad_indexes_are_reported_and_the_workspace_stays_usable(q):
     assert torch.equal(out, good)
 
 
+@pytest.mark.parametrize("lens,new,kv", [([40, 30, 20], [1, 1, 0], 2), ([80] * 39, [80] * 38 + [0], 4)])
+def test_bad_requests_without_tokens_are_reported(q, lens, new, kv):
+    # a range out of order, a length of a request that has no tokens, in the first
+    # 32 requests and beyond: append (by tokens, by blocks) and read report them and serve the others
+    c = Case(q, lens, new, kv, 64, 16).fill().append_new()
+    want = q.q4nx_kv_read(c.cache, c.tokens, c.start, c.tlens, c.table, out_dtype="f32")
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+    k, v = (dev(np.concatenate([x[n - t:] for x, n, t in zip(xs, lens, new)])) for xs in (c.k, c.v))
+    for name, x in (("start", -1), ("start", 0), ("lens", -1), ("lens", 10 ** 6)):
+        t = {"start": c.start.clone(), "lens": c.tlens.clone()}
+        t[name][-1] = x
+        c.cache.pool.fill_(0xFF)
+        c.fill()
+        for call in ("append", "read"):
+            if call == "append":
+                q.q4nx_kv_append(c.cache, k, v, t["start"], t["lens"], c.table, ws=ws)
+            else:
+                got = q.q4nx_kv_read(c.cache, c.tokens, t["start"], t["lens"], c.table, out_dtype="f32", ws=ws)
+            with pytest.raises(q.Q4NXError) as e:
+                q.q4nx_check(ws)
+            assert e.value.status == q.Q4NX_E_INDEX, (call, name, x)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_binding_refuses(q):
     c = Case(q, [40], [1], 2, 64, 16)
     x = dev(c.draw(1))
