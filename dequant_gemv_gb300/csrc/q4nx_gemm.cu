@@ -149,6 +149,7 @@ struct Args {
   int tiles, M, out_f32, grid;
   int mrows;                // X box rows: M rounded up to 8
   int64_t units;            // tiles * TC
+  int after_wait;           // the next launch may start once the previous grids are done, not before
 };
 
 // --------------------------------------------------------------- PTX ----
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t KS = a.TC;
   const int64_t first_tile = lo / KS, last_tile = (hi - 1) / KS;
   const int ntiles = static_cast<int>(last_tile - first_tile + 1);
-  asm volatile("griddepcontrol.launch_dependents;");
+  if (!a.after_wait) asm volatile("griddepcontrol.launch_dependents;");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWStages; ++s) { mbar_init(&sh->w_full[s], 1); mbar_init(&sh->w_empty[s], kDequantWarps); }
@@ -507,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpX) {
     // ----------------------------------------------------------- X
     asm volatile("griddepcontrol.wait;" ::: "memory");     // X may be the previous grid's output
+    if (a.after_wait) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int64_t ks = lo % KS;
     int j = 0;
     for (; j < n; ++j) {
@@ -855,7 +857,7 @@ uint64_t gemm_workspace_bytes(int64_t TR, int64_t TC, int M) {
 namespace {
 template <int KIND>
 cudaError_t launch_gemm_kind(EncodeTiled enc, const DeviceInfo& info, const void* chunks, int64_t TR, int64_t TC,
-                             const void* X, int M, void* Y, int out_f32, void* workspace, cudaStream_t s) {
+                             const void* X, int M, void* Y, int out_f32, void* workspace, cudaStream_t s, bool after_wait) {
   using P = gemm::Plan<KIND>;
   if (info.max_smem_optin < P::kSmemBytes) return cudaErrorNotSupported;
   // weights, q4_1: code regions as [128 B][32 rows][TC chunk columns][TR tile rows] (128-byte swizzle)
@@ -934,6 +936,7 @@ cudaError_t launch_gemm_kind(EncodeTiled enc, const DeviceInfo& info, const void
   a.mrows = (M + 7) & ~7;
   a.out_f32 = out_f32;
   a.units = tiles * TC;
+  a.after_wait = after_wait;
   // at least 4 k-steps per CTA where the work allows it, at most one CTA per SM
   int64_t grid = (a.units + 3) / 4;
   if (grid > info.sms) grid = info.sms;
@@ -973,7 +976,7 @@ cudaError_t launch_gemm_kind(EncodeTiled enc, const DeviceInfo& info, const void
 }  // namespace
 
 cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, const void* X, int M, void* Y,
-                        int out_f32, void* workspace, cudaStream_t s) {
+                        int out_f32, void* workspace, cudaStream_t s, bool after_wait) {
   if (!gemm_supports(kind)) return cudaErrorNotSupported;
   EncodeTiled enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
@@ -981,9 +984,9 @@ cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, co
   cudaError_t e = device_info(&info);
   if (e != cudaSuccess) return e;
   switch (kind) {
-    case kQ4_1: return launch_gemm_kind<kQ4_1>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s);
-    case kQ8_KR: return launch_gemm_kind<kQ8_KR>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s);
-    default: return launch_gemm_kind<kQ8_BLK>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s);
+    case kQ4_1: return launch_gemm_kind<kQ4_1>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait);
+    case kQ8_KR: return launch_gemm_kind<kQ8_KR>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait);
+    default: return launch_gemm_kind<kQ8_BLK>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait);
   }
 }
 

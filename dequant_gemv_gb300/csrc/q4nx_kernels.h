@@ -78,8 +78,9 @@ cudaError_t launch_argmax(const float* logits, int M, int64_t V, int32_t* idx, c
 // ---- GEMM (M <= 64, tcgen05) ----
 bool gemm_supports(int kind);
 uint64_t gemm_workspace_bytes(int64_t TR, int64_t TC, int M);
+// after_wait: a dependent launch that starts early finds what the grids before the GEMM wrote
 cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, const void* X, int M, void* Y,
-                        int out_f32, void* workspace, cudaStream_t s);
+                        int out_f32, void* workspace, cudaStream_t s, bool after_wait = false);
 
 // ---- 4-bit key/value cache and the attention that reads it (q4nx_kv.cuh) ----
 struct KvPool;
@@ -108,7 +109,8 @@ struct LoraCall {
   int M, R, count;
 };
 int lora_splits(int64_t K);     // parts into which shrink cuts the columns
-cudaError_t launch_lora_shrink(const LoraCall& c, const DeviceInfo& info, cudaStream_t s);
+// beside: behind the launch of the product (after_wait), while that runs
+cudaError_t launch_lora_shrink(const LoraCall& c, const DeviceInfo& info, bool beside, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraCall& c, int out_f32, cudaStream_t s);
 
 // ---- log-probabilities ----

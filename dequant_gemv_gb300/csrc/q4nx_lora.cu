@@ -5,6 +5,14 @@
 // and rounds once.  Both are bound by the adapters' bytes when the requests use many (64 adapters of rank 16 at
 // 12288 x 4096: 34 MB beside 31 MB of W), and by latency otherwise: each
 // issues all loads of a step before the first product.
+//
+// Behind the tensor-core product, whose 96 or 128 CTAs leave SMs free, shrink runs
+// beside it: the product lets it start once its own wait for earlier grids is
+// over, and with its own work done it brings the used adapters' B to L2 (cold L2, the
+// whole call: 64 adapters of rank 16 at 12288 x 4096 34.0 -> 27.3 us; rank 64 at
+// 4096 x 12288, 64 tokens of one adapter 42.2 -> 38.3).  `expand` starts when both have
+// ended: let start early, its CTAs crowd on the few free SMs (28.5 and 41.9 us).
+// The few-token product fills every SM: shrink goes before it there.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -32,6 +40,7 @@ struct LoraArgs {
   uint32_t* err;
   int64_t K, N;
   int M, R, count, splits;
+  int beside;               // shrink runs beside the product and ends after it
 };
 
 // A token's adapter, -1 for none; one outside the pool is reported and adds nothing.
@@ -74,8 +83,10 @@ __global__ void __cluster_dims__(kShrinkCluster, 1, 1) __launch_bounds__(kShrink
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!p.beside) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   if (tid < kMaxTokens) ids[tid] = adapter_of(p, tid);
   __syncthreads();
   if (tid < kMaxTokens) {                                  // the first token of each adapter, in order
@@ -174,6 +185,20 @@ __global__ void __cluster_dims__(kShrinkCluster, 1, 1) __launch_bounds__(kShrink
       if (r0 + r < p.R) p.t[(split * kMaxTokens + list[m]) * p.R + r0 + r] = sc * v;
     }
     cluster.sync();                                        // peers keep their sums until all have read
+  }
+  if (p.beside) {
+    __syncthreads();                                       // lead is written, in CTAs without an item too
+    // the used adapters' B into L2 while the product runs, this CTA's share in pieces of 2 KB
+    const int64_t bytes = p.N * p.R * 2, pieces = (bytes + 2047) / 2048;     // N * R * 2 is a multiple of 512
+    for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + tid; e < pieces * adapters; e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      const int64_t u = e / pieces, at = (e - u * pieces) * 2048;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.b) + ids[lead[u]] * bytes + at;
+      const uint32_t n = static_cast<uint32_t>(bytes - at < 2048 ? bytes - at : 2048);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(n) : "memory");
+    }
+    // `expand` waits for this grid alone: it has the product when this grid ends after
+    // it.  One CTA sees to that, so that the others make room for those still to come.
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   }
 }
 
@@ -276,6 +301,7 @@ LoraArgs lora_args(const LoraCall& c) {
   p.R = c.R;
   p.count = c.count;
   p.splits = lora_splits(c.K);
+  p.beside = 0;
   return p;
 }
 
@@ -283,8 +309,9 @@ LoraArgs lora_args(const LoraCall& c) {
 
 int lora_splits(int64_t K) { return static_cast<int>(std::clamp<int64_t>(K / kSplitCols, 1, kMaxSplits)); }
 
-cudaError_t launch_lora_shrink(const LoraCall& c, const DeviceInfo& info, cudaStream_t s) {
-  const LoraArgs p = lora_args(c);
+cudaError_t launch_lora_shrink(const LoraCall& c, const DeviceInfo& info, bool beside, cudaStream_t s) {
+  LoraArgs p = lora_args(c);
+  p.beside = beside;
   cudaLaunchConfig_t cfg = {};
   // as many clusters as there can be items and as the GPU holds
   const int clusters = std::min(p.M * ((p.R + 15) / 16) * p.splits, std::max(1, kShrinkPerSm * info.sms / kShrinkCluster));

@@ -176,8 +176,16 @@ int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_ad
   c.R = ad->rank;
   c.count = ad->count;
   DeviceInfo info;
-  if (device_info(&info) != cudaSuccess || launch_lora_shrink(c, info, s) != cudaSuccess) return Q4NX_E_CUDA;
-  if ((st = q4nx_gemm_m64(w, X_dev, M, base, Q4NX_OUT_F32, workspace_dev, workspace_bytes, stream))) return st;
+  if (device_info(&info) != cudaSuccess) return Q4NX_E_CUDA;
+  if (M > gemv_max_tokens(w->kind)) {
+    // the tensor-core product leaves SMs free: shrink runs on them beside it
+    if (launch_gemm(w->kind, w->chunks_dev, w->rows / 32, w->cols / 256, X_dev, M, base, 1, workspace_dev, s, true) != cudaSuccess ||
+        launch_lora_shrink(c, info, true, s) != cudaSuccess)
+      return Q4NX_E_CUDA;
+  } else {
+    if (launch_lora_shrink(c, info, false, s) != cudaSuccess) return Q4NX_E_CUDA;
+    if ((st = q4nx_gemm_m64(w, X_dev, M, base, Q4NX_OUT_F32, workspace_dev, workspace_bytes, stream))) return st;
+  }
   return from_cuda(launch_lora_expand(c, f32, s));
 }
 

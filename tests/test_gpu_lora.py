@@ -104,6 +104,40 @@ def test_many_identical_calls_are_identical(q):
         assert torch.equal(first, q.q4nx_gemm_lora(c.W, c.X, c.ad, c.tid))
 
 
+@pytest.mark.parametrize("M,count,rank", [(64, 64, 16), (33, 1, 64), (9, 4, 8)])
+def test_chained_calls_read_what_the_grids_before_wrote(q, M, count, rank):
+    # each call's tokens are the last one's output, its ids written just before it: every
+    # kernel of a call starts early, and what it reads has to be there all the same
+    c = Case(q, synth.Q4_1, 2048, 2048, M, rank, count, [m % (count + 1) - 1 for m in range(M)])
+
+    def steps(wait):
+        x, ids, outs = c.X, c.tid, []
+        for _ in range(6):
+            y = q.q4nx_gemm_lora(c.W, x, c.ad, ids, out_dtype="f32")
+            outs.append(y)
+            x = (y / y.abs().amax(1, keepdim=True)).bfloat16()
+            ids = torch.where(ids + 1 < count, ids + 1, -1)
+            if wait:
+                torch.cuda.synchronize()
+        return outs
+
+    want = steps(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        steps(False)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured = steps(False)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, want))
+    q.q4nx_check(device=DEV)
+
+
 def test_adapter_outside_the_pool_adds_nothing_and_is_reported(q):
     c = Case(q, synth.Q4_1, 64, 512, 6, 16, 3, [0, 3, 2, 1 << 30, -1, 1])
     c.check(q.q4nx_gemm_lora(c.W, c.X, c.ad, c.tid), False)
