@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         for (int t = 0; t < 2 && ok; ++t) {
           const uint32_t bit = 1u << t, cols = __shfl_sync(0xffffffffu, tm + t * Y::kCols, 0);
           if (pending & bit) {                                       // O (+)= p v of the step before, while the other tile's p are formed
-            if (!(ok = wait(c, &c.p_full[t], (turn >> t & 1) ^ 1, a.err))) break;      // whose warps have waited for v_full
+            if (!(ok = wait(c, &c.p_full[t], (turn >> t & 1) ^ 1, a.err))) break;      // whose warps have waited for this step's v_full
             tc_fence_after();
             const uint64_t v = sw128_desc(base + Y::kValuesAt + (b ^ 1) * Y::kValues);
             const uint32_t p = cols + Y::kS, o = cols + Y::kO;
@@ -543,15 +543,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           from = static_cast<int>(lo - t0 + 1 > 0 ? (lo - t0 + 1 < kTok ? lo - t0 + 1 : kTok) : 0);
           to = static_cast<int>(hi - t0 + 1 < kTok ? (hi - t0 + 1 > 0 ? hi - t0 + 1 : 0) : kTok);
         }
-        // the values of this step, decoded by the time of S: what is odd among them
-        if (!(ok = wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
+        // S first, then the values, of which the product (issued on p_full) and `odd` need
+        // the latter.  The order matters: a tile goes past steps that its rows do not see
+        // without a wait, and parity tells v_full's phases apart only one step of a buffer
+        // away.  S of this step means that all decoding warps have posted the values of
+        // the steps before, so that the phase awaited is the current one or the last.
+        if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err) && wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
         if (c.odd_any[b] == j + 1) {
           for (int g = 0; g < NG; ++g)
             for (int k = from; k < to; ++k)
               if (c.odd[b][g][k] == j + 1) odd |= 1u << g;
         }
         __syncwarp();
-        if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err))) break;
         tc_fence_after();
         // the row's 64 logits stay in registers between maximum and weights: read again
         // for the second pass they cost 64.5 us instead of 62
