@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
       for (int j = 0; j < SB; ++j) {
         const int64_t blk = (u.first + (x - u.start)) * SB + j;
         const uint8_t* at = nullptr;
-        if (blk * kKvBlock < u.rq.L) {
+        if (blk * kKvBlock < u.rq.L && (blk + 1) * kKvBlock > first_visible(u.rq, a.window)) {
           at = kv_block_ptr(a.pool, a.kb, D, u.b, u.h, blk);
           if (at == nullptr) atomicOr(a.err, kErrIndex);
         }

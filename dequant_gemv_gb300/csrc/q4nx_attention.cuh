@@ -136,12 +136,15 @@ struct Unit {
   KvRequest rq;
 };
 
-template <int SB>
-__device__ __forceinline__ int64_t first_visible_step(const KvRequest& rq, int64_t window) {
-  constexpr int kStepTokens = SB * kKvBlock;
+// First position that some row of the request sees: pages before it need not be there.
+__device__ __forceinline__ int64_t first_visible(const KvRequest& rq, int64_t window) {
   if (window <= 0) return 0;
   const int64_t f = rq.L - rq.T + 1 - window;
-  return f > 0 ? f / kStepTokens : 0;
+  return f > 0 ? f : 0;
+}
+template <int SB>
+__device__ __forceinline__ int64_t first_visible_step(const KvRequest& rq, int64_t window) {
+  return first_visible(rq, window) / (SB * kKvBlock);
 }
 template <int SB>
 __device__ __forceinline__ int64_t unit_steps(const KvRequest& rq, int64_t window) {

@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         const int r = j % kRawStages;
         const uint8_t* src = nullptr;
         const int64_t blk = (w.step0 + n) * kSB + lane;
-        if (lane < kSB && blk * kKvBlock < w.u.rq.L) {
+        if (lane < kSB && blk * kKvBlock < w.u.rq.L && (blk + 1) * kKvBlock > w.s.first) {
           src = kv_block_ptr(a.pool, a.kb, D, w.u.b, w.u.h, blk);
           if (src == nullptr) atomicOr(a.err, kErrIndex);
         }

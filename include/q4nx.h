@@ -289,7 +289,9 @@ int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k
  *   out[t][h] = sum_j p_j v[j][h'] / sum_j p_j,  p_j = exp(scale * q[t][h] . k[j][h']),
  * h' = h / (heads / kv_heads), over the positions j up to the token's own and,
  * where window > 0, the last `window` of those.  The token's own key and value
- * have to be in the cache (q4nx_kv_append comes first).
+ * have to be in the cache (q4nx_kv_append comes first).  Pages of which no token
+ * of the call sees a position (those before the window) need not be there any more:
+ * their table entries are not read through.
  * q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token
  * (a multiple of 8).  out_dev: [tokens][heads][head_dim] of out_dtype.  lse_dev:
  * fp32 [tokens][heads], log sum_j p_j, or NULL.  heads: a multiple of kv_heads, up to 1024.
