@@ -257,7 +257,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, in
 }
 
 // Many query rows per request (q4nx_attention_block.cu; 64 or 128 channels): the
-// size of the parts, and the launch.
+// size of the parts (0 for other sizes), and the launch.
 uint64_t attention_block_bytes(int D);
 cudaError_t launch_attention_block(int D, const AttnArgs& a, int out_f32, const DeviceInfo& info, cudaStream_t s);
 

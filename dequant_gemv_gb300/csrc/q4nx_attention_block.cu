@@ -756,7 +756,7 @@ cudaError_t launch_block_variant(const AttnArgs& a, int grid, cudaStream_t s) {
 
 }  // namespace
 
-uint64_t attention_block_bytes(int D) { return static_cast<uint64_t>(kKvMaxCtas) * kRows * (D + 2) * 4; }
+uint64_t attention_block_bytes(int D) { return D > 128 ? 0 : static_cast<uint64_t>(kKvMaxCtas) * kRows * (D + 2) * 4; }
 
 cudaError_t launch_attention_block(int D, const AttnArgs& a, int out_f32, const DeviceInfo& info, cudaStream_t s) {
   const int grid = info.sms < kKvMaxCtas / 2 ? info.sms : kKvMaxCtas / 2;      // two parts each

@@ -66,6 +66,15 @@ def test_cache_entry_points_refuse(q):
     assert calls(c, _batch(q, tokens=0)) == (0, 0, 0)
 
 
+def test_cache_workspace_holds_what_the_kernels_of_its_size_leave(q):
+    # parts of 304 CTAs: 8 rows twice (values, maximum and sum) and 8 per warp; with 64 or
+    # 128 channels also the 256 rows of the kernel for many rows, the larger of the two
+    for dim in (64, 128, 256):
+        few, many = 304 * 8 * (2 * (dim + 2) + 8 * dim) * 4, 304 * 256 * (dim + 2) * 4 if dim < 256 else 0
+        head = q.lib.q4nx_kv_workspace(ctypes.byref(_cache(q, dim=dim))) - max(few, many)
+        assert 16 + 304 * 4 <= head <= 1 << 16, dim             # error word, counters and records
+
+
 def test_lora_refuses(q):
     L, by = q.lib, ctypes.byref
     w = q.q4nx_weight(P, 1 << 30, q.Q4NX_Q4_1, 0, 64, 512)
