@@ -24,6 +24,17 @@ def pytest_collection_modifyitems(config, items):
     pass
 
 
+# Host-side tests that hand made-up addresses to several entry points at once, of
+# which one refuses and the others would launch: only where there is no GPU to
+# launch on (with one, CUDA_VISIBLE_DEVICES= hides it).
+WITHOUT_GPU = {"test_cache_entry_points_refuse"}
+
+
+def pytest_runtest_setup(item):
+    if getattr(item, "originalname", item.name) in WITHOUT_GPU and gpu_available():
+        pytest.skip("made-up addresses: run it without a GPU")
+
+
 def gpu_available() -> bool:
     try:
         import torch

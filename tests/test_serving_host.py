@@ -66,6 +66,22 @@ def test_cache_entry_points_refuse(q):
     assert calls(c, _batch(q, tokens=0)) == (0, 0, 0)
 
 
+def test_cache_entry_points_refuse_is_not_run_beside_a_gpu(monkeypatch):
+    import types
+
+    import conftest
+
+    item = types.SimpleNamespace(name="test_cache_entry_points_refuse")
+    for gpu in (False, True):
+        monkeypatch.setattr(conftest, "gpu_available", lambda: gpu)
+        if gpu:
+            with pytest.raises(pytest.skip.Exception):
+                conftest.pytest_runtest_setup(item)
+        else:
+            conftest.pytest_runtest_setup(item)
+        conftest.pytest_runtest_setup(types.SimpleNamespace(name="test_index_status"))
+
+
 def test_cache_workspace_holds_what_the_kernels_of_its_size_leave(q):
     # parts of 304 CTAs: 8 rows twice (values, maximum and sum) and 8 per warp; with 64 or
     # 128 channels also the 256 rows of the kernel for many rows, the larger of the two
