@@ -160,10 +160,33 @@ def _cuda(t: torch.Tensor, name: str):
 # _gemv_batch) leaves its workspace zero-filled after every call and relies on
 # that; the GEMM leaves partial tiles behind, and so does the attention over
 # the 4-bit cache, so the families never share one.  One per (family, device, stream); calls on one stream are ordered, so
-# they never overlap.
+# they never overlap.  A captured graph goes on using the workspace of its capture: one
+# that became too small is kept, and one made during a capture is zero-filled at
+# once and not by the graph, so that it serves calls before the first replay too.
 _ws_lock = threading.Lock()
 _ws: dict[tuple[str, int, int], torch.Tensor] = {}
+_ws_replaced: dict[tuple[str, int, int], list[torch.Tensor]] = {}
 WS_FAMILIES = ("gemv", "gemm", "kv")
+
+
+def _zeros_beside_capture(nbytes: int, device: torch.device) -> torch.Tensor:
+    """Zero bytes, ready on return, while the current stream is being captured: made on
+    another stream, in memory that is not the graph's."""
+    relaxed = ctypes.c_int(2)                       # CU_STREAM_CAPTURE_MODE_RELAXED: allocating is no error
+    exchange = ctypes.CDLL("libcuda.so.1").cuThreadExchangeStreamCaptureMode
+    if exchange(ctypes.byref(relaxed)) != 0:
+        raise RuntimeError("cuThreadExchangeStreamCaptureMode failed")
+    try:
+        for _ in range(64):
+            side = torch.cuda.Stream(device)        # one of torch's pool of 32, the captured one among them
+            with torch.cuda.stream(side):
+                if not torch.cuda.is_current_stream_capturing():
+                    t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+                    side.synchronize()
+                    return t
+        raise RuntimeError("every stream is being captured: give a workspace")
+    finally:
+        exchange(ctypes.byref(relaxed))             # the thread's own mode again
 
 
 def workspace(device: torch.device, nbytes: int, family: str = "gemv") -> torch.Tensor:
@@ -173,8 +196,14 @@ def workspace(device: torch.device, nbytes: int, family: str = "gemv") -> torch.
     with _ws_lock:
         t = _ws.get(key)
         if t is None or t.numel() < nbytes:
-            t = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device)
-            _ws[key] = t
+            # twice the last: all that are kept are together no larger than the one in use
+            want = max(nbytes, 1 << 16, 0 if t is None else 2 * t.numel())
+            with torch.cuda.device(device):
+                made = (_zeros_beside_capture(want, device) if torch.cuda.is_current_stream_capturing()
+                        else torch.zeros(want, dtype=torch.uint8, device=device))
+            if t is not None:
+                _ws_replaced.setdefault(key, []).append(t)
+            t = _ws[key] = made
         return t
 
 
@@ -417,8 +446,8 @@ def q4nx_argmax(logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.
 
 def q4nx_check(ws: torch.Tensor | None = None, device=None) -> None:
     """Raise if a bounded in-kernel wait of an earlier call on this workspace (default:
-    this stream's GEMV, GEMM and cache workspaces) gave up, or if such a call
-    met an index out of range in device memory.  A workspace that reports
+    this stream's GEMV, GEMM and cache workspaces, those among them that a larger one
+    has replaced) gave up, or if such a call met an index out of range in device memory.  A workspace that reports
     a wait that gave up must be zero-filled before its next use: the default ones
     are zero-filled here before raising; a caller's own `ws` is left to the
     caller."""
@@ -427,12 +456,13 @@ def q4nx_check(ws: torch.Tensor | None = None, device=None) -> None:
         return
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     for family in WS_FAMILIES:
-        w = workspace(device, 16, family)
-        st = lib.q4nx_check(w.data_ptr(), _stream(w.device))
-        if st != Q4NX_OK:
-            with torch.cuda.device(w.device):
-                w.zero_()
-        _check(st, "q4nx_check")
+        now = workspace(device, 16, family)
+        for w in (now, *_ws_replaced.get((family, now.device.index, _stream(now.device)), ())):
+            st = lib.q4nx_check(w.data_ptr(), _stream(w.device))
+            if st != Q4NX_OK:
+                with torch.cuda.device(w.device):
+                    w.zero_()
+            _check(st, "q4nx_check")
 
 
 from . import serving  # noqa: E402  (needs the names above; fails loudly where _serving.so has not been built)
