@@ -465,7 +465,7 @@ def q4nx_check(ws: torch.Tensor | None = None, device=None) -> None:
             _check(st, "q4nx_check")
 
 
-from . import serving  # noqa: E402  (needs the names above; fails loudly where _serving.so has not been built)
+from . import serving  # noqa: E402  (needs the names above; its calls refuse where _serving.so has not been built)
 from .serving import (Adapters, KVCache, Logprobs, Q4NX_MAX_TOP, q4nx_adapters, q4nx_gemm_lora,  # noqa: E402,F401
                       q4nx_kv_append, q4nx_kv_attention, q4nx_kv_batch, q4nx_kv_cache, q4nx_kv_page_bytes, q4nx_kv_read,
                       q4nx_logprobs)

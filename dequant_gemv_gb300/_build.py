@@ -3,7 +3,9 @@
 ``python dequant_gemv_gb300/_build.py`` or ``build()`` compiles every
 ``csrc/*.cu`` into ``_objs/`` and links ``libq4nx.so`` next to this file, and
 the native binding of the decode-step operators (``csrc/serving_binding.cpp``,
-g++ against the installed torch's headers) into ``_serving.so``.
+g++ against the installed torch's headers) into ``_serving.so``.  The library comes
+first and needs neither: where the binding cannot be built, build() raises with the
+library in place, and without torch (C callers) there is no binding to build.
 Objects are rebuilt only when a source or header is newer.  No cmake.
 """
 from __future__ import annotations
@@ -47,9 +49,12 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_jobs(nvcc: str) -> tuple[list[str], list[str]]:
-    """Commands that compile and link the native binding against the installed torch."""
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+def _binding_jobs(nvcc: str) -> tuple[list[str], list[str]] | None:
+    """Commands that compile and link the native binding against the installed torch (None: there is none)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = list(spec.submodule_search_locations)[0]
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
            "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
@@ -77,24 +82,30 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append((src, cmd))
 
-    binding, link = _binding_jobs(nvcc)
-    if _stale(binding[-1], [binding[-3], os.path.join(ROOT, "include", "q4nx.h")]):
-        jobs.append((binding[-3], binding))
+    binding, link = _binding_jobs(nvcc) or (None, None)
+    source = os.path.join(CSRC, "serving_binding.cpp")
+    if binding and _stale(binding[-1], [source, os.path.join(ROOT, "include", "q4nx.h")]):
+        jobs.append((source, binding))
 
     def run(job):
         src, cmd = job
-        p = subprocess.run(cmd, capture_output=True, text=True)
+        try:
+            p = subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:                               # no such compiler
+            return src, 127, f"{e}\n"
         return src, p.returncode, p.stdout + p.stderr
 
     if jobs:
         with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
             results = list(ex.map(run, jobs))
-        failed = [(s, out) for s, rc, out in results if rc != 0]
+        failed = [s for s, rc, out in results if rc != 0]
         for s, rc, out in results:
             if verbose or ptxas_info or rc != 0:
                 sys.stderr.write(f"== {os.path.basename(s)} (rc={rc})\n{out}")
-        if failed:
-            raise RuntimeError("compilation failed on: " + ", ".join(os.path.basename(s) for s, _ in failed))
+        if any(s != source for s in failed):
+            raise RuntimeError("compilation failed on: " + ", ".join(os.path.basename(s) for s in failed))
+    else:
+        failed = []
     objs = [os.path.join(OBJS, os.path.basename(s)[:-3] + ".o") for s in sources]
     if _stale(LIB, objs) or jobs:
         tmp = LIB + f".tmp{os.getpid()}"
@@ -103,11 +114,14 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         if p.returncode != 0:
             raise RuntimeError("link of libq4nx.so failed:\n" + p.stdout + p.stderr)
         os.replace(tmp, LIB)
-    if _stale(BINDING, [binding[-1]]):
+    if failed:
+        raise RuntimeError("compilation failed on: serving_binding.cpp (libq4nx.so is built; without the binding the "
+                           "package's products work and the operators around them refuse)")
+    if binding and _stale(BINDING, [binding[-1]]):
         tmp = BINDING + f".tmp{os.getpid()}"
-        p = subprocess.run([*link, tmp], capture_output=True, text=True)
-        if p.returncode != 0:
-            raise RuntimeError("link of _serving.so failed:\n" + p.stdout + p.stderr)
+        _, rc, out = run((source, [*link, tmp]))
+        if rc != 0:
+            raise RuntimeError("link of _serving.so failed:\n" + out)
         os.replace(tmp, BINDING)
     return LIB
 

@@ -9,7 +9,8 @@
 
 As in the rest of the binding, only arguments are marshalled; formulas,
 layouts and limits stand in ``include/q4nx.h``.  The marshalling itself is native
-(``csrc/serving_binding.cpp``): it is as long as the kernels of small calls.
+(``csrc/serving_binding.cpp``): it is as long as the kernels of small calls.  Where
+that binding has not been built these calls raise ImportError; the products need none of it.
 """
 from __future__ import annotations
 
@@ -19,9 +20,26 @@ from typing import NamedTuple
 
 import torch
 
-from . import Q4NXError, Weight, _out_code, _serving, _ws, lib, q4nx_weight, workspace
+from . import Q4NXError, Weight, _out_code, _ws, lib, q4nx_weight, workspace
 
-_serving.setup(Q4NXError, workspace, _ws)
+
+class _NotBuilt:
+    """In the place of the binding: every call of it says why there is none."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: the native binding _serving.so is not usable ({self._why}); "
+                          "build it with python dequant_gemv_gb300/_build.py") from self._why
+
+
+try:
+    from . import _serving
+except ImportError as e:                 # not built, or built for another torch or Python
+    _serving = _NotBuilt(e)
+else:
+    _serving.setup(Q4NXError, workspace, _ws)
 P, U64, I, I64, F = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
 
