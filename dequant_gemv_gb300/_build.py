@@ -49,6 +49,16 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _other_link(target: str, record: str, cmd: list[str]) -> bool:
+    """Whether target was linked by another command than cmd, as record tells: going back to an
+    earlier torch finds that one's object older than the binding of the later one."""
+    try:
+        with open(record) as f:
+            return f.read() != "\n".join(cmd)
+    except OSError:
+        return os.path.exists(target)
+
+
 def _binding_jobs(nvcc: str) -> tuple[list[str], list[str]] | None:
     """Commands that compile and link the native binding against the installed torch (None: there is none)."""
     spec = importlib.util.find_spec("torch")
@@ -117,12 +127,15 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if failed:
         raise RuntimeError("compilation failed on: serving_binding.cpp (libq4nx.so is built; without the binding the "
                            "package's products work and the operators around them refuse)")
-    if binding and _stale(BINDING, [binding[-1]]):
+    record = os.path.join(OBJS, "serving_binding.link")
+    if binding and (_stale(BINDING, [binding[-1]]) or _other_link(BINDING, record, link)):
         tmp = BINDING + f".tmp{os.getpid()}"
         _, rc, out = run((source, [*link, tmp]))
         if rc != 0:
             raise RuntimeError("link of _serving.so failed:\n" + out)
         os.replace(tmp, BINDING)
+        with open(record, "w") as f:
+            f.write("\n".join(link))
     return LIB
 
 

@@ -38,6 +38,32 @@ def test_no_binding_without_torch(build, monkeypatch, tmp_path):
     assert os.path.getsize(build.LIB) > 0 and not os.path.exists(build.BINDING)
 
 
+def test_binding_is_linked_again_for_another_torch(build, monkeypatch, tmp_path):
+    # two torches whose objects are both there, the later one's link newer than either
+    objs = {}
+    for version in ("1.0", "2.0"):
+        objs[version] = tmp_path / f"serving_binding-torch{version}.o"
+        objs[version].write_bytes(b"")
+        os.utime(objs[version], (1, 1))
+    linked, binding = [], tmp_path / "_serving.so"
+
+    def jobs(version):
+        link = [sys.executable, "-c", "import sys; open(sys.argv[-1], 'w').write(sys.argv[1])", str(objs[version])]
+        return ["true", "-o", str(objs[version])], link
+
+    monkeypatch.setattr(build, "BINDING", str(binding))
+    monkeypatch.setattr(build, "OBJS", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", os.devnull)
+    monkeypatch.setattr(build, "_stale", lambda target, deps: target == str(binding) and not binding.exists())
+    for version in ("1.0", "2.0", "2.0", "1.0"):
+        monkeypatch.setattr(build, "_binding_jobs", lambda nvcc: jobs(version))
+        before = os.stat(binding).st_ino if binding.exists() else 0
+        build.build()
+        assert binding.read_text() == str(objs[version])
+        linked.append(os.stat(binding).st_ino != before)
+    assert linked == [True, True, False, True]
+
+
 def test_products_without_the_binding(build):
     code = """
 import sys
