@@ -7,8 +7,9 @@
 //
 // Keys enter as exact fp16 codes (a code's bits are the subnormal c*2^-24: one
 // AND makes two), queries as fp16 scaled by a power of two per row (bf16 has
-// 8 significant bits, so nothing is lost above 2^-39 of the row's largest), and
-// the scales meet the products in binary32:
+// 8 significant bits, so nothing is lost above 2^-27 of the row's largest, and 2^-35
+// of it at most below; rows of 2^117 and more would overflow), and the scales meet the
+// products in binary32:
 //   q.k   = sum_g sk_g * (q_g.ck_g) + sk_g * (-8*Q_g) + mk_g * Q_g,  Q_g = sum of q over g
 //   out_g = sum_j (p sv_g) (cv - 8) + sum_j p mv_g
 // The two terms with Q_g are matrix products with it as three bf16 parts (24
@@ -16,9 +17,10 @@
 // sum_j p mv_g is one with p as two (16 bits).  The values' codes are centred before their product (fp16
 // 1024 + c, less 1032): sums over thousands of tokens stay near their result.
 // p*sv is rounded to fp16 (2^-11 of itself; a power of two per row, which
-// follows the largest p*sv seen, keeps it in range); bf16 values would cost
-// 2^-9.  Codes in the high nibble of a byte enter as 16c: their q is divided
-// by 16, and so are the sums of the values' upper 8 channels of 16.
+// keeps the largest p*sv seen between 2^9 and 2^13, so that products 2^-23 of it and
+// less are subnormal, rounded by 2^-34 of it); bf16 values would cost 2^-9.  Codes in
+// the high nibble of a byte enter as 16c: their q is divided by 16, and so are the sums
+// of the values' upper 8 channels of 16.
 //
 // Tokens are the M of the products and query rows the N (8 per tile): a
 // decode step has as few rows as query heads share a kv head, and padding

@@ -299,9 +299,13 @@ int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k
  * infinities in positions that a row does not see do not reach it.  Rows of
  * tokens of no request are not written.
  * Accuracy: sums are binary32.  Up to 64 query rows (tokens x heads per kv head)
- * per request on average, and at 256 channels, the cached values enter exactly
- * and each weight p_j times a value scale is rounded to fp16 (2^-11 of itself);
- * above, cached values and weights enter as pairs of bf16 (2^-17 of themselves).
+ * per request on average, and at 256 channels, the cached values enter exactly,
+ * each weight p_j times a value scale is rounded to fp16 after a power of two that
+ * follows the row's largest such product: by 2^-11 of itself or 2^-34 of that largest
+ * (over all tokens and groups of the row), whichever is more, so that groups whose scales
+ * are 2^-23 and less of another group's lose accuracy of their own; p_j times mid enters
+ * with p_j to 2^-17.  Queries have to be below 2^117 there.  Above 64 rows, cached
+ * values and weights enter as pairs of bf16 (2^-17 of themselves).
  * Deterministic: partial sums are joined in a fixed order. */
 int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
                       int heads, float scale, int64_t window, void* out_dev, int out_dtype, float* lse_dev,
