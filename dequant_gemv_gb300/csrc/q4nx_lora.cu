@@ -7,11 +7,13 @@
 // issues all loads of a step before the first product.
 //
 // Behind the tensor-core product, whose 96 or 128 CTAs leave SMs free, shrink runs
-// beside it: the product lets it start once its own wait for earlier grids is
-// over, and with its own work done it brings the used adapters' B to L2 (cold L2, the
-// whole call: 64 adapters of rank 16 at 12288 x 4096 34.0 -> 27.3 us; rank 64 at
-// 4096 x 12288, 64 tokens of one adapter 42.2 -> 38.3).  `expand` starts when both have
-// ended: let start early, its CTAs crowd on the few free SMs (28.5 and 41.9 us).
+// beside it: the product lets it start once its own wait for earlier grids is over (cold
+// L2, the whole call: 64 adapters of rank 16 at 12288 x 4096 34.0 -> 28.1 us; rank 64 at
+// 4096 x 12288, 64 tokens of one adapter 42.2 -> 36.1).  Bringing the used adapters' B
+// to L2 in that time takes bandwidth from the product: 0.4 to 2 us gained with 13 to 25 MB
+// of them at 12288 x 4096, 2 to 15 lost with 0.5 MB at 4096 x 12288, with 25 MB at 24576 x
+// 4096 and with 31 MB and more, so that it is left to `expand`.  `expand` starts when both have
+// ended: let start early, its CTAs crowd on the few free SMs (2 to 4 us more).
 // The few-token product fills every SM: shrink goes before it there.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -186,20 +188,9 @@ __global__ void __cluster_dims__(kShrinkCluster, 1, 1) __launch_bounds__(kShrink
     }
     cluster.sync();                                        // peers keep their sums until all have read
   }
-  if (p.beside) {
-    __syncthreads();                                       // lead is written, in CTAs without an item too
-    // the used adapters' B into L2 while the product runs, this CTA's share in pieces of 2 KB
-    const int64_t bytes = p.N * p.R * 2, pieces = (bytes + 2047) / 2048;     // N * R * 2 is a multiple of 512
-    for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + tid; e < pieces * adapters; e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-      const int64_t u = e / pieces, at = (e - u * pieces) * 2048;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.b) + ids[lead[u]] * bytes + at;
-      const uint32_t n = static_cast<uint32_t>(bytes - at < 2048 ? bytes - at : 2048);
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(n) : "memory");
-    }
-    // `expand` waits for this grid alone: it has the product when this grid ends after
-    // it.  One CTA sees to that, so that the others make room for those still to come.
-    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
+  // `expand` waits for this grid alone: it has the product when this grid ends after
+  // it.  One CTA sees to that, so that the others make room for those still to come.
+  if (p.beside && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Y = base + B t.  A thread owns one output column n, a CTA kExpandCols
