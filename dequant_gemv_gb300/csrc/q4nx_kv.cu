@@ -12,8 +12,9 @@
 // all lanes on one token's channels; prompts take a warp per (16-token block,
 // kv head, keys or values, 64 channels), which owns them during the launch and writes whole
 // sectors (a token's value codes are one byte in each of 64 words: 3351 tokens of
-// 8 heads by the first kernel 16.1 us, by the second 10.7).  Bound: bytes (4 in, 0.625
-// out per value), and the quantisation's arithmetic close behind.
+// 8 heads by the first kernel 16.1 us, by the second 10.7).  Floor: bytes (2 in, 0.625
+// out per value, 2.7 us of these); what keeps it from them are latencies: the request's look-up
+// before the loads, a lane's 64 bytes apart from the next lane's, 2-byte stores of scales.
 #include "q4nx_kernels.h"
 #include "q4nx_kv.cuh"
 

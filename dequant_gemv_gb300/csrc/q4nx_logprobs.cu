@@ -15,9 +15,9 @@
 // least half): a floor made by a nearly empty warp lets everything through.  Only threads whose own maximum reaches the
 // floor have their elements read again (from L2, by their whole warp; one thread in
 // ten), and the elements at or above it, about a hundred, get their ranks by
-// counting.  Rows with
-// more than kCand such elements (many equal ones) take `top` rounds of
-// "largest below the previous" instead.
+// counting.  Rows with more than kCand such elements (many equal ones; so few above -inf
+// that -inf is the floor) take `top` rounds of "largest below the previous" instead: one
+// row of 151936 of which 40 are allowed, top 20, 80 us instead of 10.
 #include <cooperative_groups.h>
 
 #include "q4nx_kernels.h"

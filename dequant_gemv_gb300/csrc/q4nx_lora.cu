@@ -8,8 +8,8 @@
 //
 // Behind the tensor-core product, whose 96 or 128 CTAs leave SMs free, shrink runs
 // beside it: the product lets it start once its own wait for earlier grids is over (cold
-// L2, the whole call: 64 adapters of rank 16 at 12288 x 4096 34.0 -> 28.1 us; rank 64 at
-// 4096 x 12288, 64 tokens of one adapter 42.2 -> 36.1).  Bringing the used adapters' B
+// L2, the whole call: 64 adapters of rank 16 at 12288 x 4096 34.0 -> 27.9 us; rank 64 at
+// 4096 x 12288, 64 tokens of one adapter 42.2 -> 36.0).  Bringing the used adapters' B
 // to L2 in that time takes bandwidth from the product: 0.4 to 2 us gained with 13 to 25 MB
 // of them at 12288 x 4096, 2 to 15 lost with 0.5 MB at 4096 x 12288, with 25 MB at 24576 x
 // 4096 and with 31 MB and more, so that it is left to `expand`.  `expand` starts when both have
@@ -70,8 +70,10 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // 8i..8i+7 of A's rows n, n + 8 and of token n: two k16 products, the columns in
 // the same order on both sides, every load 16 bytes): two steps a warp, whose loads
 // are issued together.  What counts is how many loads the whole GPU has in
-// flight: without the parts, at rank 64, 12288 columns and 64 tokens, only 32 CTAs have work, and
-// the whole call takes 56 us (cold L2) instead of 48.  The warps' sums meet in shared memory and the CTAs'
+// flight: without the parts, at rank 64, 12288 columns (Q8) and 64 tokens of one adapter, only 32
+// CTAs have work, and the whole call takes 45 us (cold L2) instead of 37.  With many adapters there
+// is work enough and the parts cost instead: 4 of them 39 and 40, 16 of them 45 and 58, 64
+// of them 97 and 134.  The warps' sums meet in shared memory and the CTAs'
 // through distributed shared memory, in a fixed order.
 constexpr int kShrinkWarps = 8, kShrinkCluster = 8, kShrinkPerSm = 3;
 constexpr int kSplitCols = 4096, kMaxSplits = 8;
