@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_runtime.h>
 
 #include "../../include/q4nx.h"
 
@@ -17,6 +18,11 @@ int check_grid(int64_t rows, int64_t cols);
 // Q4NX_OK, or the status of the first failing check of a weight: NULL
 // pointer, unknown kind (or nonzero reserved field), shape, length, alignment.
 int check_weight(const q4nx_weight* w);
+
+// q4nx_gemm_m64 behind its checks, with an epilogue where `ep` is not NULL.
+struct Epilogue;
+int launch_product(const q4nx_weight* w, const void* X, int M, void* Y, int out_dtype, void* workspace, cudaStream_t s,
+                   const Epilogue* ep);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,0 +1,73 @@
+// q4nx_epilogue.cuh -- what q4nx_gemm_epilogue does to a product before its one
+// rounding, shared by the GEMV and GEMM kernels:
+//   y = act(acc + bias[n]) * mul[m][n] + residual[m][n],
+// each step in binary32.  An element's operands are read by the CTA that stores it,
+// before it does, so that mul or residual may be the output itself.
+#pragma once
+
+#include <cstdint>
+
+#include "q4nx_device.cuh"
+
+namespace q4nx {
+
+enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+struct Epilogue {
+  const uint16_t* bias = nullptr;      // bf16 [N]
+  const uint16_t* mul = nullptr;       // bf16 [M][N], mul_stride elements from token to token
+  const uint16_t* residual = nullptr;  // bf16 [M][N]
+  int64_t mul_stride = 0, residual_stride = 0;
+  int act = kActNone;
+};
+
+// x / (1 + exp(-z)), right to a few units in the last place for every z: where exp(-z)
+// overflows the result is 0 (or the quotient's NaN for infinite x)
+__device__ __forceinline__ float times_sigmoid(float x, float z) { return __fdividef(x, 1.f + expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float activated(float x) {
+  if constexpr (ACT == kActRelu) return x < 0.f ? 0.f : x;                       // NaN stays NaN
+  // erfc, not 1 + erf: that would leave nothing of the tail below -4
+  if constexpr (ACT == kActGelu) return 0.5f * x * erfcf(-0.70710678118654752f * x);
+  // 0.5 x (1 + tanh u) = x / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
+  if constexpr (ACT == kActGeluTanh) return times_sigmoid(x, 1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
+  if constexpr (ACT == kActSilu) return times_sigmoid(x, x);
+  return x;
+}
+
+template <int T>
+__device__ __forceinline__ void activate(int act, float (&v)[T]) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int t = 0; t < T; ++t) v[t] = activated<kActRelu>(v[t]);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int t = 0; t < T; ++t) v[t] = activated<kActGelu>(v[t]);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int t = 0; t < T; ++t) v[t] = activated<kActGeluTanh>(v[t]);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int t = 0; t < T; ++t) v[t] = activated<kActSilu>(v[t]);
+      break;
+    default: break;
+  }
+}
+
+// One element, its operands straight from memory.
+__device__ __forceinline__ float epilogue_of(const Epilogue& e, int64_t n, int m, float acc) {
+  const uint32_t b = e.bias != nullptr ? e.bias[n] : 0u, g = e.mul != nullptr ? e.mul[m * e.mul_stride + n] : 0u,
+                 r = e.residual != nullptr ? e.residual[m * e.residual_stride + n] : 0u;
+  float v[1] = {e.bias != nullptr ? acc + bf16_bits_to_f32(b) : acc};
+  activate<1>(e.act, v);
+  if (e.mul != nullptr) v[0] *= bf16_bits_to_f32(g);
+  if (e.residual != nullptr) v[0] += bf16_bits_to_f32(r);
+  return v[0];
+}
+
+}  // namespace q4nx

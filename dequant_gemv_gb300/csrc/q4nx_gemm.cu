@@ -81,7 +81,10 @@
 // touched only after that wait.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "q4nx_device.cuh"
+#include "q4nx_epilogue.cuh"
 #include "q4nx_kernels.h"
 
 namespace q4nx {
@@ -95,13 +98,16 @@ constexpr int kXBytes = 4 * kXBox;                     // 32 KB
 constexpr int kWOff = 0;
 constexpr int kMaxWStages = 6;
 // Shared-memory plan per chunk kind: weight stages, then X stages, then barriers.
-template <int KIND>
+// EPI: a slot for a tile of one of the epilogue's operands, at the cost of a q4_1 weight stage.
+constexpr int kSlotBytes = kTileN * kTileM * 2;
+template <int KIND, bool EPI>
 struct Plan {
   static constexpr bool kQ8 = KIND == kQ8_KR || KIND == kQ8_BLK;
   static constexpr int kWBytes = kQ8 ? 4 * kQ8Bytes : 4 * kCodes + 4 * kScales;   // one k-step of 4 chunks
-  static constexpr int kWStages = kQ8 ? 3 : 6;
+  static constexpr int kWStages = kQ8 ? 3 : EPI ? 5 : 6;
   static constexpr int kXOff = kWOff + kWStages * kWBytes;
-  static constexpr int kBarOff = kXOff + kStages * kXBytes;
+  static constexpr int kSlotOff = kXOff + kStages * kXBytes;
+  static constexpr int kBarOff = kSlotOff + (EPI ? kSlotBytes : 0);
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;   // barriers and flags, alignment slack
   static_assert(kWStages <= kMaxWStages, "weight stages");
   static_assert(kWBytes % 1024 == 0 && kXOff % 1024 == 0 && kXBytes % 1024 == 0, "swizzled regions 1024-aligned");
@@ -111,12 +117,12 @@ struct Plan {
 // once the CTA's last MMA has completed: three in the weight stages, two in X
 // stages 1 and 2 (X stage 0 stages the output tile).
 constexpr int kGatherSlots = 5;
-template <int KIND>
+template <int KIND, bool EPI>
 __host__ __device__ constexpr int gather_slot(int i) {
-  return i < 3 ? kWOff + i * kXBytes : Plan<KIND>::kXOff + (i - 2) * kXBytes;
+  return i < 3 ? kWOff + i * kXBytes : Plan<KIND, EPI>::kXOff + (i - 2) * kXBytes;
 }
-static_assert(3 * kXBytes <= Plan<kQ4_1>::kWStages * Plan<kQ4_1>::kWBytes, "three partials fit the q4_1 weight stages");
-static_assert(3 * kXBytes <= Plan<kQ8_KR>::kWStages * Plan<kQ8_KR>::kWBytes, "three partials fit the Q8 weight stages");
+static_assert(3 * kXBytes <= Plan<kQ4_1, true>::kWStages * Plan<kQ4_1, true>::kWBytes, "three partials fit the q4_1 weight stages");
+static_assert(3 * kXBytes <= Plan<kQ8_KR, false>::kWStages * Plan<kQ8_KR, false>::kWBytes, "three partials fit the Q8 weight stages");
 static_assert(kStages == 3, "X stages 1 and 2 take two partials");
 
 constexpr int kDequantWarps = 8;                       // two per TMEM lane quarter, one half of the k-step each
@@ -150,6 +156,13 @@ struct Args {
   int mrows;                // X box rows: M rounded up to 8
   int64_t units;            // tiles * TC
   int after_wait;           // the next launch may start once the previous grids are done, not before
+};
+// With an epilogue: an operand of it (mul, else residual) comes tile by tile through
+// shared memory, beside the products; the other of two by loads while the tile is finished.
+struct ArgsEpilogue : Args {
+  CUtensorMap slot_map;     // bf16 [N][M]
+  int slot;                 // there is one
+  Epilogue ep;
 };
 
 // --------------------------------------------------------------- PTX ----
@@ -196,6 +209,16 @@ __device__ __forceinline__ void issue_x(uint32_t dst, const CUtensorMap* xmap, i
       "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0+16384], [%1, {x2, 0}], [%3];\n\t"
       "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0+24576], [%1, {x3, 0}], [%3];\n\t}"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(xmap)), "r"(256 * ks), "r"(bar), "r"(4 * 128 * mrows)
+      : "memory");
+}
+// A tile of an epilogue operand, [64 tokens][128 rows] from row n0 (what lies past its end
+// reads as zeros and counts its bytes), on one elected lane.
+__device__ __forceinline__ void issue_slot(uint32_t dst, const CUtensorMap* map, int n0, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %4;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, 0}], [%3];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(n0), "r"(bar), "n"(kSlotBytes)
       : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -261,6 +284,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// 8 consecutive TMEM columns of this thread's lane
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    asm volatile("" : "+r"(r[i]));
+    v[i] = __uint_as_float(r[i]);
+  }
+}
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
@@ -301,6 +337,7 @@ struct Shared {
   uint64_t drain;
   uint64_t staged;          // epilogue warps that have staged their rows of the last tile
   uint64_t gather;          // the last tile's later partials, copied into free stage memory
+  uint64_t slot_full, slot_empty;   // the epilogue operand's tile
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
   uint32_t fix_seen;        // finisher's epilogue warps that have gathered every posted partial
@@ -448,14 +485,93 @@ __device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* 
       : "memory");
 }
 
-template <int KIND>
+// The epilogue of a tile whose sums are complete in TMEM and, for a finisher, in fx:
+// to the staged tile `stg` in shared memory, or (0) to Y.  `f`: the tile's number among
+// those that pass here.  Eight tokens at a time from TMEM in a rolled loop: with a tile's
+// half in registers the activations' code is cold and long, and the operands spill.
+__device__ __forceinline__ bool finish_tile(Shared* sh, const ArgsEpilogue& a, const uint8_t* slot, uint32_t taddr, int64_t n0, int row,
+                                            bool valid_row, bool finisher, const float4 (&fx)[kTileN / 4], uint32_t bias_bits,
+                                            int f, uint32_t stg) {
+  if (finisher) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      tmem_ld32(taddr + 32 * h, v);
+      uint32_t r[32];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        r[4 * k] = __float_as_uint(v[4 * k] + fx[8 * h + k].x);
+        r[4 * k + 1] = __float_as_uint(v[4 * k + 1] + fx[8 * h + k].y);
+        r[4 * k + 2] = __float_as_uint(v[4 * k + 2] + fx[8 * h + k].z);
+        r[4 * k + 3] = __float_as_uint(v[4 * k + 3] + fx[8 * h + k].w);
+      }
+      tmem_st32_async(taddr + 32 * h, r);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+  }
+  const Epilogue& e = a.ep;
+  const int64_t n = n0 + row;
+  const bool direct = e.mul != nullptr && e.residual != nullptr && valid_row;    // the residual does not come through the slot
+  const float bias = bf16_bits_to_f32(bias_bits);
+  uint16_t next[8];                                  // it, eight tokens ahead
+  auto load = [&](int m0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) next[k] = direct && m0 + k < a.M ? e.residual[(m0 + k) * e.residual_stride + n] : uint16_t{0};
+  };
+  load(0);
+  if (a.slot && !wait_bar_warp(sh, &sh->slot_full, f & 1, a.err)) return false;
+  const uint32_t src = smem_u32(slot) + row * 2;
+#pragma unroll 1
+  for (int m0 = 0; m0 < a.M; m0 += 8) {
+    float v[8];
+    tmem_ld8(taddr + m0, v);
+    if (e.bias != nullptr)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += bias;
+    activate<8>(e.act, v);
+    if (e.mul != nullptr)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= bf16_bits_to_f32(lds_u16(src + (m0 + k) * (kTileM * 2)));
+    if (e.residual != nullptr) {
+      if (e.mul == nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += bf16_bits_to_f32(lds_u16(src + (m0 + k) * (kTileM * 2)));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += bf16_bits_to_f32(next[k]);
+        load(m0 + 8);
+      }
+    }
+    if (stg != 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t idx = static_cast<uint32_t>((m0 + k) * kTileM + row);
+        if (a.out_f32) sts_f32(stg + idx * 4, v[k]);
+        else sts_u16(stg + idx * 2, f32_to_bf16_bits(v[k]));
+      }
+    } else if (valid_row) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (m0 + k < a.M) {
+          if (a.out_f32) static_cast<float*>(a.Y)[(m0 + k) * a.N + n] = v[k];
+          else static_cast<uint16_t*>(a.Y)[(m0 + k) * a.N + n] = f32_to_bf16_bits(v[k]);
+        }
+    }
+  }
+  __syncwarp();                                      // the slot is read out
+  if (a.slot && (threadIdx.x & 31) == 0) mbar_arrive(&sh->slot_empty);
+  return true;
+}
+
+// EPI: with an epilogue on the sums.
+template <int KIND, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap smap,
                     const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
-                    const __grid_constant__ Args a) {
+                    const __grid_constant__ std::conditional_t<EPI, ArgsEpilogue, Args> a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  using P = Plan<KIND>;
+  using P = Plan<KIND, EPI>;
   constexpr int kWStages = P::kWStages, kWBytes = P::kWBytes, kXOff = P::kXOff;
   Shared* sh = reinterpret_cast<Shared*>(smem + P::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -473,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->drain, 1);
     mbar_init(&sh->staged, 4);
     mbar_init(&sh->gather, 1);
+    mbar_init(&sh->slot_full, 1);
+    mbar_init(&sh->slot_empty, 4);
     sh->abort_flag = 0u;
     sh->fix_seen = 0u;
     fence_barrier_init();
@@ -510,13 +628,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");     // X may be the previous grid's output
     if (a.after_wait) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int64_t ks = lo % KS;
+    [[maybe_unused]] int64_t tile = first_tile;
+    [[maybe_unused]] int finished = 0;               // tiles whose operand was sent for
     int j = 0;
     for (; j < n; ++j) {
       const int s = j % kStages;
       if (!wait_bar_warp(sh, &sh->empty[s], ((j / kStages) & 1) ^ 1u, a.err)) break;
       issue_x(smem_u32(smem + kXOff + s * kXBytes), &xmap, static_cast<int>(ks), smem_u32(&sh->full[s]), a.mrows);
+      if constexpr (EPI) {
+        // a tile that is finished here: its operand, at the end of its share, when the tile before
+        // is about done with the slot (what that waits for needs no X still to come)
+        if ((ks + 1 == KS || j == n - 1) && a.slot && tile * KS >= lo) {
+          if (!wait_bar_warp(sh, &sh->slot_empty, (finished & 1) ^ 1u, a.err)) break;
+          issue_slot(smem_u32(smem + P::kSlotOff), &a.slot_map, static_cast<int>(tile * kTileM), smem_u32(&sh->slot_full));
+          ++finished;
+        }
+        if (ks + 1 == KS) ++tile;
+      }
       if (++ks == KS) ks = 0;
     }
+    if constexpr (EPI)
+      if (finished > 0) mbar_wait_bounded(&sh->slot_full, (finished - 1) & 1, 100000000ull);
     // copies still in flight land first (a stage whose dequant part stopped short stays incomplete:
     // then the wait gives up after its limit, which only happens on the error path)
     for (int t = (j > kStages ? j - kStages : 0); t < j; ++t)
@@ -656,6 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");     // Y and the workspace may be the previous grid's
     const int e = warp & 3;                         // TMEM lane quarter of this warp
     const int row = 32 * e + lane;                  // row within the 128-row tile
+    [[maybe_unused]] int finished = 0;              // tiles through the epilogue
     for (int t = 0; t < ntiles; ++t) {
       const int b = t & 1;
       const int64_t tile = first_tile + t;
@@ -697,10 +830,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last epilogue warp through clears the count for the next launch
         if (lane == 0 && atomicAdd(&sh->fix_seen, 1u) == 3u) a.counters[tile] = 0u;
       }
-      if (!wait_bar(sh, &sh->acc_full[b], (t >> 1) & 1, a.err)) break;
-      tc_fence_after();
       const int64_t n0 = tile * kTileM;
       const bool valid_row = n0 + row < a.N;
+      [[maybe_unused]] uint32_t bias = 0;
+      if constexpr (EPI)
+        if (a.ep.bias != nullptr && valid_row) bias = a.ep.bias[n0 + row];
+      if (!wait_bar(sh, &sh->acc_full[b], (t >> 1) & 1, a.err)) break;
+      tc_fence_after();
       float4* mine = reinterpret_cast<float4*>(a.partials + static_cast<int64_t>(blockIdx.x) * (kTileN * kTileM)) + row;
       const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * e) << 16) + static_cast<uint32_t>(b * kTileN);
       if (last && !contrib) {
@@ -719,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               asm volatile("fence.proxy.async.global;" ::: "memory");
               mbar_arrive_expect_tx(&sh->gather, static_cast<uint32_t>(nsm * kTileN * kTileM * 4));
               for (int i = 0; i < nsm; ++i)
-                bulk_g2s(smem + gather_slot<KIND>(i), a.partials + (blockIdx.x + 2 + i) * (kTileN * kTileM),
+                bulk_g2s(smem + gather_slot<KIND, EPI>(i), a.partials + (blockIdx.x + 2 + i) * (kTileN * kTileM),
                          kTileN * kTileM * 4, &sh->gather);
             }
             if (!wait_bar(sh, &sh->gather, 0, a.err)) break;
@@ -727,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 2; ++h) {
 #pragma unroll 1
               for (int i = 0; i < nsm; ++i) {
-                const uint32_t src = smem_u32(smem + gather_slot<KIND>(i)) + static_cast<uint32_t>(row * 16);
+                const uint32_t src = smem_u32(smem + gather_slot<KIND, EPI>(i)) + static_cast<uint32_t>(row * 16);
                 float4 v[kTileN / 8];
 #pragma unroll
                 for (int k = 0; k < kTileN / 8; ++k) v[k] = lds_f32x4(src + static_cast<uint32_t>((8 * h + k) * kTileM * 16));
@@ -740,6 +876,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if constexpr (EPI) {
+          if (!finish_tile(sh, a, smem + P::kSlotOff, taddr, n0, row, valid_row, finisher, fx, bias, finished++, stg)) break;
+        } else
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[32];
@@ -775,6 +914,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
+      if (EPI && !contrib) {
+        if constexpr (EPI)
+          if (!finish_tile(sh, a, smem + P::kSlotOff, taddr, n0, row, valid_row, finisher, fx, bias, finished++, 0u)) break;
+      } else
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
@@ -857,9 +1000,11 @@ uint64_t gemm_workspace_bytes(int64_t TR, int64_t TC, int M) {
 namespace {
 template <int KIND>
 cudaError_t launch_gemm_kind(EncodeTiled enc, const DeviceInfo& info, const void* chunks, int64_t TR, int64_t TC,
-                             const void* X, int M, void* Y, int out_f32, void* workspace, cudaStream_t s, bool after_wait) {
-  using P = gemm::Plan<KIND>;
-  if (info.max_smem_optin < P::kSmemBytes) return cudaErrorNotSupported;
+                             const void* X, int M, void* Y, int out_f32, void* workspace, cudaStream_t s, bool after_wait,
+                             const Epilogue* ep) {
+  using P = gemm::Plan<KIND, false>;
+  using PE = gemm::Plan<KIND, true>;
+  if (info.max_smem_optin < (ep != nullptr ? PE::kSmemBytes : P::kSmemBytes)) return cudaErrorNotSupported;
   // weights, q4_1: code regions as [128 B][32 rows][TC chunk columns][TR tile rows] (128-byte swizzle)
   // and scale/zero regions as [256 B][4][TC][TR] from byte 4096 of each chunk; Q8: whole chunks as
   // [256 B][34][TC][TR].  X as [64 k][M tokens][K / 64]; Y as [N][M].
@@ -957,26 +1102,47 @@ cudaError_t launch_gemm_kind(EncodeTiled enc, const DeviceInfo& info, const void
   if (grid > 1024) grid = 1024;
   if (grid < 1) grid = 1;
   a.grid = static_cast<int>(grid);
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(gemm::gemm_kernel<KIND>));
+  cudaError_t e = set_max_dynamic_smem(ep != nullptr ? reinterpret_cast<const void*>(gemm::gemm_kernel<KIND, true>)
+                                                     : reinterpret_cast<const void*>(gemm::gemm_kernel<KIND, false>));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.grid);
   cfg.blockDim = dim3(gemm::kThreads);
-  cfg.dynamicSmemBytes = P::kSmemBytes;
+  cfg.dynamicSmemBytes = ep != nullptr ? PE::kSmemBytes : P::kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, gemm::gemm_kernel<KIND>, wmap, smap, xmap, ymap, a);
+  if (ep != nullptr) {
+    gemm::ArgsEpilogue b;
+    static_cast<gemm::Args&>(b) = a;
+    b.ep = *ep;
+    const uint16_t* operand = ep->mul != nullptr ? ep->mul : ep->residual;
+    b.slot = operand != nullptr;
+    b.slot_map = ymap;                              // a map all the same
+    if (operand != nullptr) {
+      cuuint64_t dims[2] = {static_cast<cuuint64_t>(TR * 32), static_cast<cuuint64_t>(M)};
+      cuuint64_t strides[1] = {static_cast<cuuint64_t>(ep->mul != nullptr ? ep->mul_stride : ep->residual_stride) * 2u};
+      cuuint32_t box[2] = {128, 64};
+      cuuint32_t es[2] = {1, 1};
+      if (enc(&b.slot_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(operand), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
+    e = cudaLaunchKernelEx(&cfg, gemm::gemm_kernel<KIND, true>, wmap, smap, xmap, ymap, b);
+  } else {
+    e = cudaLaunchKernelEx(&cfg, gemm::gemm_kernel<KIND, false>, wmap, smap, xmap, ymap, a);
+  }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 }  // namespace
 
 cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, const void* X, int M, void* Y,
-                        int out_f32, void* workspace, cudaStream_t s, bool after_wait) {
+                        int out_f32, void* workspace, cudaStream_t s, bool after_wait, const Epilogue* ep) {
   if (!gemm_supports(kind)) return cudaErrorNotSupported;
   EncodeTiled enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
@@ -984,9 +1150,9 @@ cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, co
   cudaError_t e = device_info(&info);
   if (e != cudaSuccess) return e;
   switch (kind) {
-    case kQ4_1: return launch_gemm_kind<kQ4_1>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait);
-    case kQ8_KR: return launch_gemm_kind<kQ8_KR>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait);
-    default: return launch_gemm_kind<kQ8_BLK>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait);
+    case kQ4_1: return launch_gemm_kind<kQ4_1>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait, ep);
+    case kQ8_KR: return launch_gemm_kind<kQ8_KR>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait, ep);
+    default: return launch_gemm_kind<kQ8_BLK>(enc, info, chunks, TR, TC, X, M, Y, out_f32, workspace, s, after_wait, ep);
   }
 }
 

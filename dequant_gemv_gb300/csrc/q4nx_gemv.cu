@@ -101,7 +101,10 @@ __device__ __forceinline__ void* token_y(const GemvArgs& a, void* y, int tok) {
 }
 
 template <class GemvArgs>
-__device__ __forceinline__ void store_y(const GemvArgs& a, void* y, int64_t n, float v) {
+__device__ __forceinline__ void store_y(const GemvArgs& a, void* y, int64_t n, float v, int tok) {
+  if constexpr (GemvArgs::kEpilogue) {
+    v = epilogue_of(a.ep, n, tok, v);
+  }
   if (a.top1) {
     uint64_t key = argmax_key(v, a.top1_row_base + static_cast<uint32_t>(n));
 #pragma unroll
@@ -198,7 +201,7 @@ __device__ __noinline__ void cross_cta_row(const GemvArgs& a, int64_t b, int64_t
   }
 #pragma unroll
   for (int tok = 0; tok < MT; ++tok)
-    if (tok < m) store_y(a, token_y(a, item.y, tok), tr * 32 + lane, sum[tok]);
+    if (tok < m) store_y(a, token_y(a, item.y, tok), tr * 32 + lane, sum[tok], tok);
 }
 
 // ------------------------------------------------------- chunk bodies ----
@@ -642,7 +645,7 @@ __device__ __noinline__ void finish_segment(const GemvArgs& a, int64_t b, int w,
   if (lo <= r0 && r1 <= hi) {
 #pragma unroll
     for (int tok = 0; tok < MT; ++tok)
-      if (tok < m) store_y(a, token_y(a, item.y, tok), tr * 32 + row, val[tok]);
+      if (tok < m) store_y(a, token_y(a, item.y, tok), tr * 32 + row, val[tok], tok);
     return;
   }
   const int k = (r0 <= lo) ? 0 : 1;                 // the warp's first segment iff the row holds lo
@@ -671,7 +674,7 @@ __device__ __noinline__ void finish_segment(const GemvArgs& a, int64_t b, int w,
   if (r0 >= Lc && r1 <= Hc) {
 #pragma unroll
     for (int tok = 0; tok < MT; ++tok)
-      if (tok < m) store_y(a, token_y(a, item.y, tok), tr * 32 + lane, sum[tok]);
+      if (tok < m) store_y(a, token_y(a, item.y, tok), tr * 32 + lane, sum[tok], tok);
   } else {
     cross_cta_row<MT>(a, b, Lc, it, tr, r0, r1, sum, lane);
   }
@@ -738,7 +741,7 @@ constexpr int gemv_max_threads() {
 // several, only into the launches planned to use it -- its branch alone costs
 // those that do not up to 17 %).
 template <int KIND, int MAXB, int MT, bool QTR = false, bool XCT = true>
-__global__ void __launch_bounds__(gemv_max_threads<KIND, MT>(), 1) gemv_kernel(const __grid_constant__ GemvArgsT<MAXB> a) {
+__global__ void __launch_bounds__(gemv_max_threads<KIND, MT>(), 1) gemv_kernel(const __grid_constant__ typename GemvArgsOf<MAXB>::Type a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int CB = chunk_bytes_of(KIND);                         // a ring stage holds one chunk
   constexpr bool Q4 = (KIND == kQ4_1 || KIND == kQ4_K);
@@ -1108,7 +1111,7 @@ uint64_t gemv_workspace_bytes(int64_t total_tile_rows, int64_t total_chunks, int
 }
 
 template <int KIND, int MAXB, int MT, bool QTR = false, bool XCT = true>
-static cudaError_t launch_gemv_t(const GemvArgsT<MAXB>& a, const GemvPlan& p, cudaStream_t s) {
+static cudaError_t launch_gemv_t(const typename GemvArgsOf<MAXB>::Type& a, const GemvPlan& p, cudaStream_t s) {
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(gemv_kernel<KIND, MAXB, MT, QTR, XCT>));
   if (e != cudaSuccess) return e;
   // Programmatic dependent launch: SMs freed by the previous grid start this
@@ -1148,7 +1151,7 @@ static void fill_items(GemvArgsT<MAXB>& a, const GemvItem* items, int n, int uni
 
 // One-token launch of a planned GEMV (item table already in the plan's units).
 template <int MAXB>
-static cudaError_t launch_one_token(int kind, const GemvArgsT<MAXB>& a, const GemvPlan& p, cudaStream_t s) {
+static cudaError_t launch_one_token(int kind, const typename GemvArgsOf<MAXB>::Type& a, const GemvPlan& p, cudaStream_t s) {
   if (p.quarter) {
     switch (kind) {
       case kQ4_1: return launch_gemv_t<kQ4_1, MAXB, 1, true>(a, p, s);
@@ -1238,11 +1241,12 @@ int gemv_max_tokens(int kind) {
   }
 }
 
-cudaError_t launch_gemv_tokens(int kind, const GemvItem& item, int M, int out_f32, uint32_t* err, void* workspace,
-                               const DeviceInfo& info, cudaStream_t s) {
+// One weight against M tokens; MAXB 1, or 0 with an epilogue.
+template <int MAXB>
+static cudaError_t launch_tokens(int kind, typename GemvArgsOf<MAXB>::Type& a, const GemvItem& item, int M, int out_f32, uint32_t* err,
+                                 void* workspace, const DeviceInfo& info, cudaStream_t s) {
   if (M < 1 || M > gemv_max_tokens(kind)) return cudaErrorInvalidValue;
   const int MT = M == 1 ? 1 : M == 2 ? 2 : 4;
-  GemvArgsT<1> a;
   fill_items(a, &item, 1);
   GemvPlan p;
   if (!gemv_plan(kind, a.T, info, &p, MT, item.TC)) return cudaErrorInvalidValue;
@@ -1261,21 +1265,32 @@ cudaError_t launch_gemv_tokens(int kind, const GemvItem& item, int M, int out_f3
   a.top1_row_base = 0u;
   if (MT == 1) {                                  // one token: the single-GEMV kernel itself
     if (p.quarter) fill_items(a, &item, 1, 4);
-    return launch_one_token<1>(kind, a, p, s);
+    return launch_one_token<MAXB>(kind, a, p, s);
   }
   const bool xc = p.xslots > 0;
   if (MT == 2) {
     switch (kind) {
-      case kQ4_1: return xc ? launch_gemv_t<kQ4_1, 1, 2, false, true>(a, p, s) : launch_gemv_t<kQ4_1, 1, 2, false, false>(a, p, s);
-      case kQ4_K: return xc ? launch_gemv_t<kQ4_K, 1, 2, false, true>(a, p, s) : launch_gemv_t<kQ4_K, 1, 2, false, false>(a, p, s);
+      case kQ4_1: return xc ? launch_gemv_t<kQ4_1, MAXB, 2, false, true>(a, p, s) : launch_gemv_t<kQ4_1, MAXB, 2, false, false>(a, p, s);
+      case kQ4_K: return xc ? launch_gemv_t<kQ4_K, MAXB, 2, false, true>(a, p, s) : launch_gemv_t<kQ4_K, MAXB, 2, false, false>(a, p, s);
       default: return cudaErrorInvalidValue;
     }
   }
-  switch (kind) {
-    case kQ4_1: return xc ? launch_gemv_t<kQ4_1, 1, 4, false, true>(a, p, s) : launch_gemv_t<kQ4_1, 1, 4, false, false>(a, p, s);
-    case kQ4_K: return xc ? launch_gemv_t<kQ4_K, 1, 4, false, true>(a, p, s) : launch_gemv_t<kQ4_K, 1, 4, false, false>(a, p, s);
-    default: return cudaErrorInvalidValue;
+  if constexpr (MAXB == 1) {
+    if (kind == kQ4_1) return xc ? launch_gemv_t<kQ4_1, 1, 4, false, true>(a, p, s) : launch_gemv_t<kQ4_1, 1, 4, false, false>(a, p, s);
   }
+  if (kind != kQ4_K) return cudaErrorInvalidValue;
+  return xc ? launch_gemv_t<kQ4_K, MAXB, 4, false, true>(a, p, s) : launch_gemv_t<kQ4_K, MAXB, 4, false, false>(a, p, s);
+}
+
+cudaError_t launch_gemv_tokens(int kind, const GemvItem& item, int M, int out_f32, uint32_t* err, void* workspace,
+                               const DeviceInfo& info, cudaStream_t s, const Epilogue* ep) {
+  if (ep == nullptr) {
+    GemvArgsT<1> a;
+    return launch_tokens<1>(kind, a, item, M, out_f32, err, workspace, info, s);
+  }
+  GemvArgsEpilogue a;
+  a.ep = *ep;
+  return launch_tokens<0>(kind, a, item, M, out_f32, err, workspace, info, s);
 }
 
 }  // namespace q4nx

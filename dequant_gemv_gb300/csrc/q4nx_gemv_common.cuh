@@ -12,6 +12,7 @@
 #pragma once
 
 #include "q4nx_device.cuh"
+#include "q4nx_epilogue.cuh"
 #include "q4nx_kernels.h"
 
 namespace q4nx {
@@ -35,6 +36,7 @@ struct GemvItemDev {
 // that small launches do not carry a 12 KB parameter block).
 template <int MAXB>
 struct GemvArgsT {
+  static constexpr bool kEpilogue = false;
   GemvItemDev items[MAXB];
   int nitems;
   int grid;                // CTAs; CTA b owns units [T b / grid, T (b+1) / grid)
@@ -55,6 +57,19 @@ struct GemvArgsT {
   int64_t* top1_key_out;   // null, or where the key goes (top bit flipped: signed order = key order)
   uint64_t* top1_key;      // workspace word, zero between launches
   uint32_t* top1_done;     // workspace word, zero between launches
+};
+// One item whose sums pass an epilogue before they are stored: MAXB 0.
+struct GemvArgsEpilogue : GemvArgsT<1> {
+  static constexpr bool kEpilogue = true;
+  Epilogue ep;
+};
+template <int MAXB>
+struct GemvArgsOf {
+  using Type = GemvArgsT<MAXB>;
+};
+template <>
+struct GemvArgsOf<0> {
+  using Type = GemvArgsEpilogue;
 };
 
 

@@ -58,8 +58,10 @@ cudaError_t launch_gemv_top1(int kind, const GemvItem& item, int32_t* idx, int64
 // error word to report a failed wait in.
 constexpr int kGemvTokensQ41 = 2, kGemvTokensQ4K = 4, kGemvTokensQ8 = 1, kGemvTokensMax = 4;
 int gemv_max_tokens(int kind);
+// `ep`: what is done to the sums before they are stored (q4nx_epilogue.cuh).
+struct Epilogue;
 cudaError_t launch_gemv_tokens(int kind, const GemvItem& item, int M, int out_f32, uint32_t* err, void* workspace,
-                               const DeviceInfo& info, cudaStream_t s);
+                               const DeviceInfo& info, cudaStream_t s, const Epilogue* ep = nullptr);
 
 // ---- standalone decode ----
 cudaError_t launch_decode(int kind, const void* chunks, int64_t TR, int64_t TC, void* out, cudaStream_t s);
@@ -80,7 +82,7 @@ bool gemm_supports(int kind);
 uint64_t gemm_workspace_bytes(int64_t TR, int64_t TC, int M);
 // after_wait: a dependent launch that starts early finds what the grids before the GEMM wrote
 cudaError_t launch_gemm(int kind, const void* chunks, int64_t TR, int64_t TC, const void* X, int M, void* Y,
-                        int out_f32, void* workspace, cudaStream_t s, bool after_wait = false);
+                        int out_f32, void* workspace, cudaStream_t s, bool after_wait = false, const Epilogue* ep = nullptr);
 
 // ---- 4-bit key/value cache and the attention that reads it (q4nx_kv.cuh) ----
 struct KvPool;

@@ -6,9 +6,11 @@
 // by the kernels, which skip what is out of range and report it in the
 // workspace's error word.
 #include <cstdint>
+#include <utility>
 
 #include "../../include/q4nx.h"
 #include "q4nx_checks.h"
+#include "q4nx_epilogue.cuh"
 #include "q4nx_kernels.h"
 #include "q4nx_kv.cuh"
 
@@ -63,6 +65,8 @@ KvBatch batch_of(const q4nx_kv_batch* b) {
 
 constexpr int kMaxHeads = 1024;
 constexpr int64_t kMaxStride = int64_t(1) << 40;      // elements between rows: products of it stay in 64 bits
+
+constexpr int64_t kMaxSideStride = int64_t(1) << 38;  // of an epilogue's operands: a tensor map's strides have 40 bits of bytes
 
 // 32-bit words of the adapters' inner products and of the tokens in their order
 uint64_t lora_t(int64_t cols) { return static_cast<uint64_t>(lora_splits(cols)) * 64 * 128 + 128; }
@@ -187,6 +191,33 @@ int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_ad
     if ((st = q4nx_gemm_m64(w, X_dev, M, base, Q4NX_OUT_F32, workspace_dev, workspace_bytes, stream))) return st;
   }
   return from_cuda(launch_lora_expand(c, f32, s));
+}
+
+int q4nx_gemm_epilogue(const q4nx_weight* w, const void* X_dev, int M, const q4nx_epilogue* ep, void* Y_dev, int out_dtype,
+                       void* workspace_dev, uint64_t workspace_bytes, void* stream) {
+  int st = check_weight(w);
+  if (st) return st;
+  if (X_dev == nullptr || Y_dev == nullptr || ep == nullptr) return Q4NX_E_NULL;
+  if (M < 1 || M > 64) return Q4NX_E_M;
+  if (ep->reserved != 0) return Q4NX_E_KIND;
+  if (ep->act < Q4NX_ACT_NONE || ep->act > Q4NX_ACT_SILU) return Q4NX_E_UNSUPPORTED;
+  if (!known_out(out_dtype)) return Q4NX_E_DTYPE;
+  for (const auto& [p, stride] : {std::pair{ep->mul_dev, ep->mul_stride}, std::pair{ep->residual_dev, ep->residual_stride}}) {
+    if (p == nullptr) continue;
+    if (stride < w->rows || stride > kMaxSideStride) return Q4NX_E_SHAPE;
+    if (!aligned16(p) || stride % 8 != 0) return Q4NX_E_ALIGN;
+  }
+  if (!aligned16(X_dev) || !aligned16(Y_dev) || !aligned(ep->bias_dev, 2)) return Q4NX_E_ALIGN;
+  if (M > gemv_max_tokens(w->kind) && !gemm_supports(w->kind)) return Q4NX_E_UNSUPPORTED;
+  if ((st = check_workspace(workspace_dev, workspace_bytes, q4nx_gemm_workspace(w, M)))) return st;
+  Epilogue e;
+  e.bias = static_cast<const uint16_t*>(ep->bias_dev);
+  e.mul = static_cast<const uint16_t*>(ep->mul_dev);
+  e.residual = static_cast<const uint16_t*>(ep->residual_dev);
+  e.mul_stride = ep->mul_stride;
+  e.residual_stride = ep->residual_stride;
+  e.act = ep->act;
+  return launch_product(w, X_dev, M, Y_dev, out_dtype, workspace_dev, static_cast<cudaStream_t>(stream), &e);
 }
 
 int q4nx_logprobs(const void* logits_dev, int dtype, int M, int64_t V, int64_t stride, const int32_t* tokens_dev, int top,

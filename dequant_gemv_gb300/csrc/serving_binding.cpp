@@ -240,6 +240,60 @@ PyObject* gemm_lora(PyObject* const* a) {
   return THPVariable_Wrap(std::move(out));
 }
 
+// A bf16 [M, rows] operand of an epilogue, its rows contiguous: address and stride (NULL: none).
+const void* side(const at::Tensor* t, const char* name, int64_t M, int64_t rows, c10::Device dev, int64_t& stride) {
+  stride = rows;
+  if (t == nullptr) return nullptr;
+  if (t->scalar_type() != at::kBFloat16 || t->dim() != 2 || t->device() != dev || t->size(0) != M || t->size(1) != rows ||
+      (rows > 1 && t->stride(1) != 1))
+    throw Refused(std::string(name) + " must be a bf16 [M, rows] tensor on the weight's device, contiguous within a token");
+  if (M > 1) stride = t->stride(0);
+  return t->data_ptr();
+}
+
+// (chunks, kind, rows, cols, X, bias, act, mul, residual, out, out code, ws)
+PyObject* gemm_epilogue(PyObject* const* a) {
+  const at::Tensor &chunks = tensor(a[0], "chunks"), &x = tensor(a[4], "X");
+  if (!chunks.is_cuda() || !chunks.is_contiguous()) throw Refused("chunks must be a contiguous CUDA tensor");
+  const c10::Device dev = chunks.device();
+  q4nx_weight w;
+  w.chunks_dev = chunks.data_ptr();
+  w.bytes = static_cast<uint64_t>(chunks.nbytes());
+  w.kind = static_cast<int32_t>(integer(a[1]));
+  w.reserved = 0;
+  w.rows = integer(a[2]);
+  w.cols = integer(a[3]);
+  plain(x, "X", at::kBFloat16, 2, dev);
+  if (x.size(1) != w.cols) throw Refused("X must be [M, cols]");
+  const int64_t M = x.size(0), code = integer(a[10]);
+  const int m = static_cast<int>(M < INT32_MAX ? M : INT32_MAX);
+  if (m < 1 || m > 64) check(Q4NX_E_M, "q4nx_gemm_epilogue");
+  const at::Tensor *bias = tensor_or_none(a[5], "bias"), *given = tensor_or_none(a[9], "out");
+  q4nx_epilogue e;
+  if (bias != nullptr) {
+    plain(*bias, "bias", at::kBFloat16, 1, dev);
+    if (bias->numel() != w.rows) throw Refused("bias must have one entry per row");
+  }
+  e.bias_dev = bias != nullptr ? bias->data_ptr() : nullptr;
+  e.mul_dev = side(tensor_or_none(a[7], "mul"), "mul", M, w.rows, dev, e.mul_stride);
+  e.residual_dev = side(tensor_or_none(a[8], "residual"), "residual", M, w.rows, dev, e.residual_stride);
+  e.act = static_cast<int32_t>(integer(a[6]));
+  e.reserved = 0;
+  const int64_t shape[2] = {M, w.rows};
+  if (given != nullptr) {
+    plain(*given, "out", out_type(code), 2, dev);
+    if (given->size(0) != M || given->size(1) != w.rows) throw Refused("out must be [M, rows]");
+  }
+  const uint64_t need = q4nx_gemm_workspace(&w, m);
+  if (need == 0) check(Q4NX_E_SHAPE, "q4nx_gemm_epilogue");
+  const c10::cuda::CUDAGuard guard(dev);
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  const Workspace ws = workspace(a[11], "gemm", dev, s, need);
+  at::Tensor out = given != nullptr ? *given : empty(shape, out_type(code), dev);
+  check(q4nx_gemm_epilogue(&w, x.data_ptr(), m, &e, out.data_ptr(), static_cast<int>(code), ws.ptr, ws.bytes, s), "q4nx_gemm_epilogue");
+  return THPVariable_Wrap(std::move(out));
+}
+
 // (logits, tokens, top) -> (logprob, entropy, lse, top_idx, top_logprob)
 PyObject* logprobs(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0], "logits");
@@ -309,6 +363,7 @@ PyMethodDef g_methods[] = {method<setup, 3>("setup"),
                            method<kv_read, 9>("kv_read"),
                            method<kv_attention, 13>("kv_attention"),
                            method<gemm_lora, 13>("gemm_lora"),
+                           method<gemm_epilogue, 12>("gemm_epilogue"),
                            method<logprobs, 3>("logprobs"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -5,6 +5,7 @@
     q4nx_kv_read(cache, tokens, q_start, lens, table)            -> (k, v)
     q4nx_kv_attention(cache, q, q_start, lens, table, scale)     -> [tokens, heads, head_dim]
     q4nx_gemm_lora(w, X, Adapters(a, b, scale), ids)             -> [M, N]
+    q4nx_gemm_epilogue(w, X, bias, act, mul, residual)           -> [M, N]
     q4nx_logprobs(logits, tokens, top)                           -> Logprobs
 
 As in the rest of the binding, only arguments are marshalled; formulas,
@@ -58,6 +59,11 @@ class q4nx_adapters(ctypes.Structure):
                 ("count", ctypes.c_int32), ("rank", ctypes.c_int32)]
 
 
+class q4nx_epilogue(ctypes.Structure):
+    _fields_ = [("bias_dev", P), ("mul_dev", P), ("residual_dev", P), ("mul_stride", I64), ("residual_stride", I64),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _CACHE, _BATCH = ctypes.POINTER(q4nx_kv_cache), ctypes.POINTER(q4nx_kv_batch)
 for _name, (_args, _res) in {
     "q4nx_kv_page_bytes": ([I, I, I], U64),
@@ -67,13 +73,15 @@ for _name, (_args, _res) in {
     "q4nx_kv_attention": ([_CACHE, _BATCH, P, I64, I, F, I64, P, I, P, P, U64, P], I),
     "q4nx_gemm_lora": ([ctypes.POINTER(q4nx_weight), P, I, ctypes.POINTER(q4nx_adapters), P, P, I, P, U64, P, U64, P], I),
     "q4nx_gemm_lora_scratch": ([ctypes.POINTER(q4nx_weight), I], U64),
+    "q4nx_gemm_epilogue": ([ctypes.POINTER(q4nx_weight), P, I, ctypes.POINTER(q4nx_epilogue), P, I, P, U64, P], I),
     "q4nx_logprobs": ([P, I, I, I64, I64, P, I, P, P, P, P, P, P], I),
 }.items():
     _fn = getattr(lib, _name)
     _fn.argtypes, _fn.restype = _args, _res
 EXPORTS = ("q4nx_kv_page_bytes", "q4nx_kv_workspace", "q4nx_kv_append", "q4nx_kv_read", "q4nx_kv_attention",
-           "q4nx_gemm_lora", "q4nx_gemm_lora_scratch", "q4nx_logprobs")
+           "q4nx_gemm_lora", "q4nx_gemm_lora_scratch", "q4nx_gemm_epilogue", "q4nx_logprobs")
 Q4NX_MAX_TOP = 32
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}       # enum q4nx_act
 
 
 def q4nx_kv_page_bytes(head_dim: int, kv_heads: int, page_tokens: int) -> int:
@@ -163,6 +171,17 @@ def q4nx_gemm_lora(w: Weight, X: torch.Tensor, adapters: Adapters, ids: torch.Te
                    out_dtype="bf16", ws: torch.Tensor | None = None) -> torch.Tensor:
     """w X[m] plus the adapter ids[m] (int32, below 0: none) of every token, [M, rows]."""
     return _serving.gemm_lora(w.chunks, w.kind, w.rows, w.cols, X, *adapters._fits, ids, out, _out_code(out_dtype), ws)
+
+
+def q4nx_gemm_epilogue(w: Weight, X: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none", mul: torch.Tensor | None = None,
+                       residual: torch.Tensor | None = None, out: torch.Tensor | None = None, out_dtype="bf16",
+                       ws: torch.Tensor | None = None) -> torch.Tensor:
+    """act(w X[m] + bias) * mul[m] + residual[m], [M, rows]; bias bf16 [rows], mul and residual bf16 [M, rows].
+
+    act: one of ACTIVATIONS; out may be mul or residual (a contiguous bf16 one)."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}")
+    return _serving.gemm_epilogue(w.chunks, w.kind, w.rows, w.cols, X, bias, ACTIVATIONS[act], mul, residual, out, _out_code(out_dtype), ws)
 
 
 class Logprobs(NamedTuple):

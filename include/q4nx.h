@@ -335,6 +335,36 @@ int q4nx_gemm_lora(const q4nx_weight* w, const void* X_dev, int M, const q4nx_ad
                    uint64_t scratch_bytes, void* stream);
 uint64_t q4nx_gemm_lora_scratch(const q4nx_weight* w, int M);
 
+/* What is done to a product's sums before they are rounded:
+ *   Y[m] = act(w X[m] + bias) * mul[m] + residual[m],  each step in binary32.
+ * What is NULL is left out.  mul may be another projection's output (the up half beside a
+ * gate), residual the stream that the layer adds to; either may be Y_dev itself where Y is
+ * bf16 and the strides agree (strides: rows).  Other overlaps with Y are not allowed. */
+enum q4nx_act {
+    Q4NX_ACT_NONE = 0,
+    Q4NX_ACT_RELU = 1,        /* x below 0 becomes 0, NaN stays                    */
+    Q4NX_ACT_GELU = 2,        /* x Phi(x)                                          */
+    Q4NX_ACT_GELU_TANH = 3,   /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))     */
+    Q4NX_ACT_SILU = 4         /* x / (1 + exp(-x))                                 */
+};
+typedef struct q4nx_epilogue {
+    const void* bias_dev;     /* bf16 [rows], 2-byte aligned, or NULL              */
+    const void* mul_dev;      /* bf16 [M][rows], 16-byte aligned, or NULL          */
+    const void* residual_dev; /* bf16 [M][rows], 16-byte aligned, or NULL          */
+    int64_t mul_stride;       /* elements from token to token: a multiple of 8, at least rows */
+    int64_t residual_stride;
+    int32_t act;              /* enum q4nx_act                                     */
+    int32_t reserved;         /* must be 0                                         */
+} q4nx_epilogue;
+
+/* q4nx_gemm_m64 with an epilogue: kinds, M, X, Y, out_dtype and workspace as there, the
+ * sums those that q4nx_gemm_m64 with Q4NX_OUT_F32 gives.  Q4NX_E_UNSUPPORTED for an unknown
+ * activation.  An activation is within 2^-20, relative, of its value at a number within 2^-21,
+ * relative, of the sum, as far as that is a normal number; at an infinite sum it is what
+ * x / (1 + exp(-z)) gives in IEEE arithmetic (x Phi(x) for GELU). */
+int q4nx_gemm_epilogue(const q4nx_weight* w, const void* X_dev, int M, const q4nx_epilogue* epilogue, void* Y_dev,
+                       int out_dtype, void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
 /* Log-probabilities of rows of logits (dtype Q4NX_OUT_F32 or Q4NX_OUT_BF16, [M][V], `stride`
  * elements from row to row, no alignment beyond the element's):
  *   lse = log sum exp x;  logprob[m] = x[tokens[m]] - lse;
