@@ -91,6 +91,18 @@ constexpr int kKvMaxBatch = 1024;                 // requests per call
 constexpr int kKvMaxCtas = 304;                   // CTAs of an attention launch, at most
 cudaError_t launch_kv_append(int D, const KvPool& p, const KvBatch& kb, const void* k, const void* v, int64_t stride,
                              uint32_t* err, cudaStream_t s);
+struct RotaryCall {
+  const uint16_t *q, *k, *v;   // bf16 rows of tokens
+  uint16_t* q_out;
+  int64_t q_stride, q_out_stride, kv_stride;   // elements from token to token
+  const float2* table;         // [positions][half] cosine and sine
+  int64_t positions;
+  int half;                    // pairs of channels that are turned
+  int interleaved;             // pairs are (2j, 2j + 1), else (j, j + half)
+  int heads;                   // query heads; 0: no queries
+  uint32_t* err;
+};
+cudaError_t launch_kv_append_rotary(int D, const KvPool& p, const KvBatch& kb, const RotaryCall& c, cudaStream_t s);
 cudaError_t launch_kv_read(int D, const KvPool& p, const KvBatch& kb, void* k, void* v, int out_f32, uint32_t* err,
                            cudaStream_t s);
 uint64_t attention_workspace_bytes(int D);

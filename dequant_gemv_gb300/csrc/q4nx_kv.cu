@@ -16,7 +16,7 @@
 // out per value, 2.7 us of these); what keeps it from them are latencies: the request's look-up
 // before the loads, a lane's 64 bytes apart from the next lane's, 2-byte stores of scales.
 #include "q4nx_kernels.h"
-#include "q4nx_kv.cuh"
+#include "q4nx_kv_store.cuh"
 
 namespace q4nx {
 
@@ -24,26 +24,6 @@ namespace {
 
 constexpr int kKvWarps = 8;      // warps per CTA of the append and read kernels
 constexpr int64_t kFullItems = 6144;   // (token, head) pairs from which on larger items pay: below, too few warps have work
-
-// clamp(rint((x - m) / s), -8, 7) + 8 with the quotient correctly rounded; `inv` is
-// about 1 / s.  The product with it is within 2^-21 of the quotient, relative,
-// so where it is at least 2^-13 from a tie both round alike (|quotient| < 2^7
-// or the clamp decides); elsewhere, and where 1 / s is no number, the division is done.
-__device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv) {
-  const float d = __fsub_rn(x, m);
-  const float q = d * inv;
-  float c = rintf(q);
-  if (!(fabsf(fabsf(q - c) - 0.5f) > 0x1p-13f) || !(fabsf(q) < 128.f)) c = s == 0.f ? 0.f : rintf(__fdiv_rn(d, s));
-  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -8.f), 7.f)) + 8);
-}
-// Scale and middle of a group with smallest and largest value lo, hi; `bad`: one is no number.
-__device__ __forceinline__ void scale_of(float lo, float hi, bool bad, uint32_t& s_bits, uint32_t& m_bits) {
-  s_bits = f32_to_bf16_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-  const float s = bf16_bits_to_f32(s_bits);
-  m_bits = f32_to_bf16_bits(__fadd_rn(lo, __fmul_rn(8.0f, s)));
-  const float inf = __int_as_float(0x7f800000);
-  if (bad || !(fabsf(s) < inf) || !(fabsf(bf16_bits_to_f32(m_bits)) < inf)) s_bits = m_bits = 0x7FC0;
-}
 
 // One warp per (token, kv head).  Lane l holds channels VPL*l .. of the head.
 template <int D>
@@ -87,56 +67,9 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(KvPool pool, K
       x[j] = bf16_bits_to_f32(w & 0xFFFF);
       x[j + 1] = bf16_bits_to_f32(w >> 16);
     }
-    float lo = x[0], hi = x[0];
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      lo = fminf(lo, x[j]);
-      hi = fmaxf(hi, x[j]);
-      bad |= !(fabsf(x[j]) < __int_as_float(0x7f800000));
-    }
-#pragma unroll
-    for (int o = 1; o < LPG; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), o) != 0;
-    }
-    uint32_t s_bits, m_bits;
-    scale_of(lo, hi, bad, s_bits, m_bits);
-    const float s = bf16_bits_to_f32(s_bits), m = bf16_bits_to_f32(m_bits), inv = 1.f / s;
-    if (lane % LPG == 0) {
-      const int g = lane / LPG;
-      uint16_t* sc = reinterpret_cast<uint16_t*>(blk + (which ? 18 : 16) * D);
-      sc[t * NG + g] = static_cast<uint16_t>(s_bits);
-      sc[D / 2 + (which ? g * kKvBlock + t : t * NG + g)] = static_cast<uint16_t>(m_bits);
-    }
-    __syncwarp();                                               // the codes of K are read out
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) codes[warp][lane * VPL + j] = static_cast<uint8_t>(code_of(x[j], m, s, inv));
-    __syncwarp();
-    if (which == 0) {
-      if (lane < D / 8) {                                       // channels 8*lane ..: group lane/4, i lane%4
-        const uint2 c = *reinterpret_cast<const uint2*>(&codes[warp][8 * lane]);
-        uint32_t w = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t two = (j < 2 ? c.x : c.y) >> (16 * (j & 1));
-          w |= (two & 15) << (4 * j) | (two >> 8 & 15) << (4 * j + 16);
-        }
-        *reinterpret_cast<uint32_t*>(blk + kv_k_word(D, t, lane & 3, lane >> 2)) = w;
-      }
-    } else {
-#pragma unroll
-      for (int n = lane; n < D / 2; n += 32) {
-        const int mt = n >> 3, r = n & 7;
-        blk[kv_v_byte(D, t, mt, r)] = static_cast<uint8_t>(codes[warp][16 * mt + r] | codes[warp][16 * mt + r + 8] << 4);
-      }
-    }
+    keep_token<D>(blk, t, which, x, codes[warp]);
   }
 }
-
-// A request's tokens lie in T/16 + 2 blocks at most.
-__host__ __device__ __forceinline__ int64_t most_blocks(const KvBatch& kb) { return kb.tokens / kKvBlock + 2 * kb.batch; }
 
 // One warp per (16-token block that the call writes, kv head, keys or values,
 // pair of groups): lane 2t + e holds one group of token t, so that no lane
@@ -158,31 +91,8 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_blocks_kernel(KvPool 
     if (left == most_blocks(kb) && item % (NG * pool.kv_heads) == 0) kv_report(kb, pool.page_blocks, err);
     return;
   }
-  // the request: 32 at a time, their block counts added up across the lanes
-  int b = -1;
-  KvRequest rq = {};
-  for (int b0 = 0; b0 < kb.batch && b < 0; b0 += 32) {
-    const KvRequest r = b0 + lane < kb.batch ? kv_request(kb, pool.page_blocks, b0 + lane) : KvRequest{0, 0, 0, true};
-    const int64_t from = r.L > r.T ? r.L - r.T : 0;             // tokens at positions below 0 are not kept
-    const int64_t n = r.T > 0 && r.L > from ? (r.L - 1) / kKvBlock - from / kKvBlock + 1 : 0;
-    int64_t end = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += u;
-    }
-    const uint32_t here = __ballot_sync(0xffffffffu, left < end);
-    if (here != 0) {
-      const int src = __ffs(here) - 1;
-      b = b0 + src;
-      left -= __shfl_sync(0xffffffffu, end - n, src);
-      rq.q0 = __shfl_sync(0xffffffffu, r.q0, src);
-      rq.T = __shfl_sync(0xffffffffu, r.T, src);
-      rq.L = __shfl_sync(0xffffffffu, r.L, src);
-    } else {
-      left -= __shfl_sync(0xffffffffu, end, 31);
-    }
-  }
+  int b;
+  const KvRequest rq = locate_block(kb, pool.page_blocks, left, b);
   if (b < 0) return;
   const int64_t from = rq.L > rq.T ? rq.L - rq.T : 0, blk_at = from / kKvBlock + left;
   uint8_t* blk = kv_block_ptr(pool, kb, D, b, h, blk_at);
@@ -210,45 +120,8 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_blocks_kernel(KvPool 
     hi = fmaxf(hi, fmaxf(x, y));
     bad |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
   }
-  uint32_t s_bits, m_bits;
-  scale_of(lo, hi, bad, s_bits, m_bits);
-  const float s = bf16_bits_to_f32(s_bits), m = bf16_bits_to_f32(m_bits), inv = 1.f / s;
-  uint32_t c[4] = {};                                           // channel 8i + 2j, +1 of the group: nibbles j, j + 4 of c[i]
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t x = code_of(__uint_as_float(w[j] << 16), m, s, inv), y = code_of(__uint_as_float(w[j] & 0xFFFF0000u), m, s, inv);
-    c[j >> 2] |= x << (4 * (j & 3)) | y << (4 * (j & 3) + 16);
-  }
-  uint16_t* sc = reinterpret_cast<uint16_t*>(blk + (which ? 18 : 16) * D);
-  if (mine) {
-    sc[t * NG + g] = static_cast<uint16_t>(s_bits);
-    sc[D / 2 + (which ? g * kKvBlock + t : t * NG + g)] = static_cast<uint16_t>(m_bits);
-  }
-  if (which == 0) {
-    if (mine)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(blk + kv_k_word(D, t, i, g)) = c[i];
-    return;
-  }
-  // byte (mt, r): channels r and r + 8 of the 16 of tile mt = 2g + m2: words 2*m2, 2*m2 + 1 of c
-  const int base = 8 * D + 512 * pair;
-#pragma unroll
-  for (int m2 = 0; m2 < 2; ++m2)
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int at = 4 * (r >> 1) + 16 * (r & 1);
-      const uint32_t byte = (c[2 * m2] >> at & 15) | (c[2 * m2 + 1] >> at & 15) << 4;
-      image[warp][kv_v_byte(D, t, 2 * g + m2, r) - base] = static_cast<uint8_t>(byte);
-    }
-  __syncwarp();
-  if (blk_at * kKvBlock >= from && blk_at * kKvBlock + kKvBlock <= rq.L) {
-    reinterpret_cast<uint4*>(blk + base)[lane] = reinterpret_cast<const uint4*>(image[warp])[lane];
-  } else if (mine) {                                            // other tokens' bytes stay as they are
-    for (int n = 0; n < 16; ++n) {
-      const int at = kv_v_byte(D, t, 2 * g + (n >> 3), n & 7);
-      blk[at] = image[warp][at - base];
-    }
-  }
+  keep_group<D>(blk, blk_at * kKvBlock >= from && blk_at * kKvBlock + kKvBlock <= rq.L, mine, t, g, which, lo, hi, bad,
+                [&](int j) { return j & 1 ? __uint_as_float(w[j >> 1] & 0xFFFF0000u) : __uint_as_float(w[j >> 1] << 16); }, image[warp]);
 }
 
 // One warp per (token, HEADS kv heads), which share its look-ups; lane l writes
@@ -311,23 +184,6 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_read_kernel(KvPool pool, KvB
       }
     }
   }
-}
-
-template <typename... P, typename... A>
-cudaError_t launch(void (*f)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
-  // programmatic dependent launch: the CTAs start while the previous grid
-  // drains and wait for it before their first load
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, static_cast<P>(args)...);
 }
 
 }  // namespace

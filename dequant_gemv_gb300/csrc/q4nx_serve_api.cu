@@ -101,6 +101,45 @@ int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const
                                     static_cast<uint32_t*>(workspace_dev), static_cast<cudaStream_t>(stream)));
 }
 
+int q4nx_kv_append_rotary(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const q4nx_rotary* ro, const void* q_dev,
+                          int64_t q_stride, int heads, void* q_out_dev, int64_t q_out_stride, const void* k_dev,
+                          const void* v_dev, int64_t kv_stride, void* workspace_dev, uint64_t workspace_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st == Q4NX_OK) st = check_batch(batch);
+  if (st) return st;
+  if (ro == nullptr || ro->table_dev == nullptr || k_dev == nullptr || v_dev == nullptr) return Q4NX_E_NULL;
+  if (q_dev != nullptr && q_out_dev == nullptr) return Q4NX_E_NULL;
+  if (ro->interleaved != 0 && ro->interleaved != 1) return Q4NX_E_UNSUPPORTED;
+  if (ro->dims < 16 || ro->dims > cache->head_dim || ro->dims % 16 != 0) return Q4NX_E_SHAPE;
+  if (ro->positions < 1 || ro->positions > INT32_MAX) return Q4NX_E_SHAPE;
+  if (ro->bytes / (static_cast<uint64_t>(ro->dims) * 4) < static_cast<uint64_t>(ro->positions)) return Q4NX_E_SHORT;
+  if (kv_stride < static_cast<int64_t>(cache->kv_heads) * cache->head_dim || kv_stride > kMaxStride) return Q4NX_E_SHAPE;
+  if (!aligned16(ro->table_dev) || !aligned16(k_dev) || !aligned16(v_dev) || kv_stride % 8 != 0) return Q4NX_E_ALIGN;
+  if (q_dev != nullptr) {
+    const int64_t row = static_cast<int64_t>(heads) * cache->head_dim;
+    if (heads < 1 || heads > kMaxHeads) return Q4NX_E_SHAPE;
+    if (q_stride < row || q_stride > kMaxStride || q_out_stride < row || q_out_stride > kMaxStride) return Q4NX_E_SHAPE;
+    if (!aligned16(q_dev) || !aligned16(q_out_dev) || q_stride % 8 != 0 || q_out_stride % 8 != 0) return Q4NX_E_ALIGN;
+  }
+  if ((st = check_workspace(workspace_dev, workspace_bytes, q4nx_kv_workspace(cache)))) return st;
+  if (batch->tokens == 0) return Q4NX_OK;
+  RotaryCall c;
+  c.q = static_cast<const uint16_t*>(q_dev);
+  c.k = static_cast<const uint16_t*>(k_dev);
+  c.v = static_cast<const uint16_t*>(v_dev);
+  c.q_out = static_cast<uint16_t*>(q_out_dev);
+  c.q_stride = q_stride;
+  c.q_out_stride = q_out_stride;
+  c.kv_stride = kv_stride;
+  c.table = reinterpret_cast<const float2*>(ro->table_dev);
+  c.positions = ro->positions;
+  c.half = ro->dims / 2;
+  c.interleaved = ro->interleaved;
+  c.heads = q_dev != nullptr ? heads : 0;
+  c.err = static_cast<uint32_t*>(workspace_dev);
+  return from_cuda(launch_kv_append_rotary(cache->head_dim, pool_of(cache), batch_of(batch), c, static_cast<cudaStream_t>(stream)));
+}
+
 int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k_dev, void* v_dev, int out_dtype,
                  void* workspace_dev, uint64_t workspace_bytes, void* stream) {
   int st = check_cache(cache);

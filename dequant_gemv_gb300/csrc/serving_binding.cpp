@@ -152,6 +152,45 @@ PyObject* kv_append(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// (cache, pool, ws_bytes, rotary, its table, q, k, v, q_start, lens, table, out, ws) -> the turned queries, or None
+PyObject* kv_append_rotary(PyObject* const* a) {
+  const Cache cache = cache_of(a[0], a[1]);
+  const q4nx_rotary* ro = reinterpret_cast<const q4nx_rotary*>(static_cast<uintptr_t>(integer(a[3])));
+  if (tensor(a[4], "the rotary's table").device() != cache.dev) throw Refused("the rotary's table must be on the cache's device");
+  const at::Tensor *q = tensor_or_none(a[5], "q"), *given = tensor_or_none(a[11], "out");
+  const at::Tensor &k = tensor(a[6], "k"), &v = tensor(a[7], "v");
+  const int64_t dim = cache.c->head_dim;
+  const Rows r = token_rows(k, "k", dim, cache.dev), rv = token_rows(v, "v", dim, cache.dev);
+  if (r.tokens != rv.tokens || r.heads != rv.heads || r.stride != rv.stride || r.heads != cache.c->kv_heads)
+    throw Refused("k and v must be [tokens, kv_heads, head_dim] with the same strides");
+  Rows rq = {r.tokens, 0, 0}, ro_rows = rq;
+  if (q != nullptr) {
+    rq = token_rows(*q, "q", dim, cache.dev);
+    if (rq.tokens != r.tokens || rq.heads < 1) throw Refused("q must be [tokens, heads, head_dim] of k's tokens");
+    if (given != nullptr) {
+      ro_rows = token_rows(*given, "out", dim, cache.dev);
+      if (given->sizes() != q->sizes()) throw Refused("out must have q's shape");
+    } else {
+      ro_rows = {rq.tokens, rq.heads, rq.heads * dim};
+    }
+  } else if (given != nullptr) {
+    throw Refused("out is for the queries: there are none");
+  }
+  const q4nx_kv_batch b = batch_of(a + 8, r.tokens, cache.dev);
+  const c10::cuda::CUDAGuard guard(cache.dev);
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(cache.dev.index()).stream();
+  const Workspace ws = workspace(a[12], "kv", cache.dev, s, static_cast<uint64_t>(integer(a[2])));
+  at::Tensor out;
+  if (q != nullptr) out = given != nullptr ? *given : empty(q->sizes(), at::kBFloat16, cache.dev);
+  if (r.tokens > 0)
+    check(q4nx_kv_append_rotary(cache.c, &b, ro, q != nullptr ? q->data_ptr() : nullptr, rq.stride, static_cast<int>(rq.heads),
+                                q != nullptr ? out.data_ptr() : nullptr, ro_rows.stride, k.data_ptr(), v.data_ptr(), r.stride, ws.ptr,
+                                ws.bytes, s),
+          "q4nx_kv_append_rotary");
+  if (q == nullptr) Py_RETURN_NONE;
+  return THPVariable_Wrap(std::move(out));
+}
+
 // (cache, pool, ws_bytes, tokens, q_start, lens, table, out code, ws)
 PyObject* kv_read(PyObject* const* a) {
   const Cache cache = cache_of(a[0], a[1]);
@@ -360,6 +399,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<setup, 3>("setup"),
                            method<kv_append, 9>("kv_append"),
+                           method<kv_append_rotary, 13>("kv_append_rotary"),
                            method<kv_read, 9>("kv_read"),
                            method<kv_attention, 13>("kv_attention"),
                            method<gemm_lora, 13>("gemm_lora"),

@@ -2,6 +2,7 @@
 
     KVCache.alloc(pages, kv_heads, head_dim, page_tokens, device)
     q4nx_kv_append(cache, k, v, q_start, lens, table)
+    q4nx_kv_append_rotary(cache, Rotary(table), q, k, v, q_start, lens, table) -> turned q
     q4nx_kv_read(cache, tokens, q_start, lens, table)            -> (k, v)
     q4nx_kv_attention(cache, q, q_start, lens, table, scale)     -> [tokens, heads, head_dim]
     q4nx_gemm_lora(w, X, Adapters(a, b, scale), ids)             -> [M, N]
@@ -59,6 +60,10 @@ class q4nx_adapters(ctypes.Structure):
                 ("count", ctypes.c_int32), ("rank", ctypes.c_int32)]
 
 
+class q4nx_rotary(ctypes.Structure):
+    _fields_ = [("table_dev", P), ("bytes", U64), ("positions", I64), ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 class q4nx_epilogue(ctypes.Structure):
     _fields_ = [("bias_dev", P), ("mul_dev", P), ("residual_dev", P), ("mul_stride", I64), ("residual_stride", I64),
                 ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
@@ -69,6 +74,7 @@ for _name, (_args, _res) in {
     "q4nx_kv_page_bytes": ([I, I, I], U64),
     "q4nx_kv_workspace": ([_CACHE], U64),
     "q4nx_kv_append": ([_CACHE, _BATCH, P, P, I64, P, U64, P], I),
+    "q4nx_kv_append_rotary": ([_CACHE, _BATCH, ctypes.POINTER(q4nx_rotary), P, I64, I, P, I64, P, P, I64, P, U64, P], I),
     "q4nx_kv_read": ([_CACHE, _BATCH, P, P, I, P, U64, P], I),
     "q4nx_kv_attention": ([_CACHE, _BATCH, P, I64, I, F, I64, P, I, P, P, U64, P], I),
     "q4nx_gemm_lora": ([ctypes.POINTER(q4nx_weight), P, I, ctypes.POINTER(q4nx_adapters), P, P, I, P, U64, P, U64, P], I),
@@ -78,7 +84,7 @@ for _name, (_args, _res) in {
 }.items():
     _fn = getattr(lib, _name)
     _fn.argtypes, _fn.restype = _args, _res
-EXPORTS = ("q4nx_kv_page_bytes", "q4nx_kv_workspace", "q4nx_kv_append", "q4nx_kv_read", "q4nx_kv_attention",
+EXPORTS = ("q4nx_kv_page_bytes", "q4nx_kv_workspace", "q4nx_kv_append", "q4nx_kv_append_rotary", "q4nx_kv_read", "q4nx_kv_attention",
            "q4nx_gemm_lora", "q4nx_gemm_lora_scratch", "q4nx_gemm_epilogue", "q4nx_logprobs")
 Q4NX_MAX_TOP = 32
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}       # enum q4nx_act
@@ -125,6 +131,46 @@ def q4nx_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, q_start: to
                    table: torch.Tensor, ws: torch.Tensor | None = None) -> None:
     """Quantize new keys and values (bf16 [tokens, kv_heads, head_dim]) into the cache; lens counts them already."""
     _serving.kv_append(cache._at, cache.pool, cache._ws_bytes, k, v, q_start, lens, table, ws)
+
+
+@dataclass(frozen=True)
+class Rotary:
+    """Cosines and sines of the positions: fp32 [positions, dims / 2, 2].
+
+    The first dims channels of a head are turned, in pairs (j, j + dims / 2), or (2j, 2j + 1) where interleaved."""
+    table: torch.Tensor
+    interleaved: bool = False
+
+    def __post_init__(self):
+        t = self.table
+        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[2] != 2 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("table must be a contiguous fp32 CUDA tensor [positions, dims / 2, 2]")
+        c = q4nx_rotary(t.data_ptr(), t.numel() * 4, t.shape[0], 2 * t.shape[1], int(bool(self.interleaved)))
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_at", ctypes.addressof(c))
+
+    @classmethod
+    def make(cls, positions: int, dims: int, base: float = 10000.0, frequencies: torch.Tensor | None = None,
+             interleaved: bool = False, device="cuda") -> "Rotary":
+        """The table of angles position * frequencies[j] (base ** (-2j / dims) by default), computed in 64 bits."""
+        if frequencies is None:
+            frequencies = base ** (-2 * torch.arange(dims // 2, dtype=torch.float64, device=device) / dims)
+        if frequencies.shape != (dims // 2,):
+            raise ValueError("frequencies must be [dims / 2]")
+        angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * frequencies.to(device=device, dtype=torch.float64)
+        return cls(torch.stack([angle.cos(), angle.sin()], -1).float(), interleaved)
+
+    def c(self) -> q4nx_rotary:
+        return self._c
+
+
+def q4nx_kv_append_rotary(cache: KVCache, rotary: Rotary, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+                          lens: torch.Tensor, table: torch.Tensor, out: torch.Tensor | None = None,
+                          ws: torch.Tensor | None = None) -> torch.Tensor | None:
+    """q4nx_kv_append with keys and queries (bf16 [tokens, heads, head_dim], or None) turned by their positions; the turned queries.
+
+    out: their place (it may be q)."""
+    return _serving.kv_append_rotary(cache._at, cache.pool, cache._ws_bytes, rotary._at, rotary.table, q, k, v, q_start, lens, table, out, ws)
 
 
 def q4nx_kv_read(cache: KVCache, tokens: int, q_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,

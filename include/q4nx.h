@@ -279,6 +279,32 @@ uint64_t q4nx_kv_workspace(const q4nx_kv_cache* cache);
 int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* k_dev, const void* v_dev,
                    int64_t kv_stride, void* workspace_dev, uint64_t workspace_bytes, void* stream);
 
+/* Cosines and sines of the positions' angles, made once by the caller (in 64 bits: far
+ * positions times a frequency lose their angle in 32): table_dev fp32 [positions][dims/2][2],
+ * (cosine, sine) of pair j at a position.  The first `dims` channels of a head are turned,
+ * in pairs (j, j + dims/2), or (2j, 2j + 1) where interleaved is 1; the others stay. */
+typedef struct q4nx_rotary {
+    const float* table_dev;   /* device, 16-byte aligned                           */
+    uint64_t bytes;           /* length of the table                               */
+    int64_t positions;        /* 1..INT32_MAX                                      */
+    int32_t dims;             /* a multiple of 16, 16..head_dim                    */
+    int32_t interleaved;      /* 0 or 1                                            */
+} q4nx_rotary;
+
+/* q4nx_kv_append with the call's keys, and its queries, turned by their positions on the way:
+ *   a' = a cos - b sin,  b' = b cos + a sin,  each step one IEEE binary32 operation.
+ * Keys are quantised from these binary32 numbers by the rule of q4nx_kv_append, values
+ * as there.  q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token, or NULL
+ * (keys alone; heads and the q_out arguments are not looked at).  q_out_dev: the turned queries, rounded
+ * to bf16, q_out_stride elements from token to token; it may be q_dev itself with its stride,
+ * other overlaps with the inputs are not allowed.  Strides are multiples of 8.  heads: 1..1024, any number.
+ * A token whose position the table does not reach is not kept, nor its queries written, and
+ * is reported as Q4NX_E_INDEX by q4nx_check; query rows of tokens of no request or at
+ * positions below 0 are not written. */
+int q4nx_kv_append_rotary(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const q4nx_rotary* rotary, const void* q_dev,
+                          int64_t q_stride, int heads, void* q_out_dev, int64_t q_out_stride, const void* k_dev,
+                          const void* v_dev, int64_t kv_stride, void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
 /* The cached values of the call's tokens: k_dev, v_dev [tokens][kv_heads][head_dim]
  * of out_dtype.  (code - 8) * scale is exact in binary32 and the addition of
  * mid rounds once, bf16 once more; zero for tokens at positions below 0 or of no request. */

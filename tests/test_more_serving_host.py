@@ -1,5 +1,5 @@
-"""Host-side checks of the epilogue product (no GPU needed): the documented status for every
-bad argument, before any CUDA call."""
+"""Host-side checks of the epilogue product and of the append with a rotation (no GPU needed):
+the documented status for every bad argument, before any CUDA call."""
 import ctypes
 
 import pytest
@@ -42,6 +42,46 @@ def test_epilogue_refuses(q):
     assert call(w=q.q4nx_weight(P, 1 << 30, q.Q4NX_Q4_1, 0, 63, 512)) == 3
     assert call(w=q.q4nx_weight(P, 1 << 30, 7, 0, 64, 512)) == 2
     assert call(w=q.q4nx_weight(P, 1 << 30, q.Q4NX_Q4_K, 0, 64, 512)) == 8        # no tensor-core path for this kind
+
+
+def test_append_rotary_refuses(q):
+    L, by = q.lib, ctypes.byref
+    cache = dict(pool=P, nbytes=1 << 30, dim=128, heads=8, page=64, reserved=0, pages=10)
+    batch = dict(a=P, b=P, c=P, batch=3, cols=4, tokens=3)
+    need = L.q4nx_kv_workspace(by(q.q4nx_kv_cache(*cache.values())))
+
+    def call(c=cache, b=batch, table=P, nbytes=1 << 30, positions=1000, dims=128, inter=0, qx=P, qs=4096, heads=32, out=P, os=4096, k=P, v=P,
+             kvs=1024, ws=P, n=need):
+        r = q.q4nx_rotary(table, nbytes, positions, dims, inter)
+        return L.q4nx_kv_append_rotary(None if c is None else by(q.q4nx_kv_cache(*c.values())), None if b is None else by(q.q4nx_kv_batch(*b.values())),
+                                       by(r), qx, qs, heads, out, os, k, v, kvs, ws, n, None)
+
+    assert call(c=None) == 1 and call(b=None) == 1 and call(c=dict(cache, dim=96)) == 3 and call(b=dict(batch, batch=0)) == 3
+    assert call(b=dict(batch, b=None)) == 1 and call(c=dict(cache, nbytes=10)) == 4 and call(c=dict(cache, reserved=3)) == 2
+    assert L.q4nx_kv_append_rotary(by(q.q4nx_kv_cache(*cache.values())), by(q.q4nx_kv_batch(*batch.values())), None, P, 4096, 32, P, 4096, P, P,
+                                   1024, P, need, None) == 1
+    for name in ("table", "k", "v", "out"):
+        assert call(**{name: None}) == 1, name
+    assert [call(inter=i) for i in (-1, 2)] == [8, 8]
+    assert [call(dims=d) for d in (0, 8, 24, 144, -16)] == [3] * 5 and [call(positions=p) for p in (0, -1, 1 << 31)] == [3] * 3
+    assert call(nbytes=1000 * 512 - 1) == 4 and call(dims=16, nbytes=1000 * 64 - 1) == 4
+    assert [call(heads=h) for h in (0, -1, 1025)] == [3] * 3
+    assert call(kvs=1016) == 3 and call(kvs=1028) == 5 and call(kvs=1 << 41) == 3
+    assert call(qs=4088) == 3 and call(qs=4100) == 5 and call(os=4088) == 3 and call(os=4100) == 5 and call(os=1 << 41) == 3
+    for name in ("table", "qx", "out", "k", "v", "ws"):
+        assert call(**{name: P + 8}) == 5, name
+    assert call(ws=None) == 7 and call(n=need - 1) == 7
+    # without queries theirs are not looked at; nothing to do is accepted without a launch
+    assert call(qx=None, out=None, heads=0, qs=0, os=3, ws=None) == 7 and call(b=dict(batch, tokens=0)) == 0
+    assert call(heads=5, qs=640, os=640, b=dict(batch, tokens=0)) == 0            # any number of heads
+
+
+def test_rotary_binding_refuses(q):
+    for t in (torch.zeros(4, 8, 2), torch.zeros(4, 8, 2, dtype=torch.float64), torch.zeros(4, 16)):
+        with pytest.raises(ValueError):
+            q.Rotary(t)
+    with pytest.raises(ValueError, match="frequencies"):
+        q.Rotary.make(4, 32, frequencies=torch.ones(15, dtype=torch.float64), device="cpu")
 
 
 def test_epilogue_binding_refuses(q):
