@@ -16,7 +16,8 @@ Functions keep the C names:
     q4nx_argmax(logits, out=None)                -> int32 [M]
 
 and, from ``serving.py``, the operators around the products in a decode step
-(q4nx_kv_append, q4nx_kv_append_rotary, q4nx_kv_read, q4nx_kv_attention, q4nx_gemm_lora, q4nx_gemm_epilogue, q4nx_logprobs).
+(q4nx_kv_append, q4nx_kv_append_rotary, q4nx_kv_read, q4nx_kv_attention, q4nx_kv_attention_cross,
+q4nx_kv_attention_shared, q4nx_gemm_lora, q4nx_gemm_epilogue, q4nx_logprobs).
 
 ``w`` is a :class:`Weight`: a uint8 CUDA tensor of chunk bytes plus kind, rows
 and cols (the tile grid of the "Q4NX chunks" section of the 1bit engine
@@ -468,7 +469,8 @@ def q4nx_check(ws: torch.Tensor | None = None, device=None) -> None:
 from . import serving  # noqa: E402  (needs the names above; its calls refuse where _serving.so has not been built)
 from .serving import (ACTIVATIONS, Adapters, KVCache, Logprobs, Q4NX_MAX_TOP, Rotary, q4nx_adapters, q4nx_epilogue,  # noqa: E402,F401
                       q4nx_gemm_epilogue, q4nx_gemm_lora,
-                      q4nx_kv_append, q4nx_kv_append_rotary, q4nx_kv_attention, q4nx_kv_batch, q4nx_kv_cache, q4nx_kv_page_bytes, q4nx_kv_read,
+                      q4nx_kv_append, q4nx_kv_append_rotary, q4nx_kv_attention, q4nx_kv_attention_cross,
+                      q4nx_kv_attention_shared, q4nx_kv_batch, q4nx_kv_cache, q4nx_kv_groups, q4nx_kv_page_bytes, q4nx_kv_read,
                       q4nx_logprobs, q4nx_rotary)
 
 EXPORTS += serving.EXPORTS

@@ -28,7 +28,7 @@ struct Joined {
   int64_t q0, row0;
   int h, rows;
   int parts;                // CTAs with a part of it, from this one on; 0: nothing to join
-  int pad;
+  int split;                // its rows have another part, in another pass
 };
 
 struct AttnArgs {
@@ -46,6 +46,28 @@ struct AttnArgs {
   float* partial;           // [2*grid][RB][D + 2]: a CTA's parts of the unit it began and the one it ended with
   Joined* joined;           // [grid], the kernel for many rows
   float* stash;             // [grid][kWarps][RB*D]: a warp's part of the unit it began with
+};
+
+// What the rows of a unit see of a cache: positions up to their own (kCausal, the kernels of
+// q4nx_kv_attention); all of them (kAll: another sequence's states, or what the requests of a
+// group share, the group taking a request's place); those behind what the request
+// shares, up to their own (kOwn).
+enum : int { kCausal = 0, kAll = 1, kOwn = 2 };
+template <int SEE>
+struct AttnArgsOf : AttnArgs {
+  static constexpr int kSee = SEE;
+  // Shared parts: group g is the requests first[g] .. first[g + 1] - 1, which share their first
+  // shared[g] positions.  The first pass leaves its rows' outputs and sums in part_o and
+  // part_ml (reference and sum), the second joins them to its own.
+  const int32_t *first = nullptr, *shared = nullptr;
+  int groups = 0;
+  int pass = 0;             // 0: the only one
+  float* part_o = nullptr;  // [tokens][heads][D]
+  float2* part_ml = nullptr;
+};
+template <>
+struct AttnArgsOf<kCausal> : AttnArgs {
+  static constexpr int kSee = kCausal;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -122,6 +144,7 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {   // of numbers 
 // before them add up to cost[b].
 struct Plan {
   const int64_t *prefix, *cost;    // shared memory, [batch + 1]
+  const int* lower;                // kOwn: each request's first position
   int64_t total;                   // of the costs
   int ctas;
   int batch;
@@ -136,26 +159,68 @@ struct Unit {
   KvRequest rq;
 };
 
+// How many requests (or groups of them) the call has, request b, and its row of the page table.
+template <class A>
+__device__ __forceinline__ int requests_of(const A& a) {
+  if constexpr (A::kSee == kAll)
+    if (a.first != nullptr) return a.groups;
+  return a.kb.batch;
+}
+template <class A>
+__device__ __forceinline__ KvRequest request_of(const A& a, int b) {
+  if constexpr (A::kSee == kAll)
+    if (a.first != nullptr) {
+      const int f0 = a.first[b], f1 = a.first[b + 1];
+      if (f0 < 0 || f1 < f0 || f1 > a.kb.batch) return KvRequest{0, 0, 0, false};
+      KvRequest r = kv_checked(a.kb, a.pool.page_blocks, a.kb.q_start[f0], a.kb.q_start[f1], a.shared[b]);
+      if (r.L == 0) r.T = 0;       // nothing shared: the other pass has these rows to itself
+      return r;
+    }
+  KvRequest r = kv_request(a.kb, a.pool.page_blocks, b);
+  if constexpr (A::kSee == kOwn) {
+    int lo = 0, hi = a.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.first[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    r.low = a.shared[lo];
+    // every token of the call lies behind what its request shares
+    if (a.first[lo] > b || a.first[lo + 1] <= b || r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low)) r = KvRequest{0, 0, 0, false};
+    if (r.T == 0) r.low = 0;
+  }
+  return r;
+}
+template <class A>
+__device__ __forceinline__ int table_row(const A& a, int b) {
+  if constexpr (A::kSee == kAll)
+    if (a.first != nullptr) return a.first[b];
+  return b;
+}
+
 // First position that some row of the request sees: pages before it need not be there.
-__device__ __forceinline__ int64_t first_visible(const KvRequest& rq, int64_t window) {
-  if (window <= 0) return 0;
-  const int64_t f = rq.L - rq.T + 1 - window;
+template <class A>
+__device__ __forceinline__ int64_t first_visible(const A& a, const KvRequest& rq) {
+  if constexpr (A::kSee == kAll) return 0;
+  if constexpr (A::kSee == kOwn) return rq.low;
+  if (a.window <= 0) return 0;
+  const int64_t f = rq.L - rq.T + 1 - a.window;
   return f > 0 ? f : 0;
 }
-template <int SB>
-__device__ __forceinline__ int64_t first_visible_step(const KvRequest& rq, int64_t window) {
-  return first_visible(rq, window) / (SB * kKvBlock);
+template <int SB, class A>
+__device__ __forceinline__ int64_t first_visible_step(const A& a, const KvRequest& rq) {
+  return first_visible(a, rq) / (SB * kKvBlock);
 }
-template <int SB>
-__device__ __forceinline__ int64_t unit_steps(const KvRequest& rq, int64_t window) {
+template <int SB, class A>
+__device__ __forceinline__ int64_t unit_steps(const A& a, const KvRequest& rq) {
   constexpr int kStepTokens = SB * kKvBlock;
-  const int64_t n = (rq.L + kStepTokens - 1) / kStepTokens - first_visible_step<SB>(rq, window);
+  const int64_t n = (rq.L + kStepTokens - 1) / kStepTokens - first_visible_step<SB>(a, rq);
   return n > 0 ? n : 1;     // an empty request's rows are written too
 }
 
 // Steps are of SB 16-token blocks, units of RB query rows.  The unit that holds position x, or (by_cost) the one whose cost range holds x.
-template <int SB, int RB>
-__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Plan& pl, int64_t x, bool by_cost = false) {
+template <int SB, int RB, class A>
+__device__ __forceinline__ Unit find_unit(const A& a, const Plan& pl, int64_t x, bool by_cost = false) {
   const int64_t* at = by_cost ? pl.cost : pl.prefix;
   int lo = 0, hi = pl.batch;
   while (hi - lo > 1) {
@@ -165,9 +230,14 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Plan& pl, int
   }
   Unit u;
   u.b = lo;
-  u.rq = kv_request(a.kb, a.pool.page_blocks, lo);
-  u.n = unit_steps<SB>(u.rq, a.window);
-  u.first = first_visible_step<SB>(u.rq, a.window);
+  if constexpr (A::kSee == kOwn) {
+    u.rq = kv_request(a.kb, a.pool.page_blocks, lo);
+    u.rq.low = pl.lower[lo];
+  } else {
+    u.rq = request_of(a, lo);
+  }
+  u.n = unit_steps<SB>(a, u.rq);
+  u.first = first_visible_step<SB>(a, u.rq);
   const int64_t groups = quot(u.rq.T * a.group + RB - 1, RB);
   const int64_t k = quot(x - at[lo], by_cost ? u.n + kUnitCost : u.n);
   u.h = static_cast<int>(quot(k, groups));
@@ -179,8 +249,8 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Plan& pl, int
 
 // First position of CTA c: where its share of the costs begins, moved to the
 // end of a unit that it falls into less than kCutSteps from.
-template <int SB, int RB>
-__device__ int64_t bound(const AttnArgs& a, const Plan& pl, int c) {
+template <int SB, int RB, class A>
+__device__ int64_t bound(const A& a, const Plan& pl, int c) {
   if (c >= pl.ctas) return pl.prefix[pl.batch];
   const int64_t q = quot(pl.total, pl.ctas), rest = pl.total - q * pl.ctas;
   const int64_t x = q * c + (c < rest ? c : rest);
@@ -208,19 +278,67 @@ __device__ __forceinline__ float log_total(float m, float l) {
   return l == 0.f ? -__int_as_float(0x7f800000) : (m + lg2(l)) * 0.693147180559945f;
 }
 
+// How a row's sums o become its output: own * o, and other times what the first pass left.
+// m, l: the row's reference and the sum of its weights; at: its place among the outputs'
+// rows; split: it has another part; head: this thread writes what there is one of for a row.
+struct RowScale {
+  float own, other;
+};
+template <class A>
+__device__ __forceinline__ RowScale row_scale(const A& a, bool split, int64_t at, float m, float l, bool head) {
+  if constexpr (A::kSee != kCausal) {
+    if (split && a.pass == 2) {
+      const float2 p = __ldcg(a.part_ml + at);
+      const float top = fmaxf(m, p.x), f = ex2(m - top), g = ex2(p.x - top) * p.y, all = fmaf(f, l, g), inv = 1.f / all;
+      if (head && a.lse != nullptr) a.lse[at] = log_total(top, all);
+      return {f * inv, g * inv};
+    }
+    if (split) {
+      if (head) a.part_ml[at] = make_float2(m, l);
+      return {l == 0.f ? 0.f : 1.f / l, 0.f};
+    }
+  }
+  if (head && a.lse != nullptr) a.lse[at] = log_total(m, l);
+  return {l == 0.f ? 0.f : 1.f / l, 0.f};
+}
+template <typename Out, class A>
+__device__ __forceinline__ void put_row(const A& a, bool split, int64_t at, float o, RowScale s) {
+  if constexpr (A::kSee != kCausal)
+    if (split) {
+      if (a.pass == 2) put<Out>(a, at, fmaf(o, s.own, s.other * __ldcg(a.part_o + at)));
+      else a.part_o[at] = o * s.own;
+      return;
+    }
+  put<Out>(a, at, o * s.own);
+}
+// A second pass runs beside the first one until it needs what that left; nothing of it ends before.
+template <class A>
+__device__ __forceinline__ void wait_first_pass(const A& a) {
+  if constexpr (A::kSee != kCausal)
+    if (a.pass == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The plan of the call's units, by all threads of a CTA: prefix and cost are
-// [batch + 1] and longest is [32] in shared memory.
-template <int SB, int RB>
-__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, int64_t* cost, int* longest) {
+// [batch + 1], longest is [32] and lower (kOwn) [batch] in shared memory.
+template <int SB, int RB, class A>
+__device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* cost, int* longest, int* lower) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) prefix[0] = cost[0] = 0;
   // the requests' steps and costs, and their prefix sums
-  const int B = a.kb.batch;
+  const int B = requests_of(a);
   int most = 0;
+  if constexpr (A::kSee == kOwn)
+    if (blockIdx.x == 0) {
+      // the groups take the requests in their order, all of them
+      bool bad = tid == 0 && (a.first[0] != 0 || a.first[a.groups] != a.kb.batch);
+      for (int g = tid; g < a.groups; g += blockDim.x) bad |= a.first[g] > a.first[g + 1];
+      if (bad) atomicOr(a.err, kErrIndex);
+    }
   for (int b = tid; b < B; b += blockDim.x) {
-    const KvRequest rq = kv_request(a.kb, a.pool.page_blocks, b);
+    const KvRequest rq = request_of(a, b);
     if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
-    const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(rq, a.window);
+    if constexpr (A::kSee == kOwn) lower[b] = static_cast<int>(rq.low);
+    const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(a, rq);
     prefix[b + 1] = units * n;
     cost[b + 1] = units * (n + kUnitCost);
     if (units > 0) most = max(most, static_cast<int>(n < (1 << 30) ? n : 1 << 30));
@@ -248,6 +366,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, in
   Plan pl;
   pl.prefix = prefix;
   pl.cost = cost;
+  pl.lower = lower;
   pl.batch = B;
   pl.total = cost[B];
   int64_t want = pl.total / kMinCost;
@@ -256,9 +375,21 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int64_t* prefix, in
   return pl;
 }
 
-// Many query rows per request (q4nx_attention_block.cu; 64 or 128 channels): the
+// Few query rows per request (q4nx_attention_rows.cuh): `two` tiles of 8 at a time, or one.
+template <int SEE>
+cudaError_t launch_attention_rows(int D, bool two, const AttnArgsOf<SEE>& a, int out_f32, const DeviceInfo& info, cudaStream_t s);
+// Many query rows per request (q4nx_attention_block.cuh; 64 or 128 channels): the
 // size of the parts (0 for other sizes), and the launch.
 uint64_t attention_block_bytes(int D);
-cudaError_t launch_attention_block(int D, const AttnArgs& a, int out_f32, const DeviceInfo& info, cudaStream_t s);
+template <int SEE>
+cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int out_f32, const DeviceInfo& info, cudaStream_t s);
+// each in a file of its own
+#define Q4NX_ATTN(SEE)                                                                                                      \
+  extern template cudaError_t launch_attention_rows<SEE>(int, bool, const AttnArgsOf<SEE>&, int, const DeviceInfo&, cudaStream_t); \
+  extern template cudaError_t launch_attention_block<SEE>(int, const AttnArgsOf<SEE>&, int, const DeviceInfo&, cudaStream_t);
+Q4NX_ATTN(kCausal)
+Q4NX_ATTN(kAll)
+Q4NX_ATTN(kOwn)
+#undef Q4NX_ATTN
 
 }  // namespace q4nx

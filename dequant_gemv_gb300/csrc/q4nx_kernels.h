@@ -110,6 +110,16 @@ cudaError_t launch_attention(int D, const KvPool& pool, const KvBatch& kb, const
                              float scale, int64_t window, void* out, int out_f32, float* lse, void* workspace,
                              const DeviceInfo& info, cudaStream_t s);
 
+cudaError_t launch_attention_cross(int D, const KvPool& pool, const KvBatch& kb, const void* q, int64_t q_stride, int heads,
+                                   float scale, void* out, int out_f32, float* lse, void* workspace, const DeviceInfo& info,
+                                   cudaStream_t s);
+// Requests first[g] .. first[g + 1] - 1 share their first shared[g] positions (q4nx_attention.cu).
+uint64_t attention_shared_scratch(int D, int64_t tokens, int heads);
+cudaError_t launch_attention_shared(int D, const KvPool& pool, const KvBatch& kb, const int32_t* first, const int32_t* shared,
+                                    int groups, const void* q, int64_t q_stride, int heads, float scale, void* out,
+                                    int out_f32, float* lse, void* workspace, void* scratch, const DeviceInfo& info,
+                                    cudaStream_t s);
+
 // ---- low-rank adapters beside a projection ----
 struct LoraCall {
   const void *x, *a, *b;       // bf16 [M][K], [count][R][K], [count][N][R]

@@ -57,12 +57,13 @@ struct KvRequest {
   int64_t q0;             // first token of the call
   int64_t T, L;           // tokens of the call, tokens in the cache
   bool ok;
+  int64_t low = 0;        // attention of a request's own part: its first position
 };
 
 // A request with its numbers checked: a length below 0 or beyond the table, or
 // token ranges that do not lie in 0..tokens in order, make it empty (ok false).
 __device__ __forceinline__ KvRequest kv_checked(const KvBatch& kb, int page_blocks, int64_t q0, int64_t q1, int64_t L) {
-  KvRequest r;
+  KvRequest r = {};
   const int64_t cap = static_cast<int64_t>(kb.table_cols) * page_blocks * kKvBlock;
   r.ok = q0 >= 0 && q1 >= q0 && q1 <= kb.tokens && L >= 0 && L <= cap;
   r.q0 = r.ok ? q0 : 0;

@@ -68,6 +68,21 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;      // elements between rows: 
 
 constexpr int64_t kMaxSideStride = int64_t(1) << 38;  // of an epilogue's operands: a tensor map's strides have 40 bits of bytes
 
+// What the attention entry points check alike.
+int check_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride, int heads,
+                    int64_t window, const void* out_dev, int out_dtype, const float* lse_dev, const void* workspace_dev,
+                    uint64_t workspace_bytes) {
+  int st = check_cache(cache);
+  if (st == Q4NX_OK) st = check_batch(batch);
+  if (st) return st;
+  if (q_dev == nullptr || out_dev == nullptr) return Q4NX_E_NULL;
+  if (heads < 1 || heads > kMaxHeads || heads % cache->kv_heads != 0) return Q4NX_E_SHAPE;
+  if (q_stride < static_cast<int64_t>(heads) * cache->head_dim || q_stride > kMaxStride || window < 0) return Q4NX_E_SHAPE;
+  if (!known_out(out_dtype)) return Q4NX_E_DTYPE;
+  if (!aligned16(q_dev) || !aligned16(out_dev) || q_stride % 8 != 0 || !aligned(lse_dev, 4)) return Q4NX_E_ALIGN;
+  return check_workspace(workspace_dev, workspace_bytes, q4nx_kv_workspace(cache));
+}
+
 // 32-bit words of the adapters' inner products and of the tokens in their order
 uint64_t lora_t(int64_t cols) { return static_cast<uint64_t>(lora_splits(cols)) * 64 * 128 + 128; }
 bool known_rank(int r) { return r == 8 || r == 16 || r == 32 || r == 64 || r == 128; }
@@ -158,21 +173,49 @@ int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k
 int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
                       int heads, float scale, int64_t window, void* out_dev, int out_dtype, float* lse_dev,
                       void* workspace_dev, uint64_t workspace_bytes, void* stream) {
-  int st = check_cache(cache);
-  if (st == Q4NX_OK) st = check_batch(batch);
-  if (st) return st;
-  if (q_dev == nullptr || out_dev == nullptr) return Q4NX_E_NULL;
-  if (heads < 1 || heads > kMaxHeads || heads % cache->kv_heads != 0) return Q4NX_E_SHAPE;
-  if (q_stride < static_cast<int64_t>(heads) * cache->head_dim || q_stride > kMaxStride || window < 0) return Q4NX_E_SHAPE;
-  if (!known_out(out_dtype)) return Q4NX_E_DTYPE;
-  if (!aligned16(q_dev) || !aligned16(out_dev) || q_stride % 8 != 0 || !aligned(lse_dev, 4)) return Q4NX_E_ALIGN;
-  if ((st = check_workspace(workspace_dev, workspace_bytes, q4nx_kv_workspace(cache)))) return st;
-  if (batch->tokens == 0) return Q4NX_OK;
+  int st = check_attention(cache, batch, q_dev, q_stride, heads, window, out_dev, out_dtype, lse_dev, workspace_dev, workspace_bytes);
+  if (st || batch->tokens == 0) return st;
   DeviceInfo info;
   if (device_info(&info) != cudaSuccess) return Q4NX_E_CUDA;
   return from_cuda(launch_attention(cache->head_dim, pool_of(cache), batch_of(batch), q_dev, q_stride, heads, scale, window,
                                     out_dev, out_dtype == Q4NX_OUT_F32, lse_dev, workspace_dev, info,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+int q4nx_kv_attention_cross(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
+                            int heads, float scale, void* out_dev, int out_dtype, float* lse_dev, void* workspace_dev,
+                            uint64_t workspace_bytes, void* stream) {
+  int st = check_attention(cache, batch, q_dev, q_stride, heads, 0, out_dev, out_dtype, lse_dev, workspace_dev, workspace_bytes);
+  if (st || batch->tokens == 0) return st;
+  DeviceInfo info;
+  if (device_info(&info) != cudaSuccess) return Q4NX_E_CUDA;
+  return from_cuda(launch_attention_cross(cache->head_dim, pool_of(cache), batch_of(batch), q_dev, q_stride, heads, scale, out_dev,
+                                          out_dtype == Q4NX_OUT_F32, lse_dev, workspace_dev, info,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+uint64_t q4nx_kv_attention_shared_scratch(const q4nx_kv_cache* cache, int64_t tokens, int heads) {
+  if (q4nx_kv_workspace(cache) == 0 || tokens < 0 || tokens > INT32_MAX || heads < 1 || heads > kMaxHeads) return 0;
+  return attention_shared_scratch(cache->head_dim, tokens, heads);
+}
+
+int q4nx_kv_attention_shared(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const q4nx_kv_groups* groups,
+                             const void* q_dev, int64_t q_stride, int heads, float scale, void* out_dev, int out_dtype,
+                             float* lse_dev, void* workspace_dev, uint64_t workspace_bytes, void* scratch_dev,
+                             uint64_t scratch_bytes, void* stream) {
+  int st = check_attention(cache, batch, q_dev, q_stride, heads, 0, out_dev, out_dtype, lse_dev, workspace_dev, workspace_bytes);
+  if (st) return st;
+  if (groups == nullptr || groups->first_dev == nullptr || groups->shared_dev == nullptr) return Q4NX_E_NULL;
+  if (groups->reserved != 0) return Q4NX_E_KIND;
+  if (groups->count < 1 || groups->count > kKvMaxBatch) return Q4NX_E_SHAPE;
+  if (!aligned(groups->first_dev, 4) || !aligned(groups->shared_dev, 4)) return Q4NX_E_ALIGN;
+  if ((st = check_workspace(scratch_dev, scratch_bytes, q4nx_kv_attention_shared_scratch(cache, batch->tokens, heads)))) return st;
+  if (batch->tokens == 0) return Q4NX_OK;
+  DeviceInfo info;
+  if (device_info(&info) != cudaSuccess) return Q4NX_E_CUDA;
+  return from_cuda(launch_attention_shared(cache->head_dim, pool_of(cache), batch_of(batch), groups->first_dev, groups->shared_dev,
+                                           groups->count, q_dev, q_stride, heads, scale, out_dev, out_dtype == Q4NX_OUT_F32,
+                                           lse_dev, workspace_dev, scratch_dev, info, static_cast<cudaStream_t>(stream)));
 }
 
 uint64_t q4nx_gemm_lora_scratch(const q4nx_weight* w, int M) {

@@ -207,34 +207,85 @@ PyObject* kv_read(PyObject* const* a) {
   return Py_BuildValue("NN", THPVariable_Wrap(std::move(k)), THPVariable_Wrap(std::move(v)));
 }
 
+// What the attention calls have in common: (cache, pool, ws_bytes, q, q_start, lens, table, scale) come first,
+// `rest` are their out, out code, lse and ws.
+struct Attention {
+  Cache cache;
+  const at::Tensor& q;
+  Rows r;
+  q4nx_kv_batch b;
+  float scale;
+  int code;
+  c10::cuda::CUDAGuard guard;
+  cudaStream_t s;
+  Workspace ws;
+  at::Tensor out;
+  float* lse = nullptr;
+  Attention(PyObject* const* a, PyObject* const* rest)
+      : cache(cache_of(a[0], a[1])),
+        q(tensor(a[3], "q")),
+        r(token_rows(q, "q", cache.c->head_dim, cache.dev)),
+        b(batch_of(a + 4, r.tokens, cache.dev)),
+        guard(cache.dev) {
+    const double x = PyFloat_AsDouble(a[7]);
+    if (x == -1.0 && PyErr_Occurred()) throw PythonError();
+    scale = static_cast<float>(x);
+    code = static_cast<int>(integer(rest[1]));
+    const at::Tensor *given = tensor_or_none(rest[0], "out"), *sums = tensor_or_none(rest[2], "lse");
+    s = c10::cuda::getCurrentCUDAStream(cache.dev.index()).stream();
+    ws = workspace(rest[3], "kv", cache.dev, s, static_cast<uint64_t>(integer(a[2])));
+    if (given != nullptr) {
+      plain(*given, "out", out_type(code), 3, cache.dev);
+      if (given->sizes() != q.sizes()) throw Refused("out must have q's shape");
+    }
+    if (sums != nullptr) {
+      plain(*sums, "lse", at::kFloat, 2, cache.dev);
+      if (sums->size(0) != r.tokens || sums->size(1) != r.heads) throw Refused("lse must be [tokens, heads]");
+      lse = sums->data_ptr<float>();
+    }
+    out = given != nullptr ? *given : empty(q.sizes(), out_type(code), cache.dev);
+  }
+};
+
 // (cache, pool, ws_bytes, q, q_start, lens, table, scale, window, out, out code, lse, ws)
 PyObject* kv_attention(PyObject* const* a) {
-  const Cache cache = cache_of(a[0], a[1]);
-  const at::Tensor& q = tensor(a[3], "q");
-  const Rows r = token_rows(q, "q", cache.c->head_dim, cache.dev);
-  const q4nx_kv_batch b = batch_of(a + 4, r.tokens, cache.dev);
-  const double scale = PyFloat_AsDouble(a[7]);
-  if (scale == -1.0 && PyErr_Occurred()) throw PythonError();
-  const int64_t window = integer(a[8]), code = integer(a[10]);
-  const at::Tensor *given = tensor_or_none(a[9], "out"), *lse = tensor_or_none(a[11], "lse");
-  const c10::cuda::CUDAGuard guard(cache.dev);
-  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(cache.dev.index()).stream();
-  const Workspace ws = workspace(a[12], "kv", cache.dev, s, static_cast<uint64_t>(integer(a[2])));
-  if (given != nullptr) {
-    plain(*given, "out", out_type(code), 3, cache.dev);
-    if (given->sizes() != q.sizes()) throw Refused("out must have q's shape");
-  }
-  if (lse != nullptr) {
-    plain(*lse, "lse", at::kFloat, 2, cache.dev);
-    if (lse->size(0) != r.tokens || lse->size(1) != r.heads) throw Refused("lse must be [tokens, heads]");
-  }
-  at::Tensor out = given != nullptr ? *given : empty(q.sizes(), out_type(code), cache.dev);
-  if (r.tokens > 0)
-    check(q4nx_kv_attention(cache.c, &b, q.data_ptr(), r.stride, static_cast<int>(r.heads), static_cast<float>(scale), window,
-                            out.data_ptr(), static_cast<int>(code), lse != nullptr ? lse->data_ptr<float>() : nullptr, ws.ptr,
-                            ws.bytes, s),
+  const int64_t window = integer(a[8]);
+  Attention t(a, a + 9);
+  if (t.r.tokens > 0)
+    check(q4nx_kv_attention(t.cache.c, &t.b, t.q.data_ptr(), t.r.stride, static_cast<int>(t.r.heads), t.scale, window, t.out.data_ptr(),
+                            t.code, t.lse, t.ws.ptr, t.ws.bytes, t.s),
           "q4nx_kv_attention");
-  return THPVariable_Wrap(std::move(out));
+  return THPVariable_Wrap(std::move(t.out));
+}
+
+// (cache, pool, ws_bytes, q, q_start, lens, table, scale, out, out code, lse, ws)
+PyObject* kv_attention_cross(PyObject* const* a) {
+  Attention t(a, a + 8);
+  if (t.r.tokens > 0)
+    check(q4nx_kv_attention_cross(t.cache.c, &t.b, t.q.data_ptr(), t.r.stride, static_cast<int>(t.r.heads), t.scale, t.out.data_ptr(),
+                                  t.code, t.lse, t.ws.ptr, t.ws.bytes, t.s),
+          "q4nx_kv_attention_cross");
+  return THPVariable_Wrap(std::move(t.out));
+}
+
+// (cache, pool, ws_bytes, q, q_start, lens, table, scale, first, shared, out, out code, lse, ws)
+PyObject* kv_attention_shared(PyObject* const* a) {
+  Attention t(a, a + 10);
+  const at::Tensor &first = tensor(a[8], "first"), &shared = tensor(a[9], "shared");
+  plain(first, "first", at::kInt, 1, t.cache.dev);
+  plain(shared, "shared", at::kInt, 1, t.cache.dev);
+  if (first.numel() != shared.numel() + 1 || shared.numel() > INT32_MAX) throw Refused("first must have one entry more than shared");
+  const q4nx_kv_groups g = {first.data_ptr<int32_t>(), shared.data_ptr<int32_t>(), static_cast<int32_t>(shared.numel()), 0};
+  if (t.r.tokens > 0) {
+    const int heads = static_cast<int>(t.r.heads < INT32_MAX ? t.r.heads : INT32_MAX);
+    // scratch of any content: the caching allocator keeps it to this stream's order
+    const int64_t bytes = static_cast<int64_t>(q4nx_kv_attention_shared_scratch(t.cache.c, t.r.tokens, heads));
+    const at::Tensor scratch = empty(bytes, at::kByte, t.cache.dev);
+    check(q4nx_kv_attention_shared(t.cache.c, &t.b, &g, t.q.data_ptr(), t.r.stride, heads, t.scale, t.out.data_ptr(), t.code, t.lse,
+                                   t.ws.ptr, t.ws.bytes, scratch.data_ptr(), static_cast<uint64_t>(bytes), t.s),
+          "q4nx_kv_attention_shared");
+  }
+  return THPVariable_Wrap(std::move(t.out));
 }
 
 // (chunks, kind, rows, cols, X, adapters, their device ordinal, rows and cols, ids, out, out code, ws)
@@ -402,6 +453,8 @@ PyMethodDef g_methods[] = {method<setup, 3>("setup"),
                            method<kv_append_rotary, 13>("kv_append_rotary"),
                            method<kv_read, 9>("kv_read"),
                            method<kv_attention, 13>("kv_attention"),
+                           method<kv_attention_cross, 12>("kv_attention_cross"),
+                           method<kv_attention_shared, 14>("kv_attention_shared"),
                            method<gemm_lora, 13>("gemm_lora"),
                            method<gemm_epilogue, 12>("gemm_epilogue"),
                            method<logprobs, 3>("logprobs"),

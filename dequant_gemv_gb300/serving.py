@@ -5,6 +5,8 @@
     q4nx_kv_append_rotary(cache, Rotary(table), q, k, v, q_start, lens, table) -> turned q
     q4nx_kv_read(cache, tokens, q_start, lens, table)            -> (k, v)
     q4nx_kv_attention(cache, q, q_start, lens, table, scale)     -> [tokens, heads, head_dim]
+    q4nx_kv_attention_cross(cache, q, q_start, lens, table, scale)                  -> [tokens, heads, head_dim]
+    q4nx_kv_attention_shared(cache, q, q_start, lens, table, first, shared, scale)  -> [tokens, heads, head_dim]
     q4nx_gemm_lora(w, X, Adapters(a, b, scale), ids)             -> [M, N]
     q4nx_gemm_epilogue(w, X, bias, act, mul, residual)           -> [M, N]
     q4nx_logprobs(logits, tokens, top)                           -> Logprobs
@@ -55,6 +57,10 @@ class q4nx_kv_batch(ctypes.Structure):
                 ("table_cols", ctypes.c_int32), ("tokens", I64)]
 
 
+class q4nx_kv_groups(ctypes.Structure):
+    _fields_ = [("first_dev", P), ("shared_dev", P), ("count", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class q4nx_adapters(ctypes.Structure):
     _fields_ = [("a_dev", P), ("b_dev", P), ("scale_dev", P), ("a_bytes", U64), ("b_bytes", U64),
                 ("count", ctypes.c_int32), ("rank", ctypes.c_int32)]
@@ -77,6 +83,9 @@ for _name, (_args, _res) in {
     "q4nx_kv_append_rotary": ([_CACHE, _BATCH, ctypes.POINTER(q4nx_rotary), P, I64, I, P, I64, P, P, I64, P, U64, P], I),
     "q4nx_kv_read": ([_CACHE, _BATCH, P, P, I, P, U64, P], I),
     "q4nx_kv_attention": ([_CACHE, _BATCH, P, I64, I, F, I64, P, I, P, P, U64, P], I),
+    "q4nx_kv_attention_cross": ([_CACHE, _BATCH, P, I64, I, F, P, I, P, P, U64, P], I),
+    "q4nx_kv_attention_shared": ([_CACHE, _BATCH, ctypes.POINTER(q4nx_kv_groups), P, I64, I, F, P, I, P, P, U64, P, U64, P], I),
+    "q4nx_kv_attention_shared_scratch": ([_CACHE, I64, I], U64),
     "q4nx_gemm_lora": ([ctypes.POINTER(q4nx_weight), P, I, ctypes.POINTER(q4nx_adapters), P, P, I, P, U64, P, U64, P], I),
     "q4nx_gemm_lora_scratch": ([ctypes.POINTER(q4nx_weight), I], U64),
     "q4nx_gemm_epilogue": ([ctypes.POINTER(q4nx_weight), P, I, ctypes.POINTER(q4nx_epilogue), P, I, P, U64, P], I),
@@ -85,6 +94,7 @@ for _name, (_args, _res) in {
     _fn = getattr(lib, _name)
     _fn.argtypes, _fn.restype = _args, _res
 EXPORTS = ("q4nx_kv_page_bytes", "q4nx_kv_workspace", "q4nx_kv_append", "q4nx_kv_append_rotary", "q4nx_kv_read", "q4nx_kv_attention",
+           "q4nx_kv_attention_cross", "q4nx_kv_attention_shared", "q4nx_kv_attention_shared_scratch",
            "q4nx_gemm_lora", "q4nx_gemm_lora_scratch", "q4nx_gemm_epilogue", "q4nx_logprobs")
 Q4NX_MAX_TOP = 32
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}       # enum q4nx_act
@@ -188,6 +198,27 @@ def q4nx_kv_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, le
     window: 0 for none; lse: fp32 [tokens, heads] to be filled, or None."""
     return _serving.kv_attention(cache._at, cache.pool, cache._ws_bytes, q, q_start, lens, table,
                                  cache.head_dim ** -0.5 if scale is None else scale, window, out, _out_code(out_dtype), lse, ws)
+
+
+def q4nx_kv_attention_cross(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                            scale: float | None = None, out: torch.Tensor | None = None, out_dtype="bf16",
+                            lse: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the requests' tokens to all positions of another sequence's cache; lens: its lengths.
+
+    Other arguments as of q4nx_kv_attention."""
+    return _serving.kv_attention_cross(cache._at, cache.pool, cache._ws_bytes, q, q_start, lens, table,
+                                       cache.head_dim ** -0.5 if scale is None else scale, out, _out_code(out_dtype), lse, ws)
+
+
+def q4nx_kv_attention_shared(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                             first: torch.Tensor, shared: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None,
+                             out_dtype="bf16", lse: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """q4nx_kv_attention of requests that share prefixes, each read once.
+
+    first: int32 [groups + 1], the groups' first requests and the batch; shared: int32 [groups], the
+    positions that a group's requests have in common (lens counts them); other arguments as of q4nx_kv_attention."""
+    return _serving.kv_attention_shared(cache._at, cache.pool, cache._ws_bytes, q, q_start, lens, table,
+                                        cache.head_dim ** -0.5 if scale is None else scale, first, shared, out, _out_code(out_dtype), lse, ws)
 
 
 @dataclass(frozen=True)

@@ -261,7 +261,7 @@ typedef struct q4nx_kv_batch {
     int64_t tokens;               /* rows of the call's token arrays, 0..INT32_MAX */
 } q4nx_kv_batch;
 
-/* Workspace of the three cache entry points (one size for all): zero-filled
+/* Workspace of the cache entry points (one size for all): zero-filled
  * before its first use and again after Q4NX_E_DEVICE_TIMEOUT; partial results
  * stay behind in it, so it is not shared with the GEMV or GEMM.  0 for a bad cache. */
 uint64_t q4nx_kv_workspace(const q4nx_kv_cache* cache);
@@ -336,6 +336,42 @@ int q4nx_kv_read(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, void* k
 int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
                       int heads, float scale, int64_t window, void* out_dev, int out_dtype, float* lse_dev,
                       void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
+/* Attention to all positions of another sequence's cache (an encoder's states): as
+ * q4nx_kv_attention, except that every token of request b sees all of its lens[b] cached
+ * positions.  lens says nothing of the call's own tokens, and their number may be larger or
+ * smaller.  A request whose cache is empty gives zeros and -Inf. */
+int q4nx_kv_attention_cross(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
+                            int heads, float scale, void* out_dev, int out_dtype, float* lse_dev, void* workspace_dev,
+                            uint64_t workspace_bytes, void* stream);
+
+/* What requests of a batch have in common: group g is the requests first[g] ..
+ * first[g+1]-1, and the first shared[g] positions of each of them are the same.  first[0] is 0
+ * and first[count] the batch; a group may be of one request, or share nothing (0). */
+typedef struct q4nx_kv_groups {
+    const int32_t* first_dev;     /* device int32 [count + 1]                      */
+    const int32_t* shared_dev;    /* device int32 [count]                          */
+    int32_t count;                /* 1..1024                                       */
+    int32_t reserved;             /* must be 0                                     */
+} q4nx_kv_groups;
+
+/* q4nx_kv_attention (without a window) of requests that share prefixes: the same outputs,
+ * within the accuracy stated there, each shared position read and decoded once for its group.
+ * lens and positions count the shared ones.  Shared positions are found through the page
+ * table's row of the group's first request; the other requests' entries of pages that hold
+ * nothing else are not read through.  A prefix may end inside a page: each request
+ * then has that page for itself, and its copies of the prefix's positions are not looked at.
+ * Every token of the call has to lie behind what its request shares (lens - T >= shared):
+ * requests of which that is not true, like groups out of order or lengths beyond the
+ * table, are skipped and reported as Q4NX_E_INDEX.  Which rounding applies (fp16 weights or
+ * bf16 pairs) goes by the rows of a group for what it shares and by those of a request for its own.
+ * scratch_dev: q4nx_kv_attention_shared_scratch(cache, tokens, heads) bytes, 16-byte
+ * aligned, any content, free again after the call's work on the stream. */
+int q4nx_kv_attention_shared(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const q4nx_kv_groups* groups,
+                             const void* q_dev, int64_t q_stride, int heads, float scale, void* out_dev, int out_dtype,
+                             float* lse_dev, void* workspace_dev, uint64_t workspace_bytes, void* scratch_dev,
+                             uint64_t scratch_bytes, void* stream);
+uint64_t q4nx_kv_attention_shared_scratch(const q4nx_kv_cache* cache, int64_t tokens, int heads);
 
 /* Low-rank adapters of one projection, all of one rank (8, 16, 32, 64 or 128; a
  * smaller adapter is padded with zeros). */

@@ -1,5 +1,6 @@
-"""Host-side checks of the epilogue product and of the append with a rotation (no GPU needed):
-the documented status for every bad argument, before any CUDA call."""
+"""Host-side checks of the epilogue product, the append with a rotation, cross attention and
+attention of shared prefixes (no GPU needed): the documented status for every bad argument,
+before any CUDA call."""
 import ctypes
 
 import pytest
@@ -74,6 +75,43 @@ def test_append_rotary_refuses(q):
     # without queries theirs are not looked at; nothing to do is accepted without a launch
     assert call(qx=None, out=None, heads=0, qs=0, os=3, ws=None) == 7 and call(b=dict(batch, tokens=0)) == 0
     assert call(heads=5, qs=640, os=640, b=dict(batch, tokens=0)) == 0            # any number of heads
+
+
+def test_attention_cross_and_shared_refuse(q):
+    L, by = q.lib, ctypes.byref
+    cache = dict(pool=P, nbytes=1 << 30, dim=128, heads=8, page=64, reserved=0, pages=10)
+    batch = dict(a=P, b=P, c=P, batch=3, cols=4, tokens=3)
+    c0 = q.q4nx_kv_cache(*cache.values())
+    need, sc = L.q4nx_kv_workspace(by(c0)), L.q4nx_kv_attention_shared_scratch(by(c0), 3, 32)
+    assert sc >= 3 * 32 * (128 * 4 + 8)
+    assert [L.q4nx_kv_attention_shared_scratch(*a) for a in ((None, 3, 32), (by(c0), -1, 32), (by(c0), 1 << 31, 32), (by(c0), 3, 0), (by(c0), 3, 1025),
+                                                             (by(q.q4nx_kv_cache(*dict(cache, dim=96).values())), 3, 32))] == [0] * 6
+    assert L.q4nx_kv_attention_shared_scratch(by(c0), 100000, 32) - sc >= 99000 * 32 * 520
+
+    def calls(c=cache, b=batch, qx=P, qs=4096, heads=32, out=P, dt=0, lse=P, ws=P, n=need, first=P, shared=P, count=2, reserved=0, scp=P, nsc=sc):
+        c, b = None if c is None else by(q.q4nx_kv_cache(*c.values())), None if b is None else by(q.q4nx_kv_batch(*b.values()))
+        g = q.q4nx_kv_groups(first, shared, count, reserved)
+        return (L.q4nx_kv_attention_shared(c, b, by(g), qx, qs, heads, 0.1, out, dt, lse, ws, n, scp, nsc, None),)
+
+    def both(**kw):
+        c, b = kw.pop("c", cache), kw.pop("b", batch)
+        a = dict(qx=P, qs=4096, heads=32, out=P, dt=0, lse=P, ws=P, n=need)
+        a.update(kw)
+        cross = L.q4nx_kv_attention_cross(None if c is None else by(q.q4nx_kv_cache(*c.values())), None if b is None else by(q.q4nx_kv_batch(*b.values())),
+                                          a["qx"], a["qs"], a["heads"], 0.1, a["out"], a["dt"], a["lse"], a["ws"], a["n"], None)
+        return cross, *calls(c=c, b=b, **kw)
+
+    assert both(c=None) == (1, 1) and both(b=None) == (1, 1) and both(qx=None) == (1, 1) and both(out=None) == (1, 1)
+    assert both(c=dict(cache, dim=96)) == (3, 3) and both(b=dict(batch, batch=1025)) == (3, 3) and both(b=dict(batch, c=P + 2)) == (5, 5)
+    assert [both(heads=h) for h in (0, 12, 1032)] == [(3, 3)] * 3 and both(qs=4088) == (3, 3) and both(qs=4100) == (5, 5)
+    assert both(dt=2) == (11, 11) and both(lse=P + 2) == (5, 5) and both(qx=P + 8) == (5, 5) and both(out=P + 2) == (5, 5)
+    assert both(ws=None) == (7, 7) and both(n=need - 1) == (7, 7) and both(ws=P + 8) == (5, 5)
+    assert calls(first=None) == (1,) and calls(shared=None) == (1,) and calls(reserved=1) == (2,)
+    assert [calls(count=n) for n in (0, -1, 1025)] == [(3,)] * 3 and calls(first=P + 2) == (5,) and calls(shared=P + 1) == (5,)
+    assert calls(scp=None) == (7,) and calls(nsc=sc - 1) == (7,) and calls(scp=P + 8) == (5,)
+    assert L.q4nx_kv_attention_shared(by(c0), by(q.q4nx_kv_batch(*batch.values())), None, P, 4096, 32, 0.1, P, 0, P, P, need, P, sc, None) == 1
+    # nothing to do: accepted without a launch
+    assert both(b=dict(batch, tokens=0)) == (0, 0)
 
 
 def test_rotary_binding_refuses(q):
