@@ -26,7 +26,9 @@ namespace {
 // up to 128 rows, the other one a pass for each 16: one request of 16384 tokens, 8 kv
 // heads of 128 channels: 64 rows 47 (there) and 49 us (tensor cores), 68 rows 53 and 49,
 // 256 rows 115 and 57; 16 requests of 4096: 64 rows 119 and 137, 68 rows 143 and
-// 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125.
+// 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125.  Where every
+// row sees everything (cross attention, prefixes) much the same, its two tiles sharing what few rows there
+// are: one request of 65536, 64 rows 110 and 111, 128 rows 193 and 113; 64 channels: 78 and 87, 143 and 88.
 constexpr int kManyRows = 65;
 
 // The workspace: the error word, a counter and a record per CTA and pass, then any

@@ -13,6 +13,7 @@ constexpr int kUnitCost = 4;                     // what a unit costs besides it
 // kernel for many rows takes 2 us, and up to so many come on top of a CTA's share
 template <int RB>
 constexpr int cut_steps = RB < 128 ? 4 : 2;
+constexpr int kWholeSteps = 24;
 // A CTA's least share.  The parts of a unit are joined by one CTA (few rows), so that a
 // unit of n steps is cut into 1.7 sqrt(n) parts at most, where joining takes as long as
 // they do: one request of 51015 tokens, one kv head of 128 channels (n = 1594) by 266
@@ -256,6 +257,9 @@ __device__ int64_t bound(const A& a, const Plan& pl, int c) {
   const int64_t x = q * c + (c < rest ? c : rest);
   const Unit u = find_unit<SB, RB>(a, pl, x, true);
   const int64_t in = x - u.cost - kUnitCost;
+  // short units are not cut: a warp has three steps of them, joining the parts of CTAs takes longer
+  // (48 requests of 60 to 600 tokens of their own behind a prefix, 8 kv heads: 65 us in all, 60 uncut)
+  if (A::kSee == kOwn && RB < 128 && u.rq.low > 0 && u.n <= kWholeSteps) return u.start + (2 * in < u.n ? 0 : u.n);
   return u.start + (in < cut_steps<RB> && in < u.n - cut_steps<RB> + 1 ? 0 : in > u.n - cut_steps<RB> ? u.n : in);
 }
 // The CTA whose share of the costs holds x.
@@ -301,15 +305,26 @@ __device__ __forceinline__ RowScale row_scale(const A& a, bool split, int64_t at
   if (head && a.lse != nullptr) a.lse[at] = log_total(m, l);
   return {l == 0.f ? 0.f : 1.f / l, 0.f};
 }
-template <typename Out, class A>
-__device__ __forceinline__ void put_row(const A& a, bool split, int64_t at, float o, RowScale s) {
+// N elements of a row, the k-th of them at at(k), their sums o(k).  What the first pass left of them is
+// loaded before anything is stored: one round trip, not one for each.
+template <typename Out, int N, class A, class At, class O>
+__device__ __forceinline__ void put_row(const A& a, bool split, RowScale s, At at, O o) {
   if constexpr (A::kSee != kCausal)
     if (split) {
-      if (a.pass == 2) put<Out>(a, at, fmaf(o, s.own, s.other * __ldcg(a.part_o + at)));
-      else a.part_o[at] = o * s.own;
+      if (a.pass == 2) {
+        float p[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) p[k] = __ldcg(a.part_o + at(k));
+#pragma unroll
+        for (int k = 0; k < N; ++k) put<Out>(a, at(k), fmaf(o(k), s.own, s.other * p[k]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) a.part_o[at(k)] = o(k) * s.own;
+      }
       return;
     }
-  put<Out>(a, at, o * s.own);
+#pragma unroll
+  for (int k = 0; k < N; ++k) put<Out>(a, at(k), o(k) * s.own);
 }
 // A second pass runs beside the first one until it needs what that left; nothing of it ends before.
 template <class A>

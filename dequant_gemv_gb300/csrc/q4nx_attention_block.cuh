@@ -32,7 +32,10 @@
 // start takes 8.6 us: plan, the first blocks' arrival, cold code.
 // What else was tried: two issuing warps, one for each tile: they fall into step
 // and leave the tensor cores idle together, 58 us instead of 52; the keys' wait
-// before the weights': 53; both products as rolled loops: 55.
+// before the weights': 53; both products as rolled loops: 55.  S in two buffers with q in
+// shared memory: 59 (a product reads A from TMEM in 34 cycles, N = 64, from shared memory in 50,
+// and the two kinds in turn run far below either); S by halves of 32 tokens, each a buffer: 64 (a product of
+// N = 32 costs nearly one of 64); sixteen decoding warps at 48 registers: 56.
 //
 // A CTA's steps (64 tokens) are a range of all units' steps; a unit cut between
 // CTAs leaves its parts in the workspace, with a record of whose they are, for
@@ -78,6 +81,11 @@ struct Control {
   volatile uint32_t abort_flag;
   volatile int odd_any[2];                          // the last step (from 1 on) with a value kept as NaN, by stage
   volatile int odd[2][4][kTok];                     // that of a group's token
+  uint64_t half_full, half_empty;                   // a paired unit's second half
+  struct {
+    float ref, l;
+    uint32_t odd;
+  } half[kTile];                                    // of its rows
   int64_t begin, end;
   int64_t prefix[kKvMaxBatch + 1], cost[kKvMaxBatch + 1];
 };
@@ -212,6 +220,10 @@ __device__ __forceinline__ Span span_of(const A& a, const Unit& u, int from, int
 
 // A CTA's range, piece by piece (a piece: its part of one unit), the same for
 // every warp: steps that no row sees are left out by all of them.
+// A unit of one tile's rows, where all rows see all positions, is taken by both tiles in turn, a step each, so that
+// the products of one are under way while the other's weights are formed; at the end of a
+// piece the first adds the second's sums to its own, out of TMEM.  128 rows over 65536
+// positions, 8 kv heads of 128 channels: 129 us by one tile, 113 by both; decoding bounds it then, 1.8 us a step.
 struct Range {
   int lo, hi;
 };
@@ -370,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       c.odd_any[s] = 0;
     }
     mbar_init(&c.drain, 1);
+    mbar_init(&c.half_full, 4), mbar_init(&c.half_empty, 4);
     c.abort_flag = 0;
     fence_barrier_init();
   }
@@ -438,13 +451,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     bool ok = true;
     for (; ok; next_piece(a, pl, c, w, steps)) {
       const Range r0 = range_of(w, span_of(a, w.u, 0, kTile)), r1 = range_of(w, span_of(a, w.u, kTile, kTile));
+      const bool pair = SEE == kAll && w.s.rows <= kTile;
       uint32_t fresh = 0;                                            // nothing in O yet
       for (int n = w.r.lo; n <= w.r.hi && ok; ++n) {                 // and once more for the last p v
         const bool more = n < w.r.hi;
         bool keys = false;                                           // they are there
         const int b = __shfl_sync(0xffffffffu, j & 1, 0);
 #pragma unroll 1
-        for (int t = 0; t < 2 && ok; ++t) {
+        for (int i = 0; i < 2 && ok; ++i) {
+          const int t = pair ? i ^ (n & 1) : i;                      // paired: S of this step, then p v of the step before
           const uint32_t bit = 1u << t, cols = __shfl_sync(0xffffffffu, tm + t * Y::kCols, 0);
           if (pending & bit) {                                       // O (+)= p v of the step before, while the other tile's p are formed
             if (!(ok = wait(c, &c.p_full[t], (turn >> t & 1) ^ 1, a.err))) break;      // whose warps have waited for this step's v_full
@@ -456,10 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
             mma64<idesc(D), 8, 32, 40>(o, p, v + D * 128 / 16, 1);   // p_hi v_lo
             pending ^= bit, fresh &= ~bit;
           }
-          if (t == 1 && n > w.r.lo) commit(&c.v_empty[b ^ 1]);       // the step before is done with: its values' place
+          if (i == 1 && n > w.r.lo) commit(&c.v_empty[b ^ 1]);       // the step before is done with: its values' place
           if (!more) {
             if (open & bit) commit(&c.o_full[t]);
-          } else if (n >= (t ? r1.lo : r0.lo) && n < (t ? r1.hi : r0.hi)) {
+          } else if (pair ? i == 0 : n >= (t ? r1.lo : r0.lo) && n < (t ? r1.hi : r0.hi)) {
             if (!(open & bit)) {
               if (!(ok = wait(c, &c.q_ready[t], begun >> t & 1, a.err))) break;
               open |= bit, fresh |= bit, begun ^= bit;
@@ -518,19 +533,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     const int t = (warp - kWarpSoft0) >> 2, row = kTile * t + 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + t * Y::kCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     int turn = 0;                                                    // steps of the tile
-    int piece = 0;
+    int piece = 0, pairs = 0;                                        // with products, paired
     const float none = -__int_as_float(0x7f800000), c2 = a.scale_log2;
     bool ok = true;
     for (; ok; next_piece(a, pl, c, w, steps)) {
       const int64_t x0 = c.begin + w.at, row0 = w.u.rg * kRows, left = w.u.rq.T * a.group - row0;
-      const bool have = row < w.s.rows;                              // those that have none take the last, and keep nothing of it
-      const int64_t r = row0 + (row < left ? row : left - 1), tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
+      const bool pair = SEE == kAll && w.s.rows <= kTile;
+      const int mine = pair ? row & (kTile - 1) : row;
+      const bool have = mine < w.s.rows && !(pair && t == 1);        // those that have none take the last, and keep nothing of it
+      const int64_t r = row0 + (mine < left ? mine : left - 1), tq = quot(r, a.group), head = w.u.h * a.group + (r - tq * a.group);
       const int64_t pos = w.u.rq.L - w.u.rq.T + tq;
       const int64_t hi = SEE != kAll && pos < w.u.rq.L ? pos : w.u.rq.L - 1;                // the row sees lo < position <= hi
       const int64_t lo = SEE == kOwn ? w.u.rq.low - 1 : SEE == kCausal && a.window > 0 && pos - a.window > -1 ? pos - a.window : -1;
       // the positions that all rows of the warp see; later rows see from and to later ones
       const int64_t all_lo = __shfl_sync(0xffffffffu, lo, 31), all_hi = __shfl_sync(0xffffffffu, hi, 0);
-      const Range own = range_of(w, span_of(a, w.u, kTile * t, kTile));
+      Range own = range_of(w, span_of(a, w.u, kTile * t, kTile));
+      const int stride = pair ? 2 : 1, j0 = j;
+      if (pair) own = {w.r.lo + ((w.r.lo & 1) ^ t), w.r.hi};
       // the query row into TMEM (bf16 pairs, a column each); the piece before has no products left that read it
       const uint4* q = reinterpret_cast<const uint4*>(a.q + (w.u.rq.q0 + tq) * a.q_stride + head * D);
 #pragma unroll
@@ -550,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       float ref = kRefNone, l = 0.f;
       uint32_t odd = 0;                                             // groups in which the row has seen a NaN
       j += own.lo - w.r.lo;
-      for (int n = own.lo; n < own.hi; ++n, ++j) {
+      for (int n = own.lo; n < own.hi; n += stride, j += stride) {
         const int b = j & 1;
         if (!begun && lane == 0) arrive(&c.q_ready[t]);
         const int64_t t0 = (w.step0 + n) * kTok;
@@ -638,9 +657,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         begun = true;
       }
       if (!ok) break;
-      j += w.r.hi - own.hi;
+      j = j0 + (w.r.hi - w.r.lo);
       if (begun && !(ok = wait(c, &c.o_full[t], piece++ & 1, a.err))) break;
       tc_fence_after();
+      float f0 = 1.f, f1 = 0.f;                                     // on the tile's O, on the other's
+      if (pair) {
+        if (t == 1) {
+          c.half[mine].ref = ref, c.half[mine].l = l, c.half[mine].odd = odd;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(&c.half_full);
+          if (!(ok = wait(c, &c.half_empty, pairs++ & 1, a.err))) break;      // read out: the next piece may take its place
+          if (w.end >= steps) break;
+          continue;
+        }
+        if (!(ok = wait(c, &c.half_full, pairs & 1, a.err))) break;
+        tc_fence_after();
+        const float ref1 = c.half[mine].ref, l1 = c.half[mine].l, top = fmaxf(ref, ref1);
+        f0 = ex2(ref - top);
+        if (w.r.hi - w.r.lo > (begun ? 1 : 0)) f1 = ex2(ref1 - top);      // else the other tile has no step in the piece
+        l = fmaf(f0, l, f1 * l1), ref = top, odd |= c.half[mine].odd;
+      }
       // O to the output, or as a part to the workspace
       const bool whole = x0 == w.u.start && w.end == w.u.start + w.u.n - c.begin, first = w.u.start >= c.begin;
       float* part = a.partial + static_cast<int64_t>(2 * blockIdx.x + (first ? 1 : 0)) * kRows * (D + 2);
@@ -664,23 +701,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           if (!begun || l == 0.f) o[k] = 0;
+        if (SEE == kAll && pair && f1 != 0.f) {
+          uint32_t other[32];
+          tmem_load(lanes + Y::kCols + Y::kO + 32 * h, other);
+          tmem_wait_load(other);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(f0, __uint_as_float(o[k]), f1 * __uint_as_float(other[k])));
+        }
         if (odd >> h & 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0x7fc00000u;
         if (SEE != kCausal && split && have && whole) {
-          if constexpr (SEE != kCausal)
+          if constexpr (SEE != kCausal) {
+            float4 p[8];                                            // all of them before the first store: one round trip
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              float4 y = make_float4(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv, __uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
-              if (a.pass == 1) {
-                *reinterpret_cast<float4*>(a.part_o + at * D + 32 * h + k) = y;
-                continue;
-              }
-              const float4 p = __ldcg(reinterpret_cast<const float4*>(before + 32 * h + k));
-              y = make_float4(fmaf(sc.other, p.x, y.x), fmaf(sc.other, p.y, y.y), fmaf(sc.other, p.z, y.z), fmaf(sc.other, p.w, y.w));
-              if constexpr (sizeof(Out) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + 32 * h + k) = y;
-              else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 32 * h + k) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            for (int k = 0; k < 8; ++k)
+              p[k] = a.pass == 2 ? __ldcg(reinterpret_cast<const float4*>(before + 32 * h) + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 y = make_float4(fmaf(sc.other, p[k].x, __uint_as_float(o[4 * k]) * inv), fmaf(sc.other, p[k].y, __uint_as_float(o[4 * k + 1]) * inv),
+                                           fmaf(sc.other, p[k].z, __uint_as_float(o[4 * k + 2]) * inv), fmaf(sc.other, p[k].w, __uint_as_float(o[4 * k + 3]) * inv));
+              if (a.pass == 1) *reinterpret_cast<float4*>(a.part_o + at * D + 32 * h + 4 * k) = y;
+              else if constexpr (sizeof(Out) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + 32 * h + 4 * k) = y;
+              else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 32 * h + 4 * k) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
             }
+          }
         } else if (have && whole) {
           if constexpr (sizeof(Out) == 4) {
 #pragma unroll
@@ -703,6 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         }
       }
       tc_fence_before();
+      if (pair) {
+        __syncwarp();
+        if (lane == 0) arrive(&c.half_empty);
+        ++pairs;
+      }
       if (have && !whole) *(reinterpret_cast<float2*>(part + kRows * D) + row) = make_float2(ref, l);
       if (!whole && first && row == 0) {
         // this CTA has the unit's first part: the others are those of the next CTAs up to the unit's end
@@ -764,10 +814,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
   if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (SEE != kCausal)
     if (u.split) {
-      put_row<Out>(a, true, at * D + 4 * c4, o.x, sc);
-      put_row<Out>(a, true, at * D + 4 * c4 + 1, o.y, sc);
-      put_row<Out>(a, true, at * D + 4 * c4 + 2, o.z, sc);
-      put_row<Out>(a, true, at * D + 4 * c4 + 3, o.w, sc);
+      const float sums[4] = {o.x, o.y, o.z, o.w};
+      put_row<Out, 4>(a, true, sc, [&](int k) { return at * D + 4 * c4 + k; }, [&](int k) { return sums[k]; });
       return;
     }
   if constexpr (sizeof(Out) == 4)

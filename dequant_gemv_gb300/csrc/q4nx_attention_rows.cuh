@@ -578,14 +578,13 @@ __device__ __forceinline__ void join_parts(const A& a, Smem<D, NT, A::kSee>& sm,
       o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
     }
     if (have && way == 0) {
+      wait_first_pass(a);
       const float2 t = total[r];
       const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
       const RowScale sc = row_scale(a, u.split, at, t.x, t.y, (item & (D / 4 - 1)) == 0);
       const int64_t d = at * D + (item & (D / 4 - 1)) * 4;
-      put_row<Out>(a, u.split, d, t.y == 0.f ? 0.f : o.x, sc);
-      put_row<Out>(a, u.split, d + 1, t.y == 0.f ? 0.f : o.y, sc);
-      put_row<Out>(a, u.split, d + 2, t.y == 0.f ? 0.f : o.z, sc);
-      put_row<Out>(a, u.split, d + 3, t.y == 0.f ? 0.f : o.w, sc);
+      const float sums[4] = {o.x, o.y, o.z, o.w};
+      put_row<Out, 4>(a, u.split, sc, [&](int k) { return d + k; }, [&](int k) { return t.y == 0.f ? 0.f : sums[k]; });
     }
   }
 }
@@ -748,11 +747,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
             const float l = e ? st.l[t].y : st.l[t].x;
             const int64_t at = out_row(a, p.q0, p.h, p.row0 + r);
             const RowScale sc = row_scale(a, p.split, at, e ? st.ref[t].y : st.ref[t].x, l, tk == 0);
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m) {
-              put_row<Out>(a, p.split, at * D + 16 * m + tk, l == 0.f ? 0.f : st.o[t][m][e], sc);
-              put_row<Out>(a, p.split, at * D + 16 * m + tk + 8, l == 0.f ? 0.f : st.o[t][m][e + 2], sc);
-            }
+            put_row<Out, D / 8>(a, p.split, sc, [&](int k) { return at * D + 8 * k + tk; },
+                                [&](int k) { return l == 0.f ? 0.f : st.o[t][k >> 1][e + 2 * (k & 1)]; });
           }
         }
     } else {
@@ -775,8 +771,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
     }
   }
   __syncthreads();
-  wait_first_pass(a);
-  if (sm.stopped) return;
+  if (sm.stopped) {
+    wait_first_pass(a);
+    return;
+  }
 
   // Weights of the parts: entry c, row r against the largest reference among
   // the entries of the same unit.
@@ -837,10 +835,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
       const float2 v = sm.total[e0][r];
       const bool head = e < 2 && warp < 4 && tk == 0;             // one thread per row
       if (inside) {
+        wait_first_pass(a);
         const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
         const RowScale sc = row_scale(a, u.split, at, v.x, v.y, head);
-#pragma unroll
-        for (int j = 0; j < kEach / NT; ++j) put_row<Out>(a, u.split, at * D + d0 + 32 * j, v.y == 0.f ? 0.f : o[t * (kEach / NT) + j], sc);
+        put_row<Out, kEach / NT>(a, u.split, sc, [&](int j) { return at * D + d0 + 32 * j; },
+                                 [&](int j) { return v.y == 0.f ? 0.f : o[t * (kEach / NT) + j]; });
       } else {
 #pragma unroll
         for (int j = 0; j < kEach / NT; ++j) __stcg(part + r * D + d0 + 32 * j, o[t * (kEach / NT) + j]);
@@ -848,7 +847,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
       }
     }
   }
-  if (edge[0] < 0 && edge[1] < 0) return;
+  if (edge[0] < 0 && edge[1] < 0) {
+    wait_first_pass(a);
+    return;
+  }
   __syncthreads();
   // the CTAs with a part of a unit: those whose shares begin where it may be cut, and the one before
   if (tid < 2 && edge[tid] >= 0) {
@@ -865,6 +867,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) attentio
 #pragma unroll 1
   for (int k = 0; k < 2; ++k)
     if (edge[k] >= 0 && sm.joins[k] >= 0) join_parts<D, NT, Out>(a, sm, sm.cut[edge[k]], sm.joins[k] >> 16, sm.joins[k] & 0xFFFF);
+  wait_first_pass(a);
 }
 
 template <int D, int NT, typename Out, int SEE>

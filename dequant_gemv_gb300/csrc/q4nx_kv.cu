@@ -30,7 +30,7 @@ template <int D>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(KvPool pool, KvBatch kb, const uint16_t* __restrict__ k,
                                                                  const uint16_t* __restrict__ v, int64_t stride,
                                                                  uint32_t* err) {
-  constexpr int VPL = D / 32, NG = D / 32, LPG = 32 / VPL;      // values per lane, groups, lanes per group
+  constexpr int VPL = D / 32;                                   // values per lane
   __shared__ __align__(16) uint8_t codes[kKvWarps][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -151,8 +151,7 @@ __global__ void __launch_bounds__(kWarps * 32) turn_blocks_kernel(const TurnArgs
   __shared__ __align__(16) float2 table[kKvBlock][kRow];
   __shared__ __align__(16) uint8_t image[kWarps][512];          // value codes of two groups of a block
   __shared__ struct {
-    KvRequest rq;
-    int64_t blk;
+    int64_t q0, T, L, blk;
     int b;
   } at;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -167,11 +166,11 @@ __global__ void __launch_bounds__(kWarps * 32) turn_blocks_kernel(const TurnArgs
     int b = -1;
     KvRequest rq = {};
     if (left != INT64_MAX) rq = locate_block(a.kb, a.pool.page_blocks, left, b);
-    if (lane == 0) at.rq = rq, at.blk = (rq.L > rq.T ? rq.L - rq.T : 0) / kKvBlock + left, at.b = b;
+    if (lane == 0) at.q0 = rq.q0, at.T = rq.T, at.L = rq.L, at.blk = (rq.L > rq.T ? rq.L - rq.T : 0) / kKvBlock + left, at.b = b;
   }
   __syncthreads();
   if (at.b < 0) return;
-  const KvRequest rq = at.rq;
+  const KvRequest rq = {at.q0, at.T, at.L, true};
   const int64_t blk_at = at.blk, from = rq.L > rq.T ? rq.L - rq.T : 0, p0 = blk_at * kKvBlock;
   const int64_t end = rq.L < c.positions ? rq.L : c.positions;  // positions from `from` to here have a place in cache and table
   const int first = static_cast<int>(from > p0 ? from - p0 : 0), last = static_cast<int>(end - p0 < kKvBlock ? (end > p0 ? end - p0 : 0) : kKvBlock);
