@@ -71,7 +71,7 @@ bool many_rows(int D, int64_t rows, int64_t count) { return D <= 128 && rows >= 
 template <int SEE>
 cudaError_t launch_pass(int D, const AttnArgsOf<SEE>& a, int64_t count, int out_f32, const DeviceInfo& info, cudaStream_t s) {
   const int64_t rows = a.kb.tokens * a.group;
-  if (many_rows(D, rows, count)) return launch_attention_block<SEE>(D, a, out_f32, info, s);
+  if (many_rows(D, rows, count)) return launch_attention_block<SEE>(D, a, count, out_f32, info, s);
   return launch_attention_rows<SEE>(D, rows > 8 * count, a, out_f32, info, s);
 }
 

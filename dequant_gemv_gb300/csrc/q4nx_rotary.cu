@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32) turn_tokens_kernel(const TurnArgs
 // (kKvHeads of them a CTA), then query heads (kQHeads).
 template <int D>
 constexpr int kKvHeads = D == 256 ? 2 : D == 128 ? 4 : 8;
-constexpr int kQHeads = 8;
+constexpr int kQHeads = 16;
 
 // Whether a lane that holds a group of 32 channels finds their partners in it or in its neighbour lane's.
 __host__ __device__ __forceinline__ bool by_groups(int half, bool interleaved) { return interleaved || half % 32 == 0 || half == 16; }
