@@ -115,7 +115,9 @@ cudaError_t launch_attention_shared(int D, const KvPool& pool, const KvBatch& kb
   a.part_o = b.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + parts_bytes(D));
   a.part_ml = b.part_ml = reinterpret_cast<float2*>(a.part_o + kb.tokens * heads * D);
   // The tensor-core kernel has a second launch that joins its parts: it comes last, so
-  // that nothing starts behind that launch.
+  // that nothing starts behind that launch.  Otherwise the prefixes, which are the larger part, come first
+  // (16 requests behind 65537 positions 127 us, own parts first 134).  Both at the same time on SMs divided by what
+  // they cost gained 3 of 60 us for 48 requests behind 8191 positions and took a model of the costs: not kept.
   const bool prefix_last = many_rows(D, kb.tokens * a.group, groups) && !many_rows(D, kb.tokens * a.group, kb.batch);
   a.pass = prefix_last ? 2 : 1;
   b.pass = prefix_last ? 1 : 2;

@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       bool split = false;
       if constexpr (SEE == kOwn) split = w.u.rq.low > 0;
       else if constexpr (SEE == kAll) split = a.pass != 0;
-      wait_first_pass(a);
+      if (whole) wait_first_pass(a);                                // parts need nothing of it, and further pieces may follow
       RowScale sc = {0.f, 0.f};
       if (have && whole) sc = row_scale(a, split, at, ref, l, true);
       const float inv = sc.own;
