@@ -14,7 +14,7 @@
 // 28 tcgen05.mma (M = 128, K = 16) per 128 rows and 64 tokens at 128 channels,
 // accumulated in binary32 in TMEM.
 //
-// Twenty warps, one CTA per SM: a loader (bulk copies of the cache's blocks), the
+// Twenty warps (two of them idle), one CTA per SM: a loader (bulk copies of the cache's blocks), the
 // MMA issuer, eight softmax warps (a thread is a row: its logits come from TMEM,
 // its p take their place there, as the A operand of the second product) and eight
 // decoding warps (codes to bf16 pairs in shared memory, 128-byte swizzle: keys as
@@ -56,6 +56,7 @@ constexpr int kThreads = 640, kDecodeWarps = 8, kRawStages = 4;
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpSoft0 = 4, kWarpDecode0 = 12;
 // registers per thread: 96 at launch, shared out anew (4, 8 and 8 warps)
 constexpr int kRegsRest = 64, kRegsSoft = 144, kRegsDecode = 64;
+static_assert(kRegsRest >= kRegsDecode, "two decoding warps are of the first four");
 static_assert(4 * kRegsRest + 8 * kRegsSoft + 8 * kRegsDecode <= kThreads / 32 * 96, "the split draws on the launch's registers");
 constexpr uint32_t kTmemCols = 512;
 
@@ -502,11 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     }
     commit(&c.drain);                                                // every product issued so far has completed
     mbar_wait_bounded(&c.drain, 0, 100000000ull);
-  } else if (warp >= kWarpDecode0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+  } else if (warp >= kWarpDecode0 || warp == 2 || warp == 3) {
+    if (warp >= kWarpDecode0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+    // on the three schedulers that do not issue the products (warps 13 and 17 would be on theirs and have
+    // nothing to do): 4 prompts of 449 tokens over up to 6000 positions, 32 heads 276 -> 254 us
+    const int d = warp < 4 ? warp - 2 : warp == 12 ? 2 : warp < 16 ? warp - 11 : warp == 16 ? 5 : warp - 12;
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
-    const int d = warp - kWarpDecode0, blk = d >> 1, half = d & 1;
-    bool ok = true;
+    const int blk = d >> 1, half = d & 1;
+    bool ok = warp != 13 && warp != 17;
     for (; ok; next_piece(a, pl, c, w, steps)) {
       for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int b = j & 1, r = j % kRawStages;
