@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_kernel(KvPool pool, K
       x[j] = bf16_bits_to_f32(w & 0xFFFF);
       x[j + 1] = bf16_bits_to_f32(w >> 16);
     }
-    keep_token<D>(blk, t, which, x, codes[warp]);
+    keep_token<D>(blk, t, which, false, x, codes[warp]);
   }
 }
 
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_append_blocks_kernel(KvPool 
     hi = fmaxf(hi, fmaxf(x, y));
     bad |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
   }
-  keep_group<D>(blk, blk_at * kKvBlock >= from && blk_at * kKvBlock + kKvBlock <= rq.L, mine, t, g, which, lo, hi, bad,
+  keep_group<D>(blk, blk_at * kKvBlock >= from && blk_at * kKvBlock + kKvBlock <= rq.L, mine, t, g, which, false, lo, hi, bad,
                 [&](int j) { return j & 1 ? __uint_as_float(w[j >> 1] & 0xFFFF0000u) : __uint_as_float(w[j >> 1] << 16); }, image[warp]);
 }
 

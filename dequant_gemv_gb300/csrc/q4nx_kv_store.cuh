@@ -19,8 +19,11 @@ __device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv
   return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -8.f), 7.f)) + 8);
 }
 // Scale and middle of a group with smallest and largest value lo, hi; `bad`: one is no number.
-__device__ __forceinline__ void scale_of(float lo, float hi, bool bad, uint32_t& s_bits, uint32_t& m_bits) {
-  s_bits = f32_to_bf16_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+// The range is divided by 15; that of turned keys is multiplied by the 32-bit number nearest to 1/15, one
+// operation, which is one bf16 step from the quotient's in about one group of 16000.
+__device__ __forceinline__ void scale_of(float lo, float hi, bool bad, bool turned, uint32_t& s_bits, uint32_t& m_bits) {
+  const float range = __fsub_rn(hi, lo);
+  s_bits = f32_to_bf16_bits(turned ? __fmul_rn(range, 1.0f / 15.0f) : __fdiv_rn(range, 15.0f));
   const float s = bf16_bits_to_f32(s_bits);
   m_bits = f32_to_bf16_bits(__fadd_rn(lo, __fmul_rn(8.0f, s)));
   const float inf = __int_as_float(0x7f800000);
@@ -28,9 +31,9 @@ __device__ __forceinline__ void scale_of(float lo, float hi, bool bad, uint32_t&
 }
 
 // One token's keys (which 0) or values (1) of a head into its block: by a warp, lane l
-// with channels VPL*l .. of it; `codes` is the warp's.
+// with channels VPL*l .. of it; `codes` is the warp's.  turned: see scale_of.
 template <int D>
-__device__ __forceinline__ void keep_token(uint8_t* blk, int t, int which, const float (&x)[D / 32], uint8_t (&codes)[D]) {
+__device__ __forceinline__ void keep_token(uint8_t* blk, int t, int which, bool turned, const float (&x)[D / 32], uint8_t (&codes)[D]) {
   constexpr int VPL = D / 32, NG = D / 32, LPG = 32 / VPL;      // values per lane, groups, lanes per group
   const int lane = threadIdx.x & 31;
   float lo = x[0], hi = x[0];
@@ -48,7 +51,7 @@ __device__ __forceinline__ void keep_token(uint8_t* blk, int t, int which, const
     bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), o) != 0;
   }
   uint32_t s_bits, m_bits;
-  scale_of(lo, hi, bad, s_bits, m_bits);
+  scale_of(lo, hi, bad, turned, s_bits, m_bits);
   const float s = bf16_bits_to_f32(s_bits), m = bf16_bits_to_f32(m_bits), inv = 1.f / s;
   if (lane % LPG == 0) {
     const int g = lane / LPG;
@@ -118,14 +121,14 @@ __device__ __forceinline__ KvRequest locate_block(const KvBatch& kb, int page_bl
 // One group g of token t of a block, keys or values, by a lane: x(j) its values, lo and hi
 // their extremes, bad: one is no number.  The warp's lanes 2t + e hold two groups of
 // every token, for values neighbouring ones (`image`: the warp's place to gather their bytes).
-// mine: the token is the call's; whole: all 16 are.
+// mine: the token is the call's; whole: all 16 are; turned: see scale_of.
 template <int D, typename X>
-__device__ __forceinline__ void keep_group(uint8_t* blk, bool whole, bool mine, int t, int g, int which, float lo, float hi, bool bad,
+__device__ __forceinline__ void keep_group(uint8_t* blk, bool whole, bool mine, int t, int g, int which, bool turned, float lo, float hi, bool bad,
                                            X x, uint8_t (&image)[512]) {
   constexpr int NG = D / 32;
   const int lane = threadIdx.x & 31;
   uint32_t s_bits, m_bits;
-  scale_of(lo, hi, bad, s_bits, m_bits);
+  scale_of(lo, hi, bad, turned, s_bits, m_bits);
   const float s = bf16_bits_to_f32(s_bits), m = bf16_bits_to_f32(m_bits), inv = 1.f / s;
   uint32_t c[4] = {};                                           // channel 8i + 2j, +1 of the group: nibbles j, j + 4 of c[i]
 #pragma unroll

@@ -5,7 +5,7 @@
 //   a' = a c - b s,  b' = b c + a s,
 // every product, difference and sum one IEEE binary32 operation, so that every machine
 // takes the same codes.  Keys go from there into codes as in q4nx_kv.cu, without a rounding to
-// bf16 between; queries leave as bf16.  Cosines and sines come from the caller's
+// bf16 between, but that a group's range is multiplied by 1/15 instead of divided (scale_of); queries leave as bf16.  Cosines and sines come from the caller's
 // table: they are made once in 64 bits (positions times frequencies lose their angle
 // in 32), and a token's 8 bytes a pair are shared by all of its heads.
 //
@@ -130,10 +130,10 @@ __global__ void __launch_bounds__(kWarps * 32) turn_tokens_kernel(const TurnArgs
   }
   const int t = static_cast<int>(pos % kKvBlock);
   turn_token<D>(c, pos, raw[0], x);
-  keep_token<D>(blk, t, 0, x, codes[warp]);
+  keep_token<D>(blk, t, 0, true, x, codes[warp]);
 #pragma unroll
   for (int j = 0; j < VPL / 2; ++j) x[2 * j] = lo16(raw[1][j]), x[2 * j + 1] = hi16(raw[1][j]);
-  keep_token<D>(blk, t, 1, x, codes[warp]);
+  keep_token<D>(blk, t, 1, false, x, codes[warp]);
 }
 
 // A CTA per 16-token block that the call writes and part of the heads: kv heads first
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kWarps * 32) turn_blocks_kernel(const TurnArgs
       hi = fmaxf(hi, x[j]);
       bad |= !(fabsf(x[j]) < __int_as_float(0x7f800000));
     }
-    keep_group<D>(blk, first == 0 && last == kKvBlock, mine, t, g, which, lo, hi, bad, [&](int j) { return x[j]; }, image[warp]);
+    keep_group<D>(blk, first == 0 && last == kKvBlock, mine, t, g, which, which == 0, lo, hi, bad, [&](int j) { return x[j]; }, image[warp]);
     __syncwarp();                                               // the image is read out
   }
 }

@@ -293,8 +293,8 @@ typedef struct q4nx_rotary {
 
 /* q4nx_kv_append with the call's keys, and its queries, turned by their positions on the way:
  *   a' = a cos - b sin,  b' = b cos + a sin,  each step one IEEE binary32 operation.
- * Keys are quantised from these binary32 numbers by the rule of q4nx_kv_append, values
- * as there.  q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token, or NULL
+ * Keys are quantised from these binary32 numbers by the rule of q4nx_kv_append, but for
+ * scale = bf16((hi - lo) * f) with f = 1/15 rounded to binary32; values as there.  q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token, or NULL
  * (keys alone; heads and the q_out arguments are not looked at).  q_out_dev: the turned queries, rounded
  * to bf16, q_out_stride elements from token to token; it may be q_dev itself with its stride,
  * other overlaps with the inputs are not allowed.  Strides are multiples of 8.  heads: 1..1024, any number.

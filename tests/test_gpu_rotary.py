@@ -25,6 +25,19 @@ def turn(x, pos, table, interleaved):
     return y
 
 
+def kept(x):
+    """What the cache keeps of turned keys: the rule of the plain append, the range times 1/15 in binary32."""
+    v = x.astype(np.float32).reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
+    with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
+        lo, hi = v.min(-1), v.max(-1)
+        s = _bf16((hi - lo) * (np.float32(1) / np.float32(15)))
+        m = _bf16(lo + np.float32(8) * s)
+        c = np.where(s[..., None] == 0, 0, np.clip(np.rint((v - m[..., None]) / s[..., None]), -8, 7))
+        bad = (~np.isfinite(v).all(-1) | ~np.isfinite(s) | ~np.isfinite(m))[..., None]
+    s, m, c = s.astype(np.float64)[..., None], m.astype(np.float64)[..., None], np.nan_to_num(c).astype(np.float64)
+    return np.where(bad, np.nan, c * s + m).reshape(x.shape).astype(np.float32)
+
+
 def positions(c):
     return np.concatenate([np.arange(n - t, n) for n, t in zip(c.lens, c.new)]) if c.lens else np.zeros(0, int)
 
@@ -49,7 +62,7 @@ def run(q, c, heads, dims, interleaved, merged=True, in_place=False):  # noqa: F
     assert not in_place or out.data_ptr() == qt.data_ptr()
     k, v = q.q4nx_kv_read(c.cache, len(pos), c.start, c.tlens, c.table, out_dtype="f32")
     return ((out.float().cpu().numpy(), _bf16(turn(qx, pos, table, interleaved))),
-            (k.cpu().numpy(), _values(turn(ks, pos, table, interleaved)).astype(np.float32)), (v.cpu().numpy(), _values(vs).astype(np.float32)))
+            (k.cpu().numpy(), kept(turn(ks, pos, table, interleaved))), (v.cpu().numpy(), _values(vs).astype(np.float32)))
 
 
 def equal(pairs):
@@ -119,6 +132,31 @@ def test_positions_nought_and_without_an_angle_are_the_plain_append(q):  # noqa:
     assert torch.equal(out, qx) and torch.equal(c.cache.pool, plain)
 
 
+@pytest.mark.parametrize("n", [3, 1600])
+def test_scale_of_ranges_between_two_steps(q, n):  # noqa: F811
+    """Ranges whose 15th part lies midway between two bf16 numbers: turned keys take the product, values the quotient."""
+    lo, hi = np.meshgrid(-np.arange(128, 256, dtype=np.float32) / 2 ** 11, np.arange(128, 256, dtype=np.float32) / 64)
+    d = hi - lo
+    apart = _bf16(d / np.float32(15)) != _bf16(d * (np.float32(1) / np.float32(15)))
+    lo, hi = lo[apart], hi[apart]
+    assert len(lo) > 20                                       # they are apart for these
+    c = Case(q, [n], [n], 4, 128, 16)
+    at = np.arange(n * 4 * 4) % len(lo)
+    x = np.zeros((n * 4 * 4, 32), np.float32)
+    x[:, 5], x[:, 20] = lo[at], hi[at]
+    c.k[0] = c.v[0] = x.reshape(n, 4, 128)
+    still = q.Rotary(torch.tensor([1.0, 0.0], device=DEV).repeat(n, 64, 1))
+    q.q4nx_kv_append_rotary(c.cache, still, None, dev(c.k[0]), dev(c.v[0]), c.start, c.tlens, c.table)
+    k, v = (t.cpu().numpy() for t in q.q4nx_kv_read(c.cache, n, c.start, c.tlens, c.table, out_dtype="f32"))
+    assert np.array_equal(k, kept(c.k[0])) and np.array_equal(v, _values(c.v[0]).astype(np.float32)) and not np.array_equal(k, v)
+
+
+# the case whose turned keys showed the two rules apart: one group of 16000
+def test_many_tokens_keep_the_rule(q):  # noqa: F811
+    c = Case(q, [4001, 3999], [1501, 1999], 8, 128, 64)
+    equal(run(q, c, 4, 128, False))
+
+
 def test_special_numbers(q):  # noqa: F811
     for n in (6, 1600):
         c = Case(q, [n], [n], 4, 64, 16)
@@ -149,7 +187,7 @@ def test_tokens_before_the_start(q, new):  # noqa: F811
     host = x.float().cpu().numpy()
     assert np.array_equal(out.float().cpu().numpy()[keep], _bf16(turn(host[keep, :8], pos, table, False)))
     k, _ = q.q4nx_kv_read(c.cache, 2 * new, c.start, c.tlens, c.table, out_dtype="f32")
-    assert np.array_equal(k.cpu().numpy()[keep], _values(turn(host[keep, 8:16], pos, table, False)).astype(np.float32))
+    assert np.array_equal(k.cpu().numpy()[keep], kept(turn(host[keep, 8:16], pos, table, False)))
     q.q4nx_check(device=DEV)
 
 
@@ -210,6 +248,6 @@ def test_captured_and_on_another_stream(q):  # noqa: F811
             pos = np.array([300 + n, 77 + n])
             assert np.array_equal(out.float().cpu().numpy(), _bf16(turn(x[:, :8].float().cpu().numpy(), pos, table, False)))
             k, _ = q.q4nx_kv_read(c.cache, 2, c.start, lens, c.table, out_dtype="f32")
-            assert np.array_equal(k.cpu().numpy(), _values(turn(x[:, 8:12].float().cpu().numpy(), pos, table, False)).astype(np.float32))
+            assert np.array_equal(k.cpu().numpy(), kept(turn(x[:, 8:12].float().cpu().numpy(), pos, table, False)))
     torch.cuda.current_stream().wait_stream(side)
     q.q4nx_check(device=DEV)

@@ -13,7 +13,7 @@ import torch
 
 import oracle
 from test_gpu_kv import _bf16, _values
-from test_gpu_rotary import turn
+from test_gpu_rotary import kept, turn
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -76,7 +76,7 @@ def test_layer_by_operator(ex, count, prompt, encoder):
         _within(out["qkv"], y + _n(layer.bias), tol)
         qkv, pos = out["qkv"].float().cpu().numpy(), np.full(count, prompt + n)
         assert np.array_equal(out["turned"].float().cpu().numpy(), _bf16(turn(qkv[:, :s.heads], pos, table, False)))
-        own_k.append(_values(turn(qkv[:, s.heads:s.heads + s.kv_heads], pos, table, False)).astype(np.float32).astype(np.float64))
+        own_k.append(kept(turn(qkv[:, s.heads:s.heads + s.kv_heads], pos, table, False)).astype(np.float64))
         own_v.append(_values(qkv[:, s.heads + s.kv_heads:]).astype(np.float32).astype(np.float64))
         for b in range(count):
             kb, vb = np.concatenate([pk, *[k[b:b + 1] for k in own_k]]), np.concatenate([pv, *[v[b:b + 1] for v in own_v]])
