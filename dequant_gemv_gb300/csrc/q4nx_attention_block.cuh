@@ -503,14 +503,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     }
     commit(&c.drain);                                                // every product issued so far has completed
     mbar_wait_bounded(&c.drain, 0, 100000000ull);
-  } else if (warp >= kWarpDecode0 || warp == 2 || warp == 3) {
+  } else if (warp >= kWarpDecode0 || (!PAIR && (warp == 2 || warp == 3))) {
     if (warp >= kWarpDecode0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
-    // on the three schedulers that do not issue the products (warps 13 and 17 would be on theirs and have
-    // nothing to do): 4 prompts of 449 tokens over up to 6000 positions, 32 heads 276 -> 254 us
-    const int d = warp < 4 ? warp - 2 : warp == 12 ? 2 : warp < 16 ? warp - 11 : warp == 16 ? 5 : warp - 12;
+    // On the three schedulers that do not issue the products (warps 13 and 17 would be on theirs and have
+    // nothing to do): 4 prompts of 449 tokens over up to 6000 positions, 32 heads 276 -> 254 us.  Where
+    // paired units make decoding the bound it has all four: 113 us instead of 116 for 128 rows over 65536.
+    const int d = PAIR ? warp - kWarpDecode0 : warp < 4 ? warp - 2 : warp == 12 ? 2 : warp < 16 ? warp - 11 : warp == 16 ? 5 : warp - 12;
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
     const int blk = d >> 1, half = d & 1;
-    bool ok = warp != 13 && warp != 17;
+    bool ok = PAIR || (warp != 13 && warp != 17);
     for (; ok; next_piece(a, pl, c, w, steps)) {
       for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int b = j & 1, r = j % kRawStages;
