@@ -89,7 +89,8 @@ def test_table(q, positions, dims, base):  # noqa: F811
                                       (256, 256), (256, 192), (256, 64), (256, 16), (256, 80)])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("kv,heads,lens,new", [(1, 1, [1], [1]), (2, 6, [1, 15, 16, 17, 70, 0, 130], [1, 15, 3, 17, 5, 0, 130]),
-                                               (3, 5, [700, 61, 1400, 16, 1000], [700, 60, 1357, 16, 7]), (8, 9, [801, 2000], [801, 190])])
+                                               (3, 5, [700, 61, 1400, 16, 1000], [700, 60, 1357, 16, 7]), (8, 9, [801, 2000], [801, 190]),
+                                               (4, 20, [16 + 7 * b for b in range(64)], [1 + 5 * b % 23 for b in range(64)])])
 def test_keeps_the_rule_exactly(q, dim, dims, interleaved, kv, heads, lens, new):  # noqa: F811
     c = Case(q, lens, new, kv, dim, 48, seed=dims)
     equal(run(q, c, heads, dims, interleaved))
@@ -114,25 +115,26 @@ def test_writes_only_its_tokens(q, new):  # noqa: F811
     changed = int((c.cache.pool != before).sum())
     assert 0 < changed <= sum(new) * 4 * 2 * (64 + 16)
     assert torch.all(out[sum(new):] == 3) and torch.all(out._base[:, :2] == 3) and torch.all(out._base[:, 14:] == 3)
-    again = c.cache.pool.clone()
+    again = c.cache.pool.clone()                                                           # by blocks; without queries by tokens
     assert q.q4nx_kv_append_rotary(c.cache, r, None, wide[:, 12:16], wide[:, 16:], c.start, c.tlens, c.table) is None
     assert torch.equal(c.cache.pool, again)                                                # keys alone: the same bytes
     q.q4nx_check(device=DEV)
 
 
-def test_positions_nought_and_without_an_angle_are_the_plain_append(q):  # noqa: F811
-    c = Case(q, [1, 400], [1, 400], 16, 128, 64)
+@pytest.mark.parametrize("n", [400, 1000])
+def test_positions_nought_and_without_an_angle_are_the_plain_append(q, n):  # noqa: F811
+    c = Case(q, [1, n], [1, n], 16, 128, 64)
     k, v = (dev(c.stack(x, 0, c.lens)) for x in (c.k, c.v))
     q.q4nx_kv_append(c.cache, k, v, c.start, c.tlens, c.table)
     plain = c.cache.pool.clone()
-    still = q.Rotary(torch.tensor([1.0, 0.0], device=DEV).repeat(400, 64, 1))
+    still = q.Rotary(torch.tensor([1.0, 0.0], device=DEV).repeat(n, 64, 1))
     c.cache.pool.fill_(0xFF)
-    qx = torch.randn(401, 3, 128, device=DEV).bfloat16()
+    qx = torch.randn(n + 1, 3, 128, device=DEV).bfloat16()
     out = q.q4nx_kv_append_rotary(c.cache, still, qx, k, v, c.start, c.tlens, c.table)
     assert torch.equal(out, qx) and torch.equal(c.cache.pool, plain)
 
 
-@pytest.mark.parametrize("n", [3, 1600])
+@pytest.mark.parametrize("n", [3, 4200])
 def test_scale_of_ranges_between_two_steps(q, n):  # noqa: F811
     """Ranges whose 15th part lies midway between two bf16 numbers: turned keys take the product, values the quotient."""
     lo, hi = np.meshgrid(-np.arange(128, 256, dtype=np.float32) / 2 ** 11, np.arange(128, 256, dtype=np.float32) / 64)
@@ -158,7 +160,7 @@ def test_many_tokens_keep_the_rule(q):  # noqa: F811
 
 
 def test_special_numbers(q):  # noqa: F811
-    for n in (6, 1600):
+    for n in (6, 1600, 2100):
         c = Case(q, [n], [n], 4, 64, 16)
         k = c.k[0]
         k[0, 0, 3] = np.inf                                    # at position 0: inf * 1 - x * 0, and x * 1 + inf * 0 is none
