@@ -27,9 +27,12 @@
 // Bound: the turns that a tile takes in a step of 2.1 us: softmax 1.0, the issue and
 // run of its products 0.9, the hand-over 0.2.  The products alone need 1.1 us for
 // both tiles (tensor pipe 37% busy), and the warps issue 0.6 instructions a cycle
-// and scheduler, so that neither is full: the next thing would be S in two buffers
-// beside two tiles, for which TMEM (512 columns) has no room with q in it.  The
-// start takes 8.6 us: plan, the first blocks' arrival, cold code.
+// and scheduler, so that neither is full.  Over longer ranges (4 prompts of 449 tokens over up to
+// 6000 positions, 32 heads: 253 us) the tensor pipe is busy 53% of the time
+// and 56% of the issue slots are: a step's products alone take 2570 cycles, with the other
+// roles' instructions between them 4000.  Where two tiles take one unit's tokens in turn (at most 128 rows) the
+// decoding of 128 tokens, 1.8 us a step, is the longest part.  The start takes 8.6 us: plan,
+// the first blocks' arrival, cold code.
 // What else was tried: two issuing warps, one for each tile: they fall into step
 // and leave the tensor cores idle together, 58 us instead of 52; the keys' wait
 // before the weights': 53; both products as rolled loops: 55.  S in two buffers with q in
