@@ -18,7 +18,7 @@
 // Shared (against a floor by bytes): 48 requests behind 8191 positions, 32 query
 // heads, 8 kv heads of 128: 61 us (4.7); cold and alone the requests' own 60 to 600 tokens take 24, the prefix on the
 // tensor cores 34 and its join 15; 16 requests behind 65537: 133 (14); 12 requests x 4 tokens, two groups behind 16001
-// positions, 4 kv heads of 256: 112 (5.9), six passes of 16 rows over the prefix; 4 requests behind 300: 18, two
+// positions, 4 kv heads of 256: 83 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
 // plans, look-ups and joins.  Cross: 32 requests of 410 to 4097 positions: 37 us, 2.6 TB/s, as the kernel for few rows does.
 #include "q4nx_attention_rows.cuh"
 
@@ -35,6 +35,9 @@ namespace {
 // 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125.  Where every
 // row sees everything (cross attention, prefixes) much the same, its two tiles sharing what few rows there
 // are: one request of 65536, 64 rows 110 and 111, 128 rows 193 and 113; 64 channels: 78 and 87, 143 and 88.
+// 256 channels, 4 kv heads, there alone: one request of 16384, 64 rows 53 and 53, 96 rows 62 and 55, 256 rows 119 and 79;
+// 16 of 2048: 76 and 86, 101 and 91, 222 and 168.  (Attention up to a row's own position stays with the other
+// kernel at 256 channels, whose numbers are its documented ones.)
 constexpr int kManyRows = 65;
 
 // The workspace: the error word, a counter and a record per CTA and pass, then any
@@ -71,13 +74,14 @@ void fill(AttnArgs& a, int D, const KvPool& pool, const KvBatch& kb, const void*
   a.stash = a.partial + static_cast<int64_t>(kKvMaxCtas) * 8 * 2 * (D + 2);
 }
 
-// The kernel for `rows` query rows of `count` requests.
-bool many_rows(int D, int64_t rows, int64_t count) { return D <= 128 && rows >= kManyRows * count; }
+// Whether the tensor-core kernel takes `rows` query rows of `count` requests.
+template <int SEE>
+bool many_rows(int D, int64_t rows, int64_t count) { return (D <= 128 || SEE != kCausal) && rows >= kManyRows * count; }
 
 template <int SEE>
 cudaError_t launch_pass(int D, const AttnArgsOf<SEE>& a, int64_t count, int out_f32, const DeviceInfo& info, cudaStream_t s) {
   const int64_t rows = a.kb.tokens * a.group;
-  if (many_rows(D, rows, count)) return launch_attention_block<SEE>(D, a, count, out_f32, info, s);
+  if (many_rows<SEE>(D, rows, count)) return launch_attention_block<SEE>(D, a, count, out_f32, info, s);
   return launch_attention_rows<SEE>(D, rows > 8 * count, a, out_f32, info, s);
 }
 
@@ -124,7 +128,7 @@ cudaError_t launch_attention_shared(int D, const KvPool& pool, const KvBatch& kb
   // that nothing starts behind that launch.  Otherwise the prefixes, which are the larger part, come first
   // (16 requests behind 65537 positions 127 us, own parts first 134).  Both at the same time on SMs divided by what
   // they cost gained 3 of 60 us for 48 requests behind 8191 positions and took a model of the costs: not kept.
-  const bool prefix_last = many_rows(D, kb.tokens * a.group, groups) && !many_rows(D, kb.tokens * a.group, kb.batch);
+  const bool prefix_last = many_rows<kAll>(D, kb.tokens * a.group, groups) && !many_rows<kOwn>(D, kb.tokens * a.group, kb.batch);
   a.pass = prefix_last ? 2 : 1;
   b.pass = prefix_last ? 1 : 2;
   cudaError_t e = cudaSuccess;

@@ -393,8 +393,8 @@ __device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* 
 // Few query rows per request (q4nx_attention_rows.cuh): `two` tiles of 8 at a time, or one.
 template <int SEE>
 cudaError_t launch_attention_rows(int D, bool two, const AttnArgsOf<SEE>& a, int out_f32, const DeviceInfo& info, cudaStream_t s);
-// Many query rows per request (q4nx_attention_block.cuh; 64 or 128 channels): the
-// size of the parts (0 for other sizes), and the launch.
+// Many query rows per request (q4nx_attention_block.cuh; not kCausal with 256 channels): the
+// size of the parts, and the launch.
 uint64_t attention_block_bytes(int D);
 template <int SEE>
 cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int64_t count, int out_f32, const DeviceInfo& info, cudaStream_t s);

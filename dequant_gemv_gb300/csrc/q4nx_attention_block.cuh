@@ -40,6 +40,13 @@
 // and the two kinds in turn run far below either); S by halves of 32 tokens, each a buffer: 64 (a product of
 // N = 32 costs nearly one of 64); sixteen decoding warps at 48 registers: 56.
 //
+// 256 channels (cross attention and shared parts alone): two tiles have no room. One tile of 128 rows has q in 128
+// columns, S in two buffers of 64 and O in 256, all 512, and keys and values one buffer each in shared memory.
+// S of a step is formed while the softmax of the step before is under way.  Four warps decode keys and eight values (the
+// second tile's softmax warps among them), each kind by itself: one after the other by the same eight warps a step went through
+// keys, S, p v and values in series, 4.4 us instead of 2.9. 96 rows over 16001 positions, twice, 4 kv heads: 64 us
+// (few rows' kernel 97; keys and values by 6 and 8 warps 68, 7 and 7 71, 8 and 6 70, 3 and 8 slower, 4 and 10 the same).
+//
 // A CTA's steps (64 tokens) are a range of all units' steps; a unit cut between
 // CTAs leaves its parts in the workspace, with a record of whose they are, for
 // a second kernel that joins them over the whole GPU (a part is 128 KB).
@@ -55,7 +62,7 @@ namespace {
 
 constexpr int kTile = 128, kRows = 2 * kTile;                   // rows of a tile (TMEM lanes), of a unit
 constexpr int kSB = 4, kTok = kSB * kKvBlock;                   // blocks and tokens of a step
-constexpr int kThreads = 640, kDecodeWarps = 8, kRawStages = 4;
+constexpr int kThreads = 640, kDecodeWarps = 8;
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpSoft0 = 4, kWarpDecode0 = 12;
 // registers per thread: 96 at launch, shared out anew (4, 8 and 8 warps)
 constexpr int kRegsRest = 64, kRegsSoft = 144, kRegsDecode = 64;
@@ -63,28 +70,52 @@ static_assert(kRegsRest >= kRegsDecode, "two decoding warps are of the first fou
 static_assert(4 * kRegsRest + 8 * kRegsSoft + 8 * kRegsDecode <= kThreads / 32 * 96, "the split draws on the launch's registers");
 constexpr uint32_t kTmemCols = 512;
 
+// With one tile a warp's part of the decoding: of the keys (0 ..), of the values (32 ..), or none (-1).
+__host__ __device__ constexpr int solo_task(int warp) {
+  if (warp >= kWarpDecode0) return warp < kWarpDecode0 + 4 ? warp - kWarpDecode0 : 32 + warp - kWarpDecode0 - 4;
+  return warp >= kWarpSoft0 + 4 ? 32 + warp - kWarpSoft0 : -1;
+}
+constexpr int solo_warps(int from) {
+  int n = 0;
+  for (int w = 0; w < kThreads / 32; ++w) n += solo_task(w) >= from && solo_task(w) < from + 32;
+  return n;
+}
+constexpr bool solo_tasks_whole(int from) {                     // each of 0 .. n - 1 once: the barriers count them
+  for (int x = 0; x < solo_warps(from); ++x) {
+    int n = 0;
+    for (int w = 0; w < kThreads / 32; ++w) n += solo_task(w) == from + x;
+    if (n != 1) return false;
+  }
+  return true;
+}
+constexpr int kSoloKeys = solo_warps(0), kSoloValues = solo_warps(32);
+static_assert(solo_tasks_whole(0) && solo_tasks_whole(32));
+
 template <int D>
 struct Layout {
+  // One tile a unit, where two have no room: keys and values in one buffer each and q once, S in two.
+  static constexpr bool kSolo = D > 128;
+  static constexpr int kUnit = kSolo ? kTile : kRows, kBuffers = kSolo ? 1 : 2, kRawStages = kSolo ? 3 : 4;
   static constexpr int NBX = D / 64;
   static constexpr int kKeys = 2 * NBX * 8192;                  // hi boxes (64 tokens x 64 channels), then lo
   static constexpr int kValues = 2 * D * 128;                   // hi rows (D x 64 tokens), then lo
   static constexpr int kRaw = kSB * kv_block_bytes(D);
-  static constexpr int kValuesAt = 2 * kKeys, kRawAt = kValuesAt + 2 * kValues, kControlAt = kRawAt + kRawStages * kRaw;
+  static constexpr int kValuesAt = kBuffers * kKeys, kRawAt = kValuesAt + kBuffers * kValues, kControlAt = kRawAt + kRawStages * kRaw;
   // TMEM columns of a tile; p takes the place of S, 32 columns (32 tokens) at a time: 16 of p_hi, 16 of p_lo
-  static constexpr uint32_t kQ = 0, kS = D / 2, kO = kS + kTok, kCols = kTmemCols / 2;
-  static_assert(kO + D <= kCols, "TMEM budget");
+  static constexpr uint32_t kQ = 0, kS = D / 2, kO = kS + (kSolo ? 2 : 1) * kTok, kCols = kSolo ? 0 : kTmemCols / 2;
+  static_assert(kO + D <= (kSolo ? kTmemCols : kCols), "TMEM budget");
   static_assert(kControlAt % 128 == 0 && kValuesAt % 1024 == 0, "swizzled regions");
 };
 
 struct Control {
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t raw_full[4], raw_empty[4];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];  // of a tile
+  uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];  // of a tile; with one tile s_full and p_full of a buffer
   uint64_t drain;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
   volatile int odd_any[2];                          // the last step (from 1 on) with a value kept as NaN, by stage
-  volatile int odd[2][4][kTok];                     // that of a group's token
+  volatile int odd[2][8][kTok];                     // that of a group's token
   uint64_t half_full, half_empty;                   // a paired unit's second half
   struct {
     float ref, l;
@@ -209,10 +240,10 @@ struct Span {
   int64_t first, last;
   int rows;
 };
-template <class A>
+template <int R, class A>
 __device__ __forceinline__ Span span_of(const A& a, const Unit& u, int from, int most) {     // its rows from .. from + most - 1
   Span s;
-  const int64_t base = u.rq.L - u.rq.T, row0 = u.rg * kRows + from, left = u.rq.T * a.group - row0;
+  const int64_t base = u.rq.L - u.rq.T, row0 = u.rg * R + from, left = u.rq.T * a.group - row0;
   s.rows = static_cast<int>(left < most ? left : most);
   if (s.rows <= 0) return {0, -1, 0};
   const int64_t p0 = base + quot(row0, a.group), p1 = base + quot(row0 + s.rows - 1, a.group);
@@ -244,11 +275,11 @@ __device__ __forceinline__ Range range_of(const Walk& w, const Span& s) {
   const Range r = {lo > w.at ? static_cast<int>(lo < w.end ? lo : w.end) : w.at, hi < w.end ? static_cast<int>(hi > w.at ? hi : w.at) : w.end};
   return r;
 }
-template <class A>
+template <int R, class A>
 __device__ __forceinline__ void next_piece(const A& a, const Plan& pl, const Control& c, Walk& w, int steps) {
   w.at = w.end;
-  w.u = find_unit<kSB, kRows>(a, pl, c.begin + w.at);
-  w.s = span_of(a, w.u, 0, kRows);
+  w.u = find_unit<kSB, R>(a, pl, c.begin + w.at);
+  w.s = span_of<R>(a, w.u, 0, R);
   const int64_t end = w.u.start + w.u.n - c.begin;
   w.end = static_cast<int>(end < steps ? end : steps);
   w.step0 = w.u.first + (c.begin - w.u.start);
@@ -273,17 +304,18 @@ __device__ __forceinline__ void centred(uint32_t w, float2 (&c)[4]) {
 // Keys of 8 tokens (block b, half h) of a step: token row 16b + 8h + lane/4,
 // channels 32g + 8i .. of every group, into the hi and lo boxes.
 template <int D>
-__device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, int h, int64_t tok0, const Span& span) {
-  constexpr int NG = D / 32, NBX = D / 64;
+__device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, int h, int64_t tok0, const Span& span, int from = 0,
+                                            int to_g2 = D / 64) {
+  constexpr int NG = D / 32, NBX = D / 64, kHalf = NG < 4 ? NG : 4;       // codes lie by halves of 4 groups
   const int lane = threadIdx.x & 31, i = lane & 3, t = 8 * h + (lane >> 2), row = 16 * b + t;
-  const uint32_t blk = raw + b * kv_block_bytes(D), words = blk + (t * 4 + i) * (4 * NG), scales = blk + 16 * D + t * (2 * NG);
+  const uint32_t blk = raw + b * kv_block_bytes(D), words = blk + (t * 4 + i) * (4 * kHalf), scales = blk + 16 * D + t * (2 * NG);
   const bool seen = tok0 + row >= span.first && tok0 + row <= span.last;
   // chunk 4*(g & 1) + i of 16 bytes, swizzled by the row: group g + 1 flips bit 2
   const uint32_t at = keys + row * 128 + ((i ^ (row & 7)) << 4);
 #pragma unroll 1
-  for (int g2 = 0; g2 < NG / 2; ++g2) {
+  for (int g2 = from; g2 < to_g2; ++g2) {
     uint32_t w[2], sc[1], md[1];
-    lds_words<2>(w, words + 8 * g2);
+    lds_words<2>(w, words + (NG > 4 ? 8 * (g2 & 1) + 64 * kHalf * 4 * (g2 >> 1) : 8 * g2));
     lds_words<1>(sc, scales + 4 * g2);
     lds_words<1>(md, scales + D + 4 * g2);
     if (!seen) sc[0] = md[0] = 0;                               // it may hold anything
@@ -306,7 +338,7 @@ __device__ __forceinline__ void decode_keys(uint32_t raw, uint32_t keys, int b, 
 // lane/4 and d + 8, tokens 2i, 2i+1, 2i+8, 2i+9, into the hi and lo rows d.
 template <int D>
 __device__ __forceinline__ void decode_values(Control& c, int j, uint32_t raw, uint32_t values, int b, int quad, int64_t tok0,
-                                              const Span& span) {
+                                              const Span& span, int from = 0, int to_gg = 2) {
   constexpr int NG = D / 32;
   const int lane = threadIdx.x & 31, i = lane & 3, q = lane >> 2;
   const uint32_t blk = raw + b * kv_block_bytes(D);
@@ -314,7 +346,7 @@ __device__ __forceinline__ void decode_values(Control& c, int j, uint32_t raw, u
   // row d = 16 * tile + q (+ 8), chunks 2b and 2b + 1 of it, swizzled by q
   const uint32_t at = values + q * 128 + 4 * i, at0 = at + (((2 * b) ^ q) << 4), at1 = at + (((2 * b + 1) ^ q) << 4);
 #pragma unroll 1
-  for (int gg = 0; gg < 2; ++gg) {
+  for (int gg = from; gg < to_gg; ++gg) {
     const int g = 2 * quad + gg;
     uint32_t w[2], md[2][1], bits[4];
     lds_words<2>(w, blk + 8 * D + (quad * 32 + lane) * 16 + 8 * gg);
@@ -371,18 +403,20 @@ __device__ __forceinline__ void decode_values(Control& c, int j, uint32_t raw, u
 template <int D, typename Out, int SEE, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const AttnArgsOf<SEE> a) {
   using Y = Layout<D>;
-  constexpr int NG = D / 32;
+  constexpr int NG = D / 32, R = Y::kUnit, kRawStages = Y::kRawStages;
+  constexpr bool SOLO = Y::kSolo;
+  static_assert(!(SOLO && PAIR));
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   ControlOf<SEE>& c = *reinterpret_cast<ControlOf<SEE>*>(smem + Y::kControlAt);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int k = tid; k < 2 * 4 * kTok; k += kThreads) c.odd[0][0][k] = 0;
+  for (int k = tid; k < 2 * 8 * kTok; k += kThreads) c.odd[0][0][k] = 0;
   if (tid == 0) {
-    for (int s = 0; s < kRawStages; ++s) mbar_init(&c.raw_full[s], 1), mbar_init(&c.raw_empty[s], kDecodeWarps);
+    for (int s = 0; s < kRawStages; ++s) mbar_init(&c.raw_full[s], 1), mbar_init(&c.raw_empty[s], SOLO ? kSoloKeys + kSoloValues : kDecodeWarps);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&c.k_full[s], kDecodeWarps), mbar_init(&c.k_empty[s], 1);
-      mbar_init(&c.v_full[s], kDecodeWarps), mbar_init(&c.v_empty[s], 1);
+      mbar_init(&c.k_full[s], SOLO ? kSoloKeys : kDecodeWarps), mbar_init(&c.k_empty[s], 1);
+      mbar_init(&c.v_full[s], SOLO ? kSoloValues : kDecodeWarps), mbar_init(&c.v_empty[s], 1);
       mbar_init(&c.q_ready[s], 4), mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], 4), mbar_init(&c.o_full[s], 1);
       c.odd_any[s] = 0;
@@ -397,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   if (wait_now) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) a.joined[blockIdx.x].parts = 0;
-  const Plan pl = make_plan<kSB, kRows>(a, c.prefix, c.cost, nullptr, c.lower);
+  const Plan pl = make_plan<kSB, R>(a, c.prefix, c.cost, nullptr, c.lower);
   if (pl.total == 0 || blockIdx.x >= pl.ctas) {
     wait_first_pass(a);
     return;
   }
-  if (tid < 2) (tid ? c.end : c.begin) = bound<kSB, kRows>(a, pl, blockIdx.x + tid);
+  if (tid < 2) (tid ? c.end : c.begin) = bound<kSB, R>(a, pl, blockIdx.x + tid);
   __syncthreads();
   if (c.begin >= c.end) {
     wait_first_pass(a);
@@ -411,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   const int steps = static_cast<int>(c.end - c.begin);
   Walk w;                                                        // the first piece, in code that all warps share
   w.end = 0;
-  next_piece(a, pl, c, w, steps);
+  next_piece<R>(a, pl, c, w, steps);
   if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem_base)), "r"(kTmemCols)
                  : "memory");
@@ -427,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   if (warp == kWarpLoad) {
     // ---- blocks of the cache into the raw ring; lane k < 4 copies a step's block k ----
     bool ok = true;
-    for (; ok; next_piece(a, pl, c, w, steps)) {
+    for (; ok; next_piece<R>(a, pl, c, w, steps)) {
       for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int r = j % kRawStages;
         const uint8_t* src = nullptr;
@@ -455,8 +489,43 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     uint32_t begun = 0, pending = 0, open = 0;                       // a bit per tile: phases of q_ready and s_full; p v to come; S formed in this piece
     uint32_t turn = 0;
     bool ok = true;
-    for (; ok; next_piece(a, pl, c, w, steps)) {
-      const Range r0 = range_of(w, span_of(a, w.u, 0, kTile)), r1 = range_of(w, span_of(a, w.u, kTile, kTile));
+    if constexpr (SOLO) {
+      // S of a step, then p v of the step before, whose p lie in the other buffer
+      for (; ok; next_piece<R>(a, pl, c, w, steps)) {
+        for (int n = w.r.lo; n <= w.r.hi; ++n) {                     // and once more for the last p v
+          const uint32_t b = __shfl_sync(0xffffffffu, j & 1, 0);
+          if (n < w.r.hi) {
+            if (n == w.r.lo) {
+              if (!(ok = wait(c, &c.q_ready[0], begun, a.err))) break;
+              begun ^= 1;
+            }
+            if (!(ok = wait(c, &c.k_full[0], j & 1, a.err))) break;
+            tc_fence_after();
+            const uint64_t k = sw128_desc(base);
+#pragma unroll
+            for (int x = 0; x < 2 * Y::NBX; ++x)                     // boxes of 64 channels, those of hi, then of lo
+              mma64<idesc(kTok), 8, 16, 24>(tm + Y::kS + b * kTok, tm + Y::kQ + 32 * (x % Y::NBX), k + x * 512, x > 0);
+            commit(&c.s_full[b]);
+            commit(&c.k_empty[0]);
+          }
+          if (n > w.r.lo) {
+            if (!(ok = wait(c, &c.p_full[b ^ 1], ((j - 1) >> 1) & 1, a.err))) break;      // whose warps have waited for v_full
+            tc_fence_after();
+            const uint64_t v = sw128_desc(base + Y::kValuesAt);
+            const uint32_t p = tm + Y::kS + (b ^ 1) * kTok, o = tm + Y::kO;
+            mma64<idesc(D), 8, 32, 40>(o, p, v, n > w.r.lo + 1);     // p_hi v_hi
+            mma64<idesc(D), 8, 32, 40>(o, p + 16, v, 1);             // p_lo v_hi
+            mma64<idesc(D), 8, 32, 40>(o, p, v + D * 128 / 16, 1);   // p_hi v_lo
+            commit(&c.v_empty[0]);
+            if (n == w.r.hi) commit(&c.o_full[0]);
+          }
+          if (n < w.r.hi) ++j;
+        }
+        if (w.end >= steps) break;
+      }
+    } else
+    for (; ok; next_piece<R>(a, pl, c, w, steps)) {
+      const Range r0 = range_of(w, span_of<R>(a, w.u, 0, kTile)), r1 = range_of(w, span_of<R>(a, w.u, kTile, kTile));
       const bool pair = PAIR && w.s.rows <= kTile;
       uint32_t fresh = 0;                                            // nothing in O yet
       for (int n = w.r.lo; n <= w.r.hi && ok; ++n) {                 // and once more for the last p v
@@ -506,6 +575,37 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     }
     commit(&c.drain);                                                // every product issued so far has completed
     mbar_wait_bounded(&c.drain, 0, 100000000ull);
+  } else if (SOLO && (warp >= kWarpSoft0 + 4 || warp < kWarpSoft0)) {
+    // ---- one tile: some warps for keys, the others, the second tile's softmax warps among them, for values, so that
+    // a step's values need not wait for the next one's keys ----
+    if (warp >= kWarpSoft0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+    const int task = solo_task(warp), d = task & 31;
+    const bool keys = task < 32;
+    uint64_t *empty = keys ? &c.k_empty[0] : &c.v_empty[0], *full = keys ? &c.k_full[0] : &c.v_full[0];
+    bool ok = task >= 0;
+    for (; ok; next_piece<R>(a, pl, c, w, steps)) {
+      for (int n = w.r.lo; n < w.r.hi; ++n) {
+        const int r = j % kRawStages;
+        const int64_t t0 = (w.step0 + n) * kTok;
+        const uint32_t raw = base + Y::kRawAt + r * Y::kRaw;
+        if (!(ok = wait(c, &c.raw_full[r], (j / kRawStages) & 1, a.err) && wait(c, empty, (j & 1) ^ 1, a.err))) break;
+        if (keys) {                                                  // a 16-token block's half and 64 channels at a time
+#pragma unroll 1
+          for (int x = d; x < kSB * 2 * (D / 64); x += kSoloKeys) decode_keys<D>(raw, base, x / (2 * (D / 64)), x / (D / 64) & 1, t0, w.s, x % (D / 64), x % (D / 64) + 1);
+        } else {                                                     // a block and 32 channels at a time
+#pragma unroll 1
+          for (int x = d; x < kSB * NG; x += kSoloValues) decode_values<D>(c, j, raw, base + Y::kValuesAt, x / NG, x / 2 % (D / 64), t0, w.s, x & 1, (x & 1) + 1);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          arrive(full);
+          arrive(&c.raw_empty[r]);
+        }
+        ++j;
+      }
+      if (w.end >= steps) break;
+    }
   } else if (warp >= kWarpDecode0 || (!PAIR && (warp == 2 || warp == 3))) {
     if (warp >= kWarpDecode0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     // On the three schedulers that do not issue the products (warps 13 and 17 would be on theirs and have
@@ -515,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
     // ---- codes to bf16 pairs: warp d decodes keys of block d/2, half d%2, and values of its channels 64*(d%2) .. ----
     const int blk = d >> 1, half = d & 1;
     bool ok = PAIR || (warp != 13 && warp != 17);
-    for (; ok; next_piece(a, pl, c, w, steps)) {
+    for (; ok; next_piece<R>(a, pl, c, w, steps)) {
       for (int n = w.r.lo; n < w.r.hi; ++n) {
         const int b = j & 1, r = j % kRawStages;
         const int64_t t0 = (w.step0 + n) * kTok;
@@ -540,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
   } else if (warp >= kWarpSoft0) {
     // ---- softmax, four warps a tile: a thread is a row ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int t = (warp - kWarpSoft0) >> 2, row = kTile * t + 32 * (warp & 3) + lane;
+    const int t = SOLO ? 0 : (warp - kWarpSoft0) >> 2, row = kTile * t + 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + t * Y::kCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     int turn = 0;                                                    // steps of the tile
     int piece = 0, pairs = 0;                                        // with products, paired
     const float none = -__int_as_float(0x7f800000), c2 = a.scale_log2;
     bool ok = true;
-    for (; ok; next_piece(a, pl, c, w, steps)) {
-      const int64_t x0 = c.begin + w.at, row0 = w.u.rg * kRows, left = w.u.rq.T * a.group - row0;
+    for (; ok; next_piece<R>(a, pl, c, w, steps)) {
+      const int64_t x0 = c.begin + w.at, row0 = w.u.rg * R, left = w.u.rq.T * a.group - row0;
       const bool pair = PAIR && w.s.rows <= kTile;
       const int mine = pair ? row & (kTile - 1) : row;
       const bool have = mine < w.s.rows && !(pair && t == 1);        // those that have none take the last, and keep nothing of it
@@ -557,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       const int64_t lo = SEE == kOwn ? w.u.rq.low - 1 : SEE == kCausal && a.window > 0 && pos - a.window > -1 ? pos - a.window : -1;
       // the positions that all rows of the warp see; later rows see from and to later ones
       const int64_t all_lo = __shfl_sync(0xffffffffu, lo, 31), all_hi = __shfl_sync(0xffffffffu, hi, 0);
-      Range own = range_of(w, span_of(a, w.u, kTile * t, kTile));
+      Range own = range_of(w, span_of<R>(a, w.u, kTile * t, kTile));
       const int stride = pair ? 2 : 1, j0 = j;
       if (pair) own = {w.r.lo + ((w.r.lo & 1) ^ t), w.r.hi};
       // the query row into TMEM (bf16 pairs, a column each); the piece before has no products left that read it
@@ -594,19 +694,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         // without a wait, and parity tells v_full's phases apart only one step of a buffer
         // away.  S of this step means that all decoding warps have posted the values of
         // the steps before, so that the phase awaited is the current one or the last.
-        if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err) && wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
-        if (c.odd_any[b] == j + 1) {
-          for (int g = 0; g < NG; ++g)
-            for (int k = from; k < to; ++k)
-              if (c.odd[b][g][k] == j + 1) odd |= 1u << g;
+        auto look_odd = [&] {
+          if (c.odd_any[b] == j + 1) {
+            for (int g = 0; g < NG; ++g)
+              for (int k = from; k < to; ++k)
+                if (c.odd[b][g][k] == j + 1) odd |= 1u << g;
+          }
+          __syncwarp();
+        };
+        if constexpr (SOLO) {
+          if (!(ok = wait(c, &c.s_full[b], (j >> 1) & 1, a.err))) break;         // the values are decoded meanwhile
+        } else {
+          if (!(ok = wait(c, &c.s_full[t], turn++ & 1, a.err) && wait(c, &c.v_full[b], (j >> 1) & 1, a.err))) break;
+          look_odd();
         }
-        __syncwarp();
+        const uint32_t s_at = lanes + Y::kS + (SOLO ? b * kTok : 0);
         tc_fence_after();
         // the row's 64 logits stay in registers between maximum and weights: read again
         // for the second pass they cost 64.5 us instead of 62
         uint32_t x[2][32];
-        tmem_load(lanes + Y::kS, x[0]);
-        tmem_load(lanes + Y::kS + 32, x[1]);
+        tmem_load(s_at, x[0]);
+        tmem_load(s_at + 32, x[1]);
         tmem_wait_load(x[0]);
         tmem_wait_load(x[1]);
         float top = none, mul = c2;
@@ -634,6 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
           const float now = move ? top : ref, f = ex2(ref - now);
           ref = now;
           l *= f;
+          if constexpr (SOLO) {                                      // p v of the step before may be under way
+            if (begun && !(ok = wait(c, &c.v_empty[0], (j - 1) & 1, a.err))) break;
+            tc_fence_after();
+          }
           if (begun) {                                               // O: the products before S are in it
 #pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {
@@ -657,13 +769,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
             split(y, p_hi[k], p_lo[k]);
           }
           l += sum.x + sum.y;
-          tmem_store16(lanes + Y::kS + 32 * h, p_hi);
-          tmem_store16(lanes + Y::kS + 32 * h + 16, p_lo);
+          tmem_store16(s_at + 32 * h, p_hi);
+          tmem_store16(s_at + 32 * h + 16, p_lo);
         }
         tmem_wait_store();
+        if constexpr (SOLO) {
+          if (!(ok = wait(c, &c.v_full[0], j & 1, a.err))) break;
+          look_odd();
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive(&c.p_full[t]);
+        if (lane == 0) arrive(&c.p_full[SOLO ? b : t]);
         begun = true;
       }
       if (!ok) break;
@@ -690,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       }
       // O to the output, or as a part to the workspace
       const bool whole = x0 == w.u.start && w.end == w.u.start + w.u.n - c.begin, first = w.u.start >= c.begin;
-      float* part = a.partial + static_cast<int64_t>(2 * blockIdx.x + (first ? 1 : 0)) * kRows * (D + 2);
+      float* part = a.partial + static_cast<int64_t>(2 * blockIdx.x + (first ? 1 : 0)) * R * (D + 2);
       const int64_t at = (w.u.rq.q0 + tq) * a.heads + head;
       bool split = false;
       if constexpr (SEE == kOwn) split = w.u.rq.low > 0;
@@ -754,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         } else if (have) {
 #pragma unroll
           for (int k = 0; k < 32; k += 4)                             // [D / 4][row][4]: a warp's rows side by side
-            *reinterpret_cast<uint4*>(part + ((8 * h + k / 4) * kRows + row) * 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            *reinterpret_cast<uint4*>(part + ((8 * h + k / 4) * R + row) * 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
       tc_fence_before();
@@ -763,11 +879,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (lane == 0) arrive(&c.half_empty);
         ++pairs;
       }
-      if (have && !whole) *(reinterpret_cast<float2*>(part + kRows * D) + row) = make_float2(ref, l);
+      if (have && !whole) *(reinterpret_cast<float2*>(part + R * D) + row) = make_float2(ref, l);
       if (!whole && first && row == 0) {
         // this CTA has the unit's first part: the others are those of the next CTAs up to the unit's end
-        const int c1 = share_of(pl, w.u.cost + kUnitCost + w.u.n - cut_steps<kRows>);
-        a.joined[blockIdx.x] = {w.u.rq.q0, w.u.rg * kRows, w.u.h, w.s.rows, c1 - static_cast<int>(blockIdx.x) + 1, split};
+        const int c1 = share_of(pl, w.u.cost + kUnitCost + w.u.n - cut_steps<R>);
+        a.joined[blockIdx.x] = {w.u.rq.q0, w.u.rg * R, w.u.h, w.s.rows, c1 - static_cast<int>(blockIdx.x) + 1, split};
       }
       if (w.end >= steps) break;
     }
@@ -786,11 +902,11 @@ constexpr int kJoinWarps = 8;
 
 template <int D, typename Out, int SEE>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgsOf<SEE> a) {
-  constexpr int kBatch = 10;
-  constexpr int64_t kPitch = kRows * (D + 2);
+  constexpr int kBatch = 10, R = Layout<D>::kUnit;
+  constexpr int64_t kPitch = R * (D + 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Joined u = a.joined[blockIdx.x];
-  const int slot = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), r = slot % (kRows / 32) * 32 + (threadIdx.x & 31), c4 = slot / (kRows / 32);
+  const int slot = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), r = slot % (R / 32) * 32 + (threadIdx.x & 31), c4 = slot / (R / 32);
   if (u.parts == 0 || r >= u.rows) return;
   auto part = [&](int c) { return a.partial + (2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * kPitch; };
   float m = kRefNone, l = 0.f;
@@ -802,8 +918,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const float* from = part(c + k < u.parts ? c + k : c);
-      ml[k] = __ldcg(reinterpret_cast<const float2*>(from + kRows * D) + r);
-      v[k] = __ldcg(reinterpret_cast<const float4*>(from) + c4 * kRows + r);
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(from + R * D) + r);
+      v[k] = __ldcg(reinterpret_cast<const float4*>(from) + c4 * R + r);
     }
     float top = m;
 #pragma unroll
@@ -853,7 +969,7 @@ cudaError_t launch_block_variant(const AttnArgsOf<SEE>& a, int grid, cudaStream_
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attention_block_kernel<D, Out, SEE, PAIR>, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 32 * (D / 4) / kJoinWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), Layout<D>::kUnit / 32 * (D / 4) / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, Out, SEE>, a);
@@ -874,6 +990,10 @@ cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int64_t coun
   switch (D) {
     Q4NX_BLOCK(64)
     Q4NX_BLOCK(128)
+    case 256:
+      if constexpr (SEE != kCausal)
+        return out_f32 ? launch_block_variant<256, float, SEE, false>(a, grid, s) : launch_block_variant<256, uint16_t, SEE, false>(a, grid, s);
+      return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
   }
 #undef Q4NX_BLOCK

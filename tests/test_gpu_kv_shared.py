@@ -95,7 +95,7 @@ def test_shared_matches(q, name, kv, group, page, dim):  # noqa: F811
     q.q4nx_check(device=DEV)
 
 
-@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dim", [64, 128, 256])
 def test_shared_many_rows_and_units(q, dim):  # noqa: F811
     # more than 256 rows a group, several units and kv heads, a prefix cut between CTAs
     c = Shared(q, [(2500, [(1 + 29 * i, 1 + i % 3) for i in range(40)]), (1, [(30, 1)])], 4, dim, 256, hidden=False).fill().append_new()
@@ -122,14 +122,15 @@ def test_shared_out_lse_and_rows_of_no_request(q):  # noqa: F811
     assert torch.equal(q.q4nx_kv_attention_shared(c.cache, qt, c.start, c.tlens, c.table, c.first, c.shared)[:-3], out[:-3])
 
 
-def test_shared_nan_stays_in_its_group(q):  # noqa: F811
+@pytest.mark.parametrize("dim", [128, 256])
+def test_shared_nan_stays_in_its_group(q, dim):  # noqa: F811
     for name in ("decode", "crowd"):
-        c = Shared(q, GROUPS[name], 2, 128, 16)
+        c = Shared(q, GROUPS[name], 2, dim, 16)
         c.k[0][5, 1, 3] = np.nan
         c.v[0][9, 0, 40] = np.nan
         c.fill().append_new()
         _, out, _ = run(c, 4)
-        bad = torch.isnan(out.view(c.tokens, 2, 2, 128))
+        bad = torch.isnan(out.view(c.tokens, 2, 2, dim))
         rows = int(c.start[int(c.first[1])])
         assert bad[:rows, 1].all() and bad[:rows, 0, :, 32:64].all() and not bad[:rows, 0, :, :32].any() and not bad[:rows, 0, :, 64:].any()
         assert not bad[rows:].any()
@@ -241,18 +242,20 @@ def test_cross_matches(q, T, kv, group, page, dim):  # noqa: F811
     q.q4nx_check(device=DEV)
 
 
-def test_cross_long_and_rows_of_no_request(q):  # noqa: F811
-    c = Case(q, [20000, 3], [20000, 3], 1, 128, 256).append_new()
+@pytest.mark.parametrize("dim", [128, 256])
+def test_cross_long_and_rows_of_no_request(q, dim):  # noqa: F811
+    c = Case(q, [20000, 3], [20000, 3], 1, dim, 256).append_new()
     for T in ([1, 1], [80, 70]):
         qx, out, lse = cross(c, T, 4, extra=2)
-        check(c, out, lse, *exact_cross(c, T, qx[:-2], 128 ** -0.5, 4))
+        check(c, out, lse, *exact_cross(c, T, qx[:-2], dim ** -0.5, 4))
         assert torch.all(lse[-2:] == 7)
 
 
-def test_cross_nan_and_what_lies_behind_the_length(q):  # noqa: F811
+@pytest.mark.parametrize("dim", [128, 256])
+def test_cross_nan_and_what_lies_behind_the_length(q, dim):  # noqa: F811
     # the block in which a cache ends holds NaN behind it (the pool's fill); a NaN key of one request stays there
     for T in ([1, 2], [66, 100]):
-        c = Case(q, [5, 40], [5, 40], 2, 128, 16)
+        c = Case(q, [5, 40], [5, 40], 2, dim, 16)
         c.k[1][39, 0, 0] = np.nan
         c.append_new()
         _, out, _ = cross(c, T, 2)
