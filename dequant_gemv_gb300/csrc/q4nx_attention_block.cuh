@@ -897,58 +897,84 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
 }
 
 // The parts of units cut between CTAs: a thread per row and four channels, lanes
-// along the rows, as the parts lie.
-constexpr int kJoinWarps = 8;
+// along the rows, as the parts lie.  One wave of CTAs goes through the slots (8 warps' work) of the units that were
+// cut, which each of them lists first: a CTA for every slot of every first CTA, most of them with nothing
+// to do, took 3 us more (64 tokens over 16384 positions 52 -> 49, 48 requests behind 8191 59 -> 56).
+constexpr int kJoinWarps = 8, kJoinPerSm = 3;
+static_assert(kKvMaxCtas / 2 <= kJoinWarps * 32);
 
 template <int D, typename Out, int SEE>
-__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnArgsOf<SEE> a) {
-  constexpr int kBatch = 10, R = Layout<D>::kUnit;
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) attention_join_kernel(const AttnArgsOf<SEE> a, int ctas) {
+  constexpr int kBatch = 10, R = Layout<D>::kUnit, kSlots = R / 32 * (D / 4) / kJoinWarps;
   constexpr int64_t kPitch = R * (D + 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Joined u = a.joined[blockIdx.x];
-  const int slot = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), r = slot % (R / 32) * 32 + (threadIdx.x & 31), c4 = slot / (R / 32);
-  if (u.parts == 0 || r >= u.rows) return;
-  auto part = [&](int c) { return a.partial + (2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * kPitch; };
-  float m = kRefNone, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-  for (int c = 0; c < u.parts; c += kBatch) {
-    float2 ml[kBatch];
-    float4 v[kBatch];
+  __shared__ Joined cut[kKvMaxCtas / 2];
+  __shared__ int first[kKvMaxCtas / 2], found[kJoinWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int units = 0;
+  {
+    Joined u;
+    u.parts = 0;
+    if (tid < ctas) u = a.joined[tid];
+    const uint32_t has = __ballot_sync(0xffffffffu, u.parts != 0);
+    if (lane == 0) found[warp] = __popc(has);
+    __syncthreads();
+    int at = __popc(has & ((1u << lane) - 1));
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const float* from = part(c + k < u.parts ? c + k : c);
-      ml[k] = __ldcg(reinterpret_cast<const float2*>(from + R * D) + r);
-      v[k] = __ldcg(reinterpret_cast<const float4*>(from) + c4 * R + r);
+    for (int k = 0; k < kJoinWarps; ++k) {
+      if (k < warp) at += found[k];
+      units += found[k];
     }
-    float top = m;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);           // a part taken twice changes no maximum
-    const float f0 = ex2(m - top);
-    m = top, l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (c + k < u.parts) {
-        const float f = ex2(ml[k].x - m);
-        l = fmaf(f, ml[k].y, l);
-        o.x = fmaf(f, v[k].x, o.x), o.y = fmaf(f, v[k].y, o.y), o.z = fmaf(f, v[k].z, o.z), o.w = fmaf(f, v[k].w, o.w);
-      }
+    if (u.parts != 0) cut[at] = u, first[at] = tid;
+    __syncthreads();
   }
-  const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
-  const RowScale sc = row_scale(a, u.split, at, m, l, c4 == 0);
-  const float inv = sc.own;
-  if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if constexpr (SEE != kCausal)
-    if (u.split) {
-      const float sums[4] = {o.x, o.y, o.z, o.w};
-      put_row<Out, 4>(a, true, sc, [&](int k) { return at * D + 4 * c4 + k; }, [&](int k) { return sums[k]; });
-      return;
+#pragma unroll 1
+  for (int item = blockIdx.x; item < units * kSlots; item += gridDim.x) {
+    const Joined u = cut[item / kSlots];
+    const int cta = first[item / kSlots], slot = item % kSlots * kJoinWarps + warp, r = slot % (R / 32) * 32 + lane, c4 = slot / (R / 32);
+    if (r >= u.rows) continue;
+    auto part = [&](int c) { return a.partial + (2 * (cta + c) + (c == 0 ? 1 : 0)) * kPitch; };
+    float m = kRefNone, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c = 0; c < u.parts; c += kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float* from = part(c + k < u.parts ? c + k : c);
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(from + R * D) + r);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(from) + c4 * R + r);
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);           // a part taken twice changes no maximum
+      const float f0 = ex2(m - top);
+      m = top, l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (c + k < u.parts) {
+          const float f = ex2(ml[k].x - m);
+          l = fmaf(f, ml[k].y, l);
+          o.x = fmaf(f, v[k].x, o.x), o.y = fmaf(f, v[k].y, o.y), o.z = fmaf(f, v[k].z, o.z), o.w = fmaf(f, v[k].w, o.w);
+        }
     }
-  if constexpr (sizeof(Out) == 4)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + 4 * c4) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * c4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
+    const RowScale sc = row_scale(a, u.split, at, m, l, c4 == 0);
+    const float inv = sc.own;
+    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (SEE != kCausal)
+      if (u.split) {
+        const float sums[4] = {o.x, o.y, o.z, o.w};
+        put_row<Out, 4>(a, true, sc, [&](int k) { return at * D + 4 * c4 + k; }, [&](int k) { return sums[k]; });
+        continue;
+      }
+    if constexpr (sizeof(Out) == 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + 4 * c4) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * c4) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
 }
 
 template <int D, typename Out, int SEE, bool PAIR>
@@ -969,10 +995,10 @@ cudaError_t launch_block_variant(const AttnArgsOf<SEE>& a, int grid, cudaStream_
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attention_block_kernel<D, Out, SEE, PAIR>, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), Layout<D>::kUnit / 32 * (D / 4) / kJoinWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>(kJoinPerSm * grid));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, Out, SEE>, a);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, Out, SEE>, a, grid);
 }
 
 }  // namespace
