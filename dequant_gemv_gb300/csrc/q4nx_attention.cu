@@ -16,9 +16,9 @@
 // for it only then, so that the second plan, look-ups and first copies cost no time of their own.
 //
 // Shared (against a floor by bytes): 48 requests behind 8191 positions, 32 query
-// heads, 8 kv heads of 128: 61 us (4.7); cold and alone the requests' own 60 to 600 tokens take 24, the prefix on the
-// tensor cores 34 and its join 15; 16 requests behind 65537: 133 (14); 12 requests x 4 tokens, two groups behind 16001
-// positions, 4 kv heads of 256: 83 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
+// heads, 8 kv heads of 128: 57 us (4.7); cold and alone the requests' own 60 to 600 tokens take 24 and the prefix on the
+// tensor cores 34; 16 requests behind 65537: 133 (14); 12 requests x 4 tokens, two groups behind 16001
+// positions, 4 kv heads of 256: 82 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
 // plans, look-ups and joins.  Cross: 32 requests of 410 to 4097 positions: 37 us, 2.6 TB/s, as the kernel for few rows does.
 #include "q4nx_attention_rows.cuh"
 
