@@ -340,7 +340,8 @@ int q4nx_kv_attention(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, co
 /* Attention to all positions of another sequence's cache (an encoder's states): as
  * q4nx_kv_attention, except that every token of request b sees all of its lens[b] cached
  * positions.  lens says nothing of the call's own tokens, and their number may be larger or
- * smaller.  A request whose cache is empty gives zeros and -Inf. */
+ * smaller.  A request whose cache is empty gives zeros and -Inf.  Beyond 64 query rows per
+ * request the bf16 pairs' accuracy applies at 256 channels too. */
 int q4nx_kv_attention_cross(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const void* q_dev, int64_t q_stride,
                             int heads, float scale, void* out_dev, int out_dtype, float* lse_dev, void* workspace_dev,
                             uint64_t workspace_bytes, void* stream);
@@ -364,7 +365,7 @@ typedef struct q4nx_kv_groups {
  * Every token of the call has to lie behind what its request shares (lens - T >= shared):
  * requests of which that is not true, like groups out of order or lengths beyond the
  * table, are skipped and reported as Q4NX_E_INDEX.  Which rounding applies (fp16 weights or
- * bf16 pairs) goes by the rows of a group for what it shares and by those of a request for its own.
+ * bf16 pairs, at 256 channels too) goes by the rows of a group for what it shares and by those of a request for its own.
  * scratch_dev: q4nx_kv_attention_shared_scratch(cache, tokens, heads) bytes, 16-byte
  * aligned, any content, free again after the call's work on the stream. */
 int q4nx_kv_attention_shared(const q4nx_kv_cache* cache, const q4nx_kv_batch* batch, const q4nx_kv_groups* groups,
