@@ -32,9 +32,9 @@ namespace {
 // up to 128 rows, the other one a pass for each 16: one request of 16384 tokens, 8 kv
 // heads of 128 channels: 64 rows 47 (there) and 49 us (tensor cores), 68 rows 53 and 49,
 // 256 rows 115 and 57; 16 requests of 4096: 64 rows 119 and 137, 68 rows 143 and
-// 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125.  Where every
+// 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125 (with a join that took 3 us more).  Where every
 // row sees everything (cross attention, prefixes) much the same, its two tiles sharing what few rows there
-// are: one request of 65536, 64 rows 110 and 111, 128 rows 193 and 113; 64 channels: 78 and 87, 143 and 88.
+// are: one request of 65536, 64 rows 104 and 108, 128 rows 193 and 110; 64 channels: 78 and 87, 143 and 87.
 // 256 channels, 4 kv heads, there alone: one request of 16384, 64 rows 53 and 53, 96 rows 62 and 55, 256 rows 119 and 79;
 // 16 of 2048: 76 and 86, 101 and 91, 222 and 168.  (Attention up to a row's own position stays with the other
 // kernel at 256 channels, whose numbers are its documented ones.)

@@ -141,10 +141,10 @@ BAD = [("shared", 0, -1), ("shared", 0, 10 ** 6), ("shared", 0, 39), ("first", 0
 
 
 @pytest.mark.parametrize("name,at,x", BAD)
-@pytest.mark.parametrize("count", [1, 24])
-def test_shared_reports_what_is_out_of_range(q, name, at, x, count):  # noqa: F811
+@pytest.mark.parametrize("count,dim", [(1, 64), (24, 64), (24, 256)])
+def test_shared_reports_what_is_out_of_range(q, name, at, x, count, dim):  # noqa: F811
     """Two groups of two requests (24: of many rows): reported, and nothing else is disturbed."""
-    c = Shared(q, [(37, [(2, 1), (20, 1)] * count), (50, [(1, 1), (4, 1)])], 2, 64, 16).fill().append_new()
+    c = Shared(q, [(37, [(2, 1), (20, 1)] * count), (50, [(1, 1), (4, 1)])], 2, dim, 16).fill().append_new()
     qx, good, _ = run(c, 8)
     ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
     t = dict(shared=c.shared.clone(), first=c.first.clone(), table=c.table, lens=c.tlens, start=c.start)
@@ -164,10 +164,10 @@ def test_shared_reports_what_is_out_of_range(q, name, at, x, count):  # noqa: F8
     q.q4nx_check(ws)
 
 
-@pytest.mark.parametrize("name", ["decode", "crowd", "prompts"])
-def test_shared_captured_on_other_streams_and_workspaces(q, name):  # noqa: F811
+@pytest.mark.parametrize("name,dim", [("decode", 128), ("crowd", 128), ("prompts", 128), ("crowd", 256), ("prompts", 256)])
+def test_shared_captured_on_other_streams_and_workspaces(q, name, dim):  # noqa: F811
     """Two captured graphs of two streams, replayed at once: their workspaces and scratch are their own."""
-    cases = [Shared(q, GROUPS[name], 2, 128, 16, seed=s).fill().append_new() for s in (1, 2)]
+    cases = [Shared(q, GROUPS[name], 2, dim, 16, seed=s).fill().append_new() for s in (1, 2)]
     qs = [c.draw(c.tokens, 8) for c in cases]
     want = [run(c, 8, qx=x)[1].clone() for c, x in zip(cases, qs)]
     graphs, outs = [], []
@@ -262,11 +262,11 @@ def test_cross_nan_and_what_lies_behind_the_length(q, dim):  # noqa: F811
         assert torch.isfinite(out[:T[0]]).all() and torch.isnan(out[T[0]:, 0]).all() and torch.isfinite(out[T[0]:, 1]).all()
 
 
-@pytest.mark.parametrize("T", [[1, 1], [90, 70]])
+@pytest.mark.parametrize("T,dim", [([1, 1], 64), ([90, 70], 64), ([90, 70], 256)])
 @pytest.mark.parametrize("name,at,x", [("table", (0, 1), 10 ** 6), ("table", (1, 0), -1), ("lens", 0, -3), ("lens", 1, 10 ** 6), ("start", 1, 10 ** 6),
                                        ("start", 2, 0)])
-def test_cross_reports_what_is_out_of_range(q, T, name, at, x):  # noqa: F811
-    c = Case(q, [40, 33], [40, 33], 2, 64, 16).append_new()
+def test_cross_reports_what_is_out_of_range(q, T, dim, name, at, x):  # noqa: F811
+    c = Case(q, [40, 33], [40, 33], 2, dim, 16).append_new()
     ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
     t = dict(start=ints(np.concatenate([[0], np.cumsum(T)])), lens=c.tlens.clone(), table=c.table.clone())
     qt = dev(c.draw(sum(T), 4))
