@@ -18,7 +18,7 @@
 // Shared (against a floor by bytes): 48 requests behind 8191 positions, 32 query
 // heads, 8 kv heads of 128: 57 us (4.7); cold and alone the requests' own 60 to 600 tokens take 24 and the prefix on the
 // tensor cores 34; 16 requests behind 65537: 133 (14); 12 requests x 4 tokens, two groups behind 16001
-// positions, 4 kv heads of 256: 82 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
+// positions, 4 kv heads of 256: 80 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
 // plans, look-ups and joins.  Cross: 32 requests of 410 to 4097 positions: 37 us, 2.6 TB/s, as the kernel for few rows does.
 #include "q4nx_attention_rows.cuh"
 
@@ -35,8 +35,8 @@ namespace {
 // 139, 256 rows 401 and 172; 64 channels: 88 and 109, 104 and 109, 285 and 125 (with a join that took 3 us more).  Where every
 // row sees everything (cross attention, prefixes) much the same, its two tiles sharing what few rows there
 // are: one request of 65536, 64 rows 104 and 108, 128 rows 193 and 110; 64 channels: 78 and 87, 143 and 87.
-// 256 channels, 4 kv heads, there alone: one request of 16384, 64 rows 53 and 53, 96 rows 62 and 55, 256 rows 119 and 79;
-// 16 of 2048: 76 and 86, 101 and 91, 222 and 168.  (Attention up to a row's own position stays with the other
+// 256 channels, 4 kv heads, there alone: one request of 16384, 64 rows 53 and 53, 96 rows 62 and 51, 256 rows 119 and 83;
+// 16 of 2048: 96 rows 101 and 101, 128 rows 125 and 105, 256 rows 222 and 171.  (Attention up to a row's own position stays with the other
 // kernel at 256 channels, whose numbers are its documented ones.)
 constexpr int kManyRows = 65;
 
@@ -48,10 +48,14 @@ constexpr uint64_t kPassBytes = kKvMaxCtas * 4 + kKvMaxCtas * sizeof(Joined);
 constexpr uint64_t kPassesAt = 16, kPartsAt = kPassesAt + 2 * kPassBytes;
 static_assert(kKvMaxCtas * 4 % 16 == 0 && kPassBytes % 16 == 0 && kPartsAt % 16 == 0);
 
+// At 256 channels the workspace has the former alone, and the tensor-core kernel as many CTAs as have their
+// parts in it (94 of 152), or, for shared prefixes, the whole in the caller's scratch.
+uint64_t few_bytes(int D) { return static_cast<uint64_t>(kKvMaxCtas) * 8 * (2 * (D + 2) + kWarps * D) * 4; }
 uint64_t parts_bytes(int D) {
-  const uint64_t few = static_cast<uint64_t>(kKvMaxCtas) * 8 * (2 * (D + 2) + kWarps * D) * 4, many = attention_block_bytes(D);
+  const uint64_t few = few_bytes(D), many = D > 128 ? 0 : attention_block_bytes(D);
   return few > many ? few : many;
 }
+uint64_t scratch_parts_bytes(int D) { return D > 128 ? 2 * attention_block_bytes(D) : parts_bytes(D); }
 
 void fill(AttnArgs& a, int D, const KvPool& pool, const KvBatch& kb, const void* q, int64_t q_stride, int heads, float scale, void* out,
           float* lse, void* workspace, int pass, void* parts) {
@@ -78,10 +82,18 @@ void fill(AttnArgs& a, int D, const KvPool& pool, const KvBatch& kb, const void*
 template <int SEE>
 bool many_rows(int D, int64_t rows, int64_t count) { return (D <= 128 || SEE != kCausal) && rows >= kManyRows * count; }
 
+// The CTAs whose parts (two each) have a place.
+template <int SEE>
+int most_block_ctas(int D, const AttnArgsOf<SEE>& a) {
+  if constexpr (SEE != kCausal)
+    if (D > 128 && a.pass == 0) return static_cast<int>(parts_bytes(D) / (attention_block_bytes(D) / (kKvMaxCtas / 2)));
+  return kKvMaxCtas / 2;
+}
+
 template <int SEE>
 cudaError_t launch_pass(int D, const AttnArgsOf<SEE>& a, int64_t count, int out_f32, const DeviceInfo& info, cudaStream_t s) {
   const int64_t rows = a.kb.tokens * a.group;
-  if (many_rows<SEE>(D, rows, count)) return launch_attention_block<SEE>(D, a, count, out_f32, info, s);
+  if (many_rows<SEE>(D, rows, count)) return launch_attention_block<SEE>(D, a, count, most_block_ctas<SEE>(D, a), out_f32, info, s);
   return launch_attention_rows<SEE>(D, rows > 8 * count, a, out_f32, info, s);
 }
 
@@ -91,7 +103,7 @@ uint64_t attention_workspace_bytes(int D) { return kPartsAt + parts_bytes(D); }
 
 uint64_t attention_shared_scratch(int D, int64_t tokens, int heads) {
   const uint64_t rows = static_cast<uint64_t>(tokens) * static_cast<uint64_t>(heads);
-  return parts_bytes(D) + rows * static_cast<uint64_t>(D) * 4 + rows * 8;
+  return scratch_parts_bytes(D) + rows * static_cast<uint64_t>(D) * 4 + rows * 8;
 }
 
 cudaError_t launch_attention(int D, const KvPool& pool, const KvBatch& kb, const void* q, int64_t q_stride, int heads,
@@ -117,12 +129,13 @@ cudaError_t launch_attention_shared(int D, const KvPool& pool, const KvBatch& kb
                                     cudaStream_t s) {
   AttnArgsOf<kAll> a;
   AttnArgsOf<kOwn> b;
-  fill(a, D, pool, kb, q, q_stride, heads, scale, out, lse, workspace, 0, static_cast<uint8_t*>(workspace) + kPartsAt);
+  void* other = static_cast<uint8_t*>(D > 128 ? scratch : workspace) + (D > 128 ? attention_block_bytes(D) : kPartsAt);
+  fill(a, D, pool, kb, q, q_stride, heads, scale, out, lse, workspace, 0, other);
   fill(b, D, pool, kb, q, q_stride, heads, scale, out, lse, workspace, 1, scratch);
   a.first = b.first = first;
   a.shared = b.shared = shared;
   a.groups = b.groups = groups;
-  a.part_o = b.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + parts_bytes(D));
+  a.part_o = b.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + scratch_parts_bytes(D));
   a.part_ml = b.part_ml = reinterpret_cast<float2*>(a.part_o + kb.tokens * heads * D);
   // The tensor-core kernel has a second launch that joins its parts: it comes last, so
   // that nothing starts behind that launch.  Otherwise the prefixes, which are the larger part, come first

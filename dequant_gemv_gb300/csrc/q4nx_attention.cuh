@@ -397,11 +397,11 @@ cudaError_t launch_attention_rows(int D, bool two, const AttnArgsOf<SEE>& a, int
 // size of the parts, and the launch.
 uint64_t attention_block_bytes(int D);
 template <int SEE>
-cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int64_t count, int out_f32, const DeviceInfo& info, cudaStream_t s);
+cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int64_t count, int most, int out_f32, const DeviceInfo& info, cudaStream_t s);
 // each in a file of its own
 #define Q4NX_ATTN(SEE)                                                                                                      \
   extern template cudaError_t launch_attention_rows<SEE>(int, bool, const AttnArgsOf<SEE>&, int, const DeviceInfo&, cudaStream_t); \
-  extern template cudaError_t launch_attention_block<SEE>(int, const AttnArgsOf<SEE>&, int64_t, int, const DeviceInfo&, cudaStream_t);
+  extern template cudaError_t launch_attention_block<SEE>(int, const AttnArgsOf<SEE>&, int64_t, int, int, const DeviceInfo&, cudaStream_t);
 Q4NX_ATTN(kCausal)
 Q4NX_ATTN(kAll)
 Q4NX_ATTN(kOwn)

@@ -44,7 +44,7 @@
 // columns, S in two buffers of 64 and O in 256, all 512, and keys and values one buffer each in shared memory.
 // S of a step is formed while the softmax of the step before is under way.  Four warps decode keys and eight values (the
 // second tile's softmax warps among them), each kind by itself: one after the other by the same eight warps a step went through
-// keys, S, p v and values in series, 4.4 us instead of 2.9. 96 rows over 16001 positions, twice, 4 kv heads: 64 us
+// keys, S, p v and values in series, 4.4 us instead of 2.9. 96 rows over 16001 positions, twice, 4 kv heads, by 152 CTAs: 64 us
 // (few rows' kernel 97; keys and values by 6 and 8 warps 68, 7 and 7 71, 8 and 6 70, 3 and 8 slower, 4 and 10 the same).
 //
 // A CTA's steps (64 tokens) are a range of all units' steps; a unit cut between
@@ -1006,8 +1006,8 @@ cudaError_t launch_block_variant(const AttnArgsOf<SEE>& a, int grid, cudaStream_
 }  // namespace
 
 template <int SEE>
-cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int64_t count, int out_f32, const DeviceInfo& info, cudaStream_t s) {
-  const int grid = info.sms < kKvMaxCtas / 2 ? info.sms : kKvMaxCtas / 2;      // two parts each
+cudaError_t launch_attention_block(int D, const AttnArgsOf<SEE>& a, int64_t count, int most, int out_f32, const DeviceInfo& info, cudaStream_t s) {
+  const int grid = info.sms < most ? info.sms : most;      // two parts each
   // requests of up to one tile of rows on average
   const bool pair = SEE == kAll && a.kb.tokens * a.group <= kTile * count;
 #define Q4NX_BLOCK(DD)                                                                                                        \

@@ -3,6 +3,6 @@
 
 namespace q4nx {
 
-template cudaError_t launch_attention_block<kAll>(int, const AttnArgsOf<kAll>&, int64_t, int, const DeviceInfo&, cudaStream_t);
+template cudaError_t launch_attention_block<kAll>(int, const AttnArgsOf<kAll>&, int64_t, int, int, const DeviceInfo&, cudaStream_t);
 
 }  // namespace q4nx

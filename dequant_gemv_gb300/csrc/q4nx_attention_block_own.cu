@@ -3,6 +3,6 @@
 
 namespace q4nx {
 
-template cudaError_t launch_attention_block<kOwn>(int, const AttnArgsOf<kOwn>&, int64_t, int, const DeviceInfo&, cudaStream_t);
+template cudaError_t launch_attention_block<kOwn>(int, const AttnArgsOf<kOwn>&, int64_t, int, int, const DeviceInfo&, cudaStream_t);
 
 }  // namespace q4nx
