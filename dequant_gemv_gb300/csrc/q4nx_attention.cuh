@@ -167,30 +167,75 @@ __device__ __forceinline__ int requests_of(const A& a) {
     if (a.first != nullptr) return a.groups;
   return a.kb.batch;
 }
+// The group that request b belongs to, or -1: the one that holds it and begins behind the ends of all groups
+// before it, so that no two groups have a request in common.  ordered: the bounds never fall.
+__device__ __forceinline__ int group_of(const int32_t* first, int groups, int b, bool ordered) {
+  int lo = 0;
+  if (ordered) {
+    int hi = groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    return first[lo] <= b && b < first[lo + 1] ? lo : -1;
+  }
+  int top = first[0];
+  for (; lo < groups; ++lo) {
+    top = max(top, first[lo]);
+    if (first[lo] == top && top <= b && b < first[lo + 1]) return lo;
+  }
+  return -1;
+}
+// What group g shares, with the tokens of all of its requests as those of one request; refused
+// where its requests do not lie in the batch, or do not begin behind the groups before it.
+__device__ __forceinline__ KvRequest shared_by(const KvBatch& kb, int page_blocks, const int32_t* first, const int32_t* shared, int g, bool ordered) {
+  const int f0 = first[g], f1 = first[g + 1];
+  if (f0 < 0 || f1 < f0 || f1 > kb.batch) return KvRequest{0, 0, 0, false};
+  if (!ordered)
+    for (int k = 0; k < g; ++k)
+      if (first[k] > f0) return KvRequest{0, 0, 0, false};
+  return kv_checked(kb, page_blocks, kb.q_start[f0], kb.q_start[f1], shared[g]);
+}
+// Request b with what it shares (low); refused with its group where that is, since its rows need both
+// parts, and where a token of the call does not lie behind what it shares.
+__device__ __forceinline__ KvRequest own_request(const KvBatch& kb, int page_blocks, const int32_t* first, const int32_t* shared, int groups,
+                                                 int b, bool ordered) {
+  KvRequest r = kv_request(kb, page_blocks, b);
+  const int g = group_of(first, groups, b, ordered);
+  r.low = g >= 0 ? shared[g] : -1;
+  if (r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low) || (r.low > 0 && !shared_by(kb, page_blocks, first, shared, g, ordered).ok))
+    return KvRequest{0, 0, 0, false};
+  if (r.T == 0) r.low = 0;
+  return r;
+}
 template <class A>
-__device__ __forceinline__ KvRequest request_of(const A& a, int b) {
+__device__ __forceinline__ KvRequest request_of(const A& a, int b, bool ordered = true) {
+  if constexpr (A::kSee == kOwn) return own_request(a.kb, a.pool.page_blocks, a.first, a.shared, a.groups, b, ordered);
   if constexpr (A::kSee == kAll)
     if (a.first != nullptr) {
-      const int f0 = a.first[b], f1 = a.first[b + 1];
-      if (f0 < 0 || f1 < f0 || f1 > a.kb.batch) return KvRequest{0, 0, 0, false};
-      KvRequest r = kv_checked(a.kb, a.pool.page_blocks, a.kb.q_start[f0], a.kb.q_start[f1], a.shared[b]);
+      KvRequest r = shared_by(a.kb, a.pool.page_blocks, a.first, a.shared, b, ordered);
       if (r.L == 0) r.T = 0;       // nothing shared: the other pass has these rows to itself
       return r;
     }
-  KvRequest r = kv_request(a.kb, a.pool.page_blocks, b);
-  if constexpr (A::kSee == kOwn) {
-    int lo = 0, hi = a.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.first[mid] <= b) lo = mid;
-      else hi = mid;
+  return kv_request(a.kb, a.pool.page_blocks, b);
+}
+// Where the prefixes come second: whether the other pass left nothing of a row (its place among the outputs'
+// rows) because its request is refused; the row is not written then.  Both passes' refusals are in the error word by now.
+static __device__ __noinline__ bool no_own_part(const KvBatch kb, int page_blocks, const int32_t* first, const int32_t* shared, int groups,
+                                         int64_t token) {
+  for (int b = 0; b < kb.batch; ++b)
+    if (kb.q_start[b] <= token && token < kb.q_start[b + 1]) {
+      const KvRequest r = own_request(kb, page_blocks, first, shared, groups, b, false);
+      if (r.ok && r.low > 0) return false;
     }
-    r.low = a.shared[lo];
-    // every token of the call lies behind what its request shares
-    if (a.first[lo] > b || a.first[lo + 1] <= b || r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low)) r = KvRequest{0, 0, 0, false};
-    if (r.T == 0) r.low = 0;
-  }
-  return r;
+  return true;
+}
+template <class A>
+__device__ __forceinline__ bool row_refused(const A& a, bool split, uint32_t err, int64_t at) {
+  if constexpr (A::kSee == kAll)
+    if (split && a.pass == 2 && (err & kErrIndex) != 0) return no_own_part(a.kb, a.pool.page_blocks, a.first, a.shared, a.groups, quot(at, a.heads));
+  return false;
 }
 template <class A>
 __device__ __forceinline__ int table_row(const A& a, int b) {
@@ -249,7 +294,7 @@ __device__ __forceinline__ Unit find_unit(const A& a, const Plan& pl, int64_t x,
 }
 
 // First position of CTA c: where its share of the costs begins, moved to the
-// end of a unit that it falls into less than kCutSteps from.
+// end of a unit that it falls into less than cut_steps from.
 template <int SB, int RB, class A>
 __device__ int64_t bound(const A& a, const Plan& pl, int c) {
   if (c >= pl.ctas) return pl.prefix[pl.batch];
@@ -341,28 +386,35 @@ __device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* 
   if (tid == 0) prefix[0] = cost[0] = 0;
   // the requests' steps and costs, and their prefix sums
   const int B = requests_of(a);
-  int most = 0;
-  if constexpr (A::kSee == kOwn)
-    if (blockIdx.x == 0) {
-      // the groups take the requests in their order, all of them
-      bool bad = tid == 0 && (a.first[0] != 0 || a.first[a.groups] != a.kb.batch);
-      for (int g = tid; g < a.groups; g += blockDim.x) bad |= a.first[g] > a.first[g + 1];
-      if (bad) atomicOr(a.err, kErrIndex);
+  bool fell = false;                                            // the groups' bounds do, somewhere
+  if constexpr (A::kSee != kCausal)
+    for (int g = tid; g < a.groups; g += blockDim.x) fell |= a.first[g] > a.first[g + 1];
+  if constexpr (A::kSee == kOwn)                                // the groups take the requests in their order, all of them
+    if (blockIdx.x == 0 && (fell || (tid == 0 && (a.first[0] != 0 || a.first[a.groups] != a.kb.batch)))) atomicOr(a.err, kErrIndex);
+#pragma unroll 1
+  for (bool ordered = true;; ordered = false) {
+    int most = 0;
+    for (int b = tid; b < B; b += blockDim.x) {
+      const KvRequest rq = request_of(a, b, ordered);
+      if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
+      if constexpr (A::kSee == kOwn) lower[b] = static_cast<int>(rq.low);
+      const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(a, rq);
+      prefix[b + 1] = units * n;
+      cost[b + 1] = units * (n + kUnitCost);
+      if (units > 0) most = max(most, static_cast<int>(n < (1 << 30) ? n : 1 << 30));
     }
-  for (int b = tid; b < B; b += blockDim.x) {
-    const KvRequest rq = request_of(a, b);
-    if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
-    if constexpr (A::kSee == kOwn) lower[b] = static_cast<int>(rq.low);
-    const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(a, rq);
-    prefix[b + 1] = units * n;
-    cost[b + 1] = units * (n + kUnitCost);
-    if (units > 0) most = max(most, static_cast<int>(n < (1 << 30) ? n : 1 << 30));
+    if constexpr (RB < 128) {
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) longest[warp] = most;
+    }
+    if constexpr (A::kSee == kCausal) {
+      __syncthreads();
+      break;
+    } else {
+      // once more where the groups are out of order, with the search that does not rely on it
+      if (!__syncthreads_or(fell && ordered)) break;
+    }
   }
-  if constexpr (RB < 128) {
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) longest[warp] = most;
-  }
-  __syncthreads();
   if (warp < 2) {
     int64_t *sum = warp ? cost : prefix, run = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {

@@ -812,8 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
       if constexpr (SEE == kOwn) split = w.u.rq.low > 0;
       else if constexpr (SEE == kAll) split = a.pass != 0;
       if (whole) wait_first_pass(a);                                // parts need nothing of it, and further pieces may follow
+      bool store = have && whole;
+      if constexpr (SEE == kAll)
+        if (store && a.pass == 2) store = !row_refused(a, split, __ldcg(a.err), at);
       RowScale sc = {0.f, 0.f};
-      if (have && whole) sc = row_scale(a, split, at, ref, l, true);
+      if (store) sc = row_scale(a, split, at, ref, l, true);
+      __syncwarp();                                                 // what follows takes whole warps
       const float inv = sc.own;
       [[maybe_unused]] const float* before = nullptr;               // what the first pass left of the row
       if constexpr (SEE != kCausal) before = a.part_o + at * D;
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (odd >> h & 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0x7fc00000u;
-        if (SEE != kCausal && split && have && whole) {
+        if (SEE != kCausal && split && store) {
           if constexpr (SEE != kCausal) {
             float4 p[8];                                            // all of them before the first store: one round trip
 #pragma unroll
@@ -852,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
               else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 32 * h + 4 * k) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
             }
           }
-        } else if (have && whole) {
+        } else if (store) {
           if constexpr (sizeof(Out) == 4) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
@@ -867,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
                              pack_bf16x2(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
                              pack_bf16x2(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
           }
-        } else if (have) {
+        } else if (have && !whole) {
 #pragma unroll
           for (int k = 0; k < 32; k += 4)                             // [D / 4][row][4]: a warp's rows side by side
             *reinterpret_cast<uint4*>(part + ((8 * h + k / 4) * R + row) * 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
@@ -914,6 +918,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) attention_join_ke
   __shared__ int first[kKvMaxCtas / 2], found[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int units = 0;
+  const uint32_t err = SEE == kAll ? __ldcg(a.err) : 0u;
   {
     Joined u;
     u.parts = 0;
@@ -962,6 +967,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinPerSm) attention_join_ke
         }
     }
     const int64_t at = out_row(a, u.q0, u.h, u.row0 + r);
+    if (row_refused(a, u.split, err, at)) continue;
     const RowScale sc = row_scale(a, u.split, at, m, l, c4 == 0);
     const float inv = sc.own;
     if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -362,9 +362,11 @@ typedef struct q4nx_kv_groups {
  * table's row of the group's first request; the other requests' entries of pages that hold
  * nothing else are not read through.  A prefix may end inside a page: each request
  * then has that page for itself, and its copies of the prefix's positions are not looked at.
- * Every token of the call has to lie behind what its request shares (lens - T >= shared):
- * requests of which that is not true, like groups out of order or lengths beyond the
- * table, are skipped and reported as Q4NX_E_INDEX.  Which rounding applies (fp16 weights or
+ * Every token of the call has to lie behind what its request shares (lens - T >= shared).
+ * Requests of which that is not true, or whose numbers are out of range, are skipped and reported as
+ * Q4NX_E_INDEX, and so are all requests of a group whose bounds, tokens or shared length are
+ * out of range or that begins before the end of an earlier one.  Rows of skipped requests stay
+ * as they were, and the others' are what they are without them.  Which rounding applies (fp16 weights or
  * bf16 pairs, at 256 channels too) goes by the rows of a group for what it shares and by those of a request for its own.
  * scratch_dev: q4nx_kv_attention_shared_scratch(cache, tokens, heads) bytes, 16-byte
  * aligned, any content, free again after the call's work on the stream. */
