@@ -338,7 +338,7 @@ __device__ __forceinline__ RowScale row_scale(const A& a, bool split, int64_t at
   if constexpr (A::kSee != kCausal) {
     if (split && a.pass == 2) {
       const float2 p = __ldcg(a.part_ml + at);
-      const float top = fmaxf(m, p.x), f = ex2(m - top), g = ex2(p.x - top) * p.y, all = fmaf(f, l, g), inv = 1.f / all;
+      const float top = fmaxf(m, p.x), f = ex2(m - top), g = ex2(p.x - top) * p.y, all = fmaf(f, l, g), inv = all == 0.f ? 0.f : 1.f / all;
       if (head && a.lse != nullptr) a.lse[at] = log_total(top, all);
       return {f * inv, g * inv};
     }
