@@ -26,24 +26,53 @@ struct Epilogue {
   int act = kActNone;
 };
 
-// x / (1 + exp(-z)), right to a few units in the last place for every z: where exp(-z)
-// overflows the result is 0 (or the quotient's NaN for infinite x)
-__device__ __forceinline__ float times_sigmoid(float x, float z) { return __fdividef(x, 1.f + expf(-z)); }
+// x / (1 + exp(-z)), right to a few units in the last place down to z = -87, where the denominator is still
+// below 2^126 and its reciprocal normal.  Further on that ends, and then binary32, while the quotient
+// is a normal number down to -92: far_tail.
+constexpr float kFarTail = -87.f;
+__device__ __forceinline__ float times_sigmoid(float x, float z) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + expf(-z)));
+  return x * y;
+}
+// That, for z below kFarTail: x exp(z), the power taken by halves, which stay normal (IEEE arithmetic's NaN where both are infinite).
+__device__ __forceinline__ float far_tail(float x, float z) {
+  const float half = expf(0.5f * z);
+  return x * half * half;
+}
+// 2 u for tanh GELU: 0.5 x (1 + tanh u) = x / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
+__device__ __forceinline__ float gelu_tanh_z(float x) { return 1.5957691216057308f * fmaf(0.044715f * x * x, x, x); }
 
 template <int ACT>
 __device__ __forceinline__ float activated(float x) {
   if constexpr (ACT == kActRelu) return x < 0.f ? 0.f : x;                       // NaN stays NaN
   // erfc, not 1 + erf: that would leave nothing of the tail below -4
   if constexpr (ACT == kActGelu) return 0.5f * x * erfcf(-0.70710678118654752f * x);
-  // 0.5 x (1 + tanh u) = x / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
-  if constexpr (ACT == kActGeluTanh) return times_sigmoid(x, 1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
-  if constexpr (ACT == kActSilu) return times_sigmoid(x, x);
   return x;
 }
 
 // Four at a call: its code, the longest of them, is there once and warm from the second call on.
 static __device__ __noinline__ float4 gelu4(float4 x) {
   return make_float4(activated<kActGelu>(x.x), activated<kActGelu>(x.y), activated<kActGelu>(x.z), activated<kActGelu>(x.w));
+}
+
+// Both kinds of x / (1 + exp(-z)), T at a time.  The tail's test is one for all of them: a branch for each
+// kept them from running side by side (12288x4096, 64 tokens, SiLU and gate 17.4 us; this way 16.3, without the tail 16.1).
+template <int T, typename Z>
+__device__ __forceinline__ void times_sigmoid(float (&v)[T], Z z) {
+  float y[T], least = z(v[0]);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    least = fminf(least, z(v[t]));
+    y[t] = times_sigmoid(v[t], z(v[t]));
+  }
+  if (least < kFarTail) {
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      if (z(v[t]) < kFarTail) y[t] = far_tail(v[t], z(v[t]));
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) v[t] = y[t];
 }
 
 template <int T>
@@ -65,14 +94,8 @@ __device__ __forceinline__ void activate(int act, float (&v)[T]) {
         for (int t = 0; t < T; ++t) v[t] = activated<kActGelu>(v[t]);
       }
       break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int t = 0; t < T; ++t) v[t] = activated<kActGeluTanh>(v[t]);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int t = 0; t < T; ++t) v[t] = activated<kActSilu>(v[t]);
-      break;
+    case kActGeluTanh: times_sigmoid(v, [](float x) { return gelu_tanh_z(x); }); break;
+    case kActSilu: times_sigmoid(v, [](float x) { return x; }); break;
     default: break;
   }
 }
