@@ -168,10 +168,11 @@ __device__ __forceinline__ int requests_of(const A& a) {
   return a.kb.batch;
 }
 // The group that request b belongs to, or -1: the one that holds it and begins behind the ends of all groups
-// before it, so that no two groups have a request in common.  ordered: the bounds never fall.
-__device__ __forceinline__ int group_of(const int32_t* first, int groups, int b, bool ordered) {
+// before it, so that no two groups have a request in common.  sound: the groups have been found in
+// order and none refused (make_plan), so that the bounds never fall.
+__device__ __forceinline__ int group_of(const int32_t* first, int groups, int b, bool sound) {
   int lo = 0;
-  if (ordered) {
+  if (sound) {
     int hi = groups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -189,10 +190,10 @@ __device__ __forceinline__ int group_of(const int32_t* first, int groups, int b,
 }
 // What group g shares, with the tokens of all of its requests as those of one request; refused
 // where its requests do not lie in the batch, or do not begin behind the groups before it.
-__device__ __forceinline__ KvRequest shared_by(const KvBatch& kb, int page_blocks, const int32_t* first, const int32_t* shared, int g, bool ordered) {
+__device__ __forceinline__ KvRequest shared_by(const KvBatch& kb, int page_blocks, const int32_t* first, const int32_t* shared, int g, bool sound) {
   const int f0 = first[g], f1 = first[g + 1];
   if (f0 < 0 || f1 < f0 || f1 > kb.batch) return KvRequest{0, 0, 0, false};
-  if (!ordered)
+  if (!sound)
     for (int k = 0; k < g; ++k)
       if (first[k] > f0) return KvRequest{0, 0, 0, false};
   return kv_checked(kb, page_blocks, kb.q_start[f0], kb.q_start[f1], shared[g]);
@@ -200,21 +201,21 @@ __device__ __forceinline__ KvRequest shared_by(const KvBatch& kb, int page_block
 // Request b with what it shares (low); refused with its group where that is, since its rows need both
 // parts, and where a token of the call does not lie behind what it shares.
 __device__ __forceinline__ KvRequest own_request(const KvBatch& kb, int page_blocks, const int32_t* first, const int32_t* shared, int groups,
-                                                 int b, bool ordered) {
+                                                 int b, bool sound) {
   KvRequest r = kv_request(kb, page_blocks, b);
-  const int g = group_of(first, groups, b, ordered);
+  const int g = group_of(first, groups, b, sound);
   r.low = g >= 0 ? shared[g] : -1;
-  if (r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low) || (r.low > 0 && !shared_by(kb, page_blocks, first, shared, g, ordered).ok))
+  if (r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low) || (!sound && r.low > 0 && !shared_by(kb, page_blocks, first, shared, g, false).ok))
     return KvRequest{0, 0, 0, false};
   if (r.T == 0) r.low = 0;
   return r;
 }
 template <class A>
-__device__ __forceinline__ KvRequest request_of(const A& a, int b, bool ordered = true) {
-  if constexpr (A::kSee == kOwn) return own_request(a.kb, a.pool.page_blocks, a.first, a.shared, a.groups, b, ordered);
+__device__ __forceinline__ KvRequest request_of(const A& a, int b, bool sound = true) {
+  if constexpr (A::kSee == kOwn) return own_request(a.kb, a.pool.page_blocks, a.first, a.shared, a.groups, b, sound);
   if constexpr (A::kSee == kAll)
     if (a.first != nullptr) {
-      KvRequest r = shared_by(a.kb, a.pool.page_blocks, a.first, a.shared, b, ordered);
+      KvRequest r = shared_by(a.kb, a.pool.page_blocks, a.first, a.shared, b, sound);
       if (r.L == 0) r.T = 0;       // nothing shared: the other pass has these rows to itself
       return r;
     }
@@ -386,16 +387,10 @@ __device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* 
   if (tid == 0) prefix[0] = cost[0] = 0;
   // the requests' steps and costs, and their prefix sums
   const int B = requests_of(a);
-  bool fell = false;                                            // the groups' bounds do, somewhere
-  if constexpr (A::kSee != kCausal)
-    for (int g = tid; g < a.groups; g += blockDim.x) fell |= a.first[g] > a.first[g + 1];
-  if constexpr (A::kSee == kOwn)                                // the groups take the requests in their order, all of them
-    if (blockIdx.x == 0 && (fell || (tid == 0 && (a.first[0] != 0 || a.first[a.groups] != a.kb.batch)))) atomicOr(a.err, kErrIndex);
-#pragma unroll 1
-  for (bool ordered = true;; ordered = false) {
+  auto look = [&](bool sound) {
     int most = 0;
     for (int b = tid; b < B; b += blockDim.x) {
-      const KvRequest rq = request_of(a, b, ordered);
+      const KvRequest rq = request_of(a, b, sound);
       if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
       if constexpr (A::kSee == kOwn) lower[b] = static_cast<int>(rq.low);
       const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(a, rq);
@@ -407,12 +402,25 @@ __device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* 
       most = __reduce_max_sync(0xffffffffu, most);
       if (lane == 0) longest[warp] = most;
     }
-    if constexpr (A::kSee == kCausal) {
+  };
+  if constexpr (A::kSee == kCausal) {
+    look(true);
+    __syncthreads();
+  } else {
+    // The groups, by the last threads, beside the requests' look-ups, which trust them and are made again where one
+    // is out of order or refused (looked up behind one another they took 0.4 us).
+    bool odd = false;
+    for (int g = blockDim.x - 1 - tid; g < a.groups; g += blockDim.x) {
+      odd |= a.first[g] > a.first[g + 1];
+      if constexpr (A::kSee == kOwn) odd |= !shared_by(a.kb, a.pool.page_blocks, a.first, a.shared, g, true).ok;
+    }
+    look(true);
+    if constexpr (A::kSee == kOwn) {                            // the groups take the requests in their order, all of them
+      if (blockIdx.x == 0 && (odd || (tid == 0 && (a.first[0] != 0 || a.first[a.groups] != a.kb.batch)))) atomicOr(a.err, kErrIndex);
+    }
+    if (__syncthreads_or(odd)) {
+      look(false);
       __syncthreads();
-      break;
-    } else {
-      // once more where the groups are out of order, with the search that does not rely on it
-      if (!__syncthreads_or(fell && ordered)) break;
     }
   }
   if (warp < 2) {
