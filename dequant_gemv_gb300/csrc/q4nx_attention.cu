@@ -15,10 +15,10 @@
 // joins them to its own when it writes a row.  It starts beside the first one and waits
 // for it only then, so that the second plan, look-ups and first copies cost no time of their own.
 //
-// Shared (against a floor by bytes): 48 requests behind 8191 positions, 32 query
-// heads, 8 kv heads of 128: 57 us (4.7); cold and alone the requests' own 60 to 600 tokens take 24 and the prefix on the
-// tensor cores 34; 16 requests behind 65537: 133 (14); 12 requests x 4 tokens, two groups behind 16001
-// positions, 4 kv heads of 256: 80 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
+// Shared (whole calls, against a floor by bytes): 48 requests behind 8191 positions, 32 query
+// heads, 8 kv heads of 128: 59 us (4.7); cold and alone the requests' own 60 to 600 tokens take 24 and the prefix on the
+// tensor cores 34; 16 requests behind 65537: 135 (14); 12 requests x 4 tokens, two groups behind 16001
+// positions, 4 kv heads of 256: 83 (5.9), by passes of 16 rows over the prefix 108; 4 requests behind 300: 18, two
 // plans, look-ups and joins.  Cross: 32 requests of 410 to 4097 positions: 37 us, 2.6 TB/s, as the kernel for few rows does.
 #include "q4nx_attention_rows.cuh"
 
@@ -139,7 +139,7 @@ cudaError_t launch_attention_shared(int D, const KvPool& pool, const KvBatch& kb
   a.part_ml = b.part_ml = reinterpret_cast<float2*>(a.part_o + kb.tokens * heads * D);
   // The tensor-core kernel has a second launch that joins its parts: it comes last, so
   // that nothing starts behind that launch.  Otherwise the prefixes, which are the larger part, come first
-  // (16 requests behind 65537 positions 127 us, own parts first 134).  Both at the same time on SMs divided by what
+  // (16 requests behind 65537 positions: own parts first took 5 % more).  Both at the same time on SMs divided by what
   // they cost gained 3 of 60 us for 48 requests behind 8191 positions and took a model of the costs: not kept.
   const bool prefix_last = many_rows<kAll>(D, kb.tokens * a.group, groups) && !many_rows<kOwn>(D, kb.tokens * a.group, kb.batch);
   a.pass = prefix_last ? 2 : 1;

@@ -303,7 +303,8 @@ __device__ int64_t bound(const A& a, const Plan& pl, int c) {
   const int64_t x = q * c + (c < rest ? c : rest);
   const Unit u = find_unit<SB, RB>(a, pl, x, true);
   const int64_t in = x - u.cost - kUnitCost;
-  // short units are not cut: a warp has three steps of them, joining the parts of CTAs takes longer
+  // short units are not cut (kWholeSteps: 768 positions, 384 at 256 channels, where a step is half as long): a warp has
+  // three steps of them, joining the parts of CTAs takes longer
   // (48 requests of 60 to 600 tokens of their own behind a prefix, 8 kv heads: 65 us in all, 60 uncut)
   if (A::kSee == kOwn && RB < 128 && u.rq.low > 0 && u.n <= kWholeSteps) return u.start + (2 * in < u.n ? 0 : u.n);
   return u.start + (in < cut_steps<RB> && in < u.n - cut_steps<RB> + 1 ? 0 : in > u.n - cut_steps<RB> ? u.n : in);

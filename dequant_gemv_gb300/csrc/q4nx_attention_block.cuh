@@ -31,7 +31,7 @@
 // 6000 positions, 32 heads: 253 us) the tensor pipe is busy 53% of the time
 // and 56% of the issue slots are: a step's products alone take 2570 cycles, with the other
 // roles' instructions between them 4000.  Where two tiles take one unit's tokens in turn (at most 128 rows) the
-// decoding of 128 tokens, 1.8 us a step, is the longest part.  The start takes 8.6 us: plan,
+// decoding of a step's 64 tokens, 1.8 us, is the longest part.  The start takes 8.6 us: plan,
 // the first blocks' arrival, cold code.
 // What else was tried: two issuing warps, one for each tile: they fall into step
 // and leave the tensor cores idle together, 58 us instead of 52; the keys' wait

@@ -4,10 +4,11 @@
 // each step in binary32.  An element's operands are read by the CTA that stores it,
 // before it does, so that mul or residual may be the output itself.
 //
-// What it costs (back to back): 1024x2048 q4_1, one token with a residual 4.8 -> 5.1 us; 12288x4096
-// q4_1, 64 tokens, SiLU and gate 14.1 -> 16.0, which moves 1.6 MB more and the activation's instructions at
+// What it costs (back to back in a graph): 1024x2048 q4_1, one token with a residual 4.6 -> 5.1 us; 12288x4096 q4_1, one
+// token, SiLU and gate 10.4 -> 11.0, 64 tokens 14.0 -> 16.4, which moves 1.6 MB more and the activation's instructions at
 // the launch's end, 12 warps of an SM on 128 rows x 64 tokens; Q8 4096x12288, 33 tokens, bias, GELU (tanh) and
-// residual 17.8 -> 22.3.  As operations of their own behind the product these read and write it again.
+// residual 17.6 -> 21.4 (whole calls 22.7).  The tensor-core kernel spills with an epilogue (216 bytes of stores, 496 of
+// loads at 128 registers, none without).  As operations of their own behind the product these read and write it again.
 #pragma once
 
 #include <cstdint>

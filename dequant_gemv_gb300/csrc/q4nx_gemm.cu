@@ -910,8 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if constexpr (EPI) {
           // With the dequant warps, which are done: one warp a scheduler waits for every result of its
-          // own (12288x4096, 64 tokens: gate with SiLU 17.6 us by four warps, 16.3 by twelve, GELU 20.7
-          // and 17.7; 14.1 without an epilogue; Q8 4096x12288 with bias, GELU and residual 22.3 and 20.6, 17.8)
+          // own (12288x4096, 64 tokens, in a graph: gate with SiLU 17.6 us by four warps, 16.4 by twelve, GELU by erfc 20.7
+          // and 17.6; 14.0 without an epilogue; Q8 4096x12288 with bias, GELU (tanh) and residual 21.4 by twelve, 17.6 without)
           if (finisher) {
             complete_sums(taddr, fx);
             tc_fence_before();

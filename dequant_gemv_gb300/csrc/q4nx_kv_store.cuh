@@ -20,7 +20,7 @@ __device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv
 }
 // Scale and middle of a group with smallest and largest value lo, hi; `bad`: one is no number.
 // The range is divided by 15; that of turned keys is multiplied by the 32-bit number nearest to 1/15, one
-// operation, which is one bf16 step from the quotient's in about one group of 16000.
+// operation, whose scale is a bf16 step from the quotient's in one group of 90000 (5 million of turned normal numbers).
 __device__ __forceinline__ void scale_of(float lo, float hi, bool bad, bool turned, uint32_t& s_bits, uint32_t& m_bits) {
   const float range = __fsub_rn(hi, lo);
   s_bits = f32_to_bf16_bits(turned ? __fmul_rn(range, 1.0f / 15.0f) : __fdiv_rn(range, 15.0f));

@@ -14,9 +14,9 @@
 // some of the heads, with the block's cosines and sines in shared memory for its keys, and in
 // a thread's registers, which turns the same channels of many heads, for its queries.
 //
-// Bound.  3 prompts of up to 1501 tokens, 32 query and 8 kv heads of 128 (2854 tokens): 19 us, 12 of them for keys
-// and values alone.  64 MB with the cosines: 3.4 TB/s, half of a copy's rate.  A key or value costs about 44
-// instructions of a lane (turn, extremes, code with its exact ties), the queries' 47 MB are the other 7 us: the two
+// Bound.  3 prompts of up to 1501 tokens, 32 query and 8 kv heads of 128 (2854 tokens): 19 to 20.5 us, keys
+// and values alone 12 to 19 from run to run.  64 MB with the cosines: 3.1 to 3.4 TB/s, half of a copy's rate.  A key or value costs about 44
+// instructions of a lane (turn, extremes, code with its exact ties), the queries' 47 MB come on top: the two
 // parts run beside one another only where one ends, and their CTAs alternating in the grid took 21.6 us
 // (query rows no longer in order), five CTAs an SM no less.  A CTA's 16 query heads: 18.9; 8: 19.5; 4: 22.2
 // (the look-up again for each).  Two numbers an instruction (packed binary32), ties by one test for both: 36, with the
@@ -317,10 +317,12 @@ template <int D>
 cudaError_t launch_turn(const TurnArgs& a, cudaStream_t s) {
   const int kv = a.pool.kv_heads;
   // By blocks from 8 tokens per request on average on, where there are enough of them.  32 query and 8 kv heads of
-  // 128, requests x tokens, by tokens and by blocks: 1 x 256 6.4 and 8.5 us, 1 x 512 9.5 and 8.8,
-  // 16 x 32 9.6 and 9.5, 1 x 1024 15.8 and 9.4, 1 x 4096 54 and 26; 48 x 5 6.4 and 9.7, 32 x 24 12.5 and
-  // 10.9, 64 x 16 16 and 12, 256 x 8 35 and 32; keys alone: 1 x 1024 7.8 and 8.6, 1 x 2048 12.3 and 9.9; 16
-  // and 4 of 256: 1 x 512 8.3 and 15, 1 x 1024 13.0 and 14.9, 1 x 2048 22 and 12; 32 and 8 of 64: 1 x 512 8.8 and 8.3.
+  // 128, requests x tokens, by tokens and by blocks: 1 x 256 6.5 and 8.7 us, 1 x 512 9.9 and 8.7 to 9.8,
+  // 16 x 32 9.7 and 9.5, 1 x 1024 16.0 and 9.5, 1 x 4096 55 and 26; 48 x 5 6.4 and 16, 32 x 24 12.6 and
+  // 10.8, 64 x 16 16 and 12, 256 x 8 35 and 31; keys alone: 1 x 1024 7.8 and 15, 1 x 2048 12.5 and 10 to 15; 16
+  // and 4 of 256: 1 x 512 8.4 and 15, 1 x 1024 13.1 and 10.5 to 15, 1 x 2048 22 and 12 to 16; 32 and 8 of 64: 1 x 512 8.8
+  // and 8.2.  (By blocks a call has two times, 5 us apart, of which a process shows one or the other.)  Rotations whose
+  // pairs by_groups does not find are by tokens at any size: 48 of 128 channels turned, 1 x 4096 55 us.
   if (by_groups(a.c.half, a.c.interleaved) && a.kb.tokens >= static_cast<int64_t>(8) * a.kb.batch && a.kb.tokens * (kv + a.c.heads) >= kFullItems) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(most_blocks(a.kb) + 1),       // and one that reports what is out of range

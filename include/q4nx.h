@@ -294,7 +294,8 @@ typedef struct q4nx_rotary {
 /* q4nx_kv_append with the call's keys, and its queries, turned by their positions on the way:
  *   a' = a cos - b sin,  b' = b cos + a sin,  each step one IEEE binary32 operation.
  * Keys are quantised from these binary32 numbers by the rule of q4nx_kv_append, but for
- * scale = bf16((hi - lo) * f) with f = 1/15 rounded to binary32; values as there.  q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token, or NULL
+ * scale = bf16((hi - lo) * f) with f = 1/15 rounded to binary32, turned or not; values as there.
+ * q_dev: bf16 [tokens][heads][head_dim], q_stride elements from token to token, or NULL
  * (keys alone; heads and the q_out arguments are not looked at).  q_out_dev: the turned queries, rounded
  * to bf16, q_out_stride elements from token to token; it may be q_dev itself with its stride,
  * other overlaps with the inputs are not allowed.  Strides are multiples of 8.  heads: 1..1024, any number.
@@ -362,6 +363,9 @@ typedef struct q4nx_kv_groups {
  * table's row of the group's first request; the other requests' entries of pages that hold
  * nothing else are not read through.  A prefix may end inside a page: each request
  * then has that page for itself, and its copies of the prefix's positions are not looked at.
+ * It pays for many requests behind a long prefix: with one token each and 32 query heads over 8
+ * kv heads of 128 from about 3000 shared positions for 48 requests, 4000 for 16, and not for 4;
+ * of 256 channels later.
  * Every token of the call has to lie behind what its request shares (lens - T >= shared).
  * Requests of which that is not true, or whose numbers are out of range, are skipped and reported as
  * Q4NX_E_INDEX, and so are all requests of a group whose bounds, tokens or shared length are
