@@ -804,6 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (w.r.hi - w.r.lo > (begun ? 1 : 0)) f1 = ex2(ref1 - top);      // else the other tile has no step in the piece
         l = fmaf(f0, l, f1 * l1), ref = top, odd |= c.half[mine].odd;
       }
+      // of some row of the warp: a load from TMEM takes whole warps, and a row's factor may be 0 beside others' that are not
+      const bool both_tiles = PAIR && __any_sync(0xffffffffu, f1 != 0.f);
       // O to the output, or as a part to the workspace
       const bool whole = x0 == w.u.start && w.end == w.u.start + w.u.n - c.begin, first = w.u.start >= c.begin;
       float* part = a.partial + static_cast<int64_t>(2 * blockIdx.x + (first ? 1 : 0)) * R * (D + 2);
@@ -817,12 +819,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
         if (store && a.pass == 2) store = !row_refused(a, split, __ldcg(a.err), at);
       RowScale sc = {0.f, 0.f};
       if (store) sc = row_scale(a, split, at, ref, l, true);
-      __syncwarp();                                                 // what follows takes whole warps
       const float inv = sc.own;
       [[maybe_unused]] const float* before = nullptr;               // what the first pass left of the row
       if constexpr (SEE != kCausal) before = a.part_o + at * D;
 #pragma unroll 1
       for (int h = 0; h < D / 32; ++h) {
+        __syncwarp();                                               // the loads take whole warps
         uint32_t o[32];
         if (begun) {
           tmem_load(lanes + Y::kO + 32 * h, o);
@@ -831,12 +833,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_block_kernel(const Attn
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           if (!begun || l == 0.f) o[k] = 0;
-        if (pair && f1 != 0.f) {
+        if (pair && both_tiles) {
           uint32_t other[32];
           tmem_load(lanes + Y::kCols + Y::kO + 32 * h, other);
           tmem_wait_load(other);
+          if (f1 != 0.f) {                                           // a row that has nothing of it takes none of its infinities
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(f0, __uint_as_float(o[k]), f1 * __uint_as_float(other[k])));
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(f0, __uint_as_float(o[k]), f1 * __uint_as_float(other[k])));
+          }
         }
         if (odd >> h & 1)
 #pragma unroll
