@@ -168,8 +168,8 @@ __device__ __forceinline__ int requests_of(const A& a) {
   return a.kb.batch;
 }
 // The group that request b belongs to, or -1: the one that holds it and begins behind the ends of all groups
-// before it, so that no two groups have a request in common.  sound: the groups have been found in
-// order and none refused (make_plan), so that the bounds never fall.
+// before it, so that no two groups have a request in common.  sound: no group and no request has been
+// found out of order or refused (make_plan), so that the bounds never fall.
 __device__ __forceinline__ int group_of(const int32_t* first, int groups, int b, bool sound) {
   int lo = 0;
   if (sound) {
@@ -198,15 +198,18 @@ __device__ __forceinline__ KvRequest shared_by(const KvBatch& kb, int page_block
       if (first[k] > f0) return KvRequest{0, 0, 0, false};
   return kv_checked(kb, page_blocks, kb.q_start[f0], kb.q_start[f1], shared[g]);
 }
-// Request b with what it shares (low); refused with its group where that is, since its rows need both
-// parts, and where a token of the call does not lie behind what it shares.
+// Request b with what it shares (low); refused where a token of the call does not lie behind what it
+// shares, and, since its rows need both parts, where its group is refused or has other tokens.
 __device__ __forceinline__ KvRequest own_request(const KvBatch& kb, int page_blocks, const int32_t* first, const int32_t* shared, int groups,
                                                  int b, bool sound) {
   KvRequest r = kv_request(kb, page_blocks, b);
   const int g = group_of(first, groups, b, sound);
   r.low = g >= 0 ? shared[g] : -1;
-  if (r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low) || (!sound && r.low > 0 && !shared_by(kb, page_blocks, first, shared, g, false).ok))
-    return KvRequest{0, 0, 0, false};
+  if (r.low < 0 || (r.T > 0 && r.low > 0 && r.L - r.T < r.low)) return KvRequest{0, 0, 0, false};
+  if (!sound) {
+    const KvRequest all = shared_by(kb, page_blocks, first, shared, g, false);
+    if (!all.ok || (r.T > 0 && (r.q0 < all.q0 || r.q0 + r.T > all.q0 + all.T))) return KvRequest{0, 0, 0, false};
+  }
   if (r.T == 0) r.low = 0;
   return r;
 }
@@ -388,10 +391,12 @@ __device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* 
   if (tid == 0) prefix[0] = cost[0] = 0;
   // the requests' steps and costs, and their prefix sums
   const int B = requests_of(a);
+  bool odd = false;                                             // something is out of order or refused
   auto look = [&](bool sound) {
     int most = 0;
     for (int b = tid; b < B; b += blockDim.x) {
       const KvRequest rq = request_of(a, b, sound);
+      odd |= !rq.ok;
       if (!rq.ok && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
       if constexpr (A::kSee == kOwn) lower[b] = static_cast<int>(rq.low);
       const int64_t units = rq.T > 0 ? quot(rq.T * a.group + RB - 1, RB) * a.pool.kv_heads : 0, n = unit_steps<SB>(a, rq);
@@ -409,8 +414,7 @@ __device__ __forceinline__ Plan make_plan(const A& a, int64_t* prefix, int64_t* 
     __syncthreads();
   } else {
     // The groups, by the last threads, beside the requests' look-ups, which trust them and are made again where one
-    // is out of order or refused (looked up behind one another they took 0.4 us).
-    bool odd = false;
+    // is out of order or refused, or a request is (looked up behind one another they took 0.4 us).
     for (int g = blockDim.x - 1 - tid; g < a.groups; g += blockDim.x) {
       odd |= a.first[g] > a.first[g + 1];
       if constexpr (A::kSee == kOwn) odd |= !shared_by(a.kb, a.pool.page_blocks, a.first, a.shared, g, true).ok;

@@ -32,9 +32,9 @@ def refused(first, shared, start, lens, tokens, cap):
         ok = 0 <= start[b] <= start[b + 1] <= tokens and 0 <= n <= cap
         at = [g for g in range(len(shared)) if first[g] <= b < first[g + 1] and first[g] >= max(first[:g], default=0)]
         ok = ok and len(at) > 0
-        if ok and shared[at[0]] != 0:
+        if ok:
             s, f0, f1 = shared[at[0]], first[at[0]], first[at[0] + 1]
-            ok = 0 <= s <= cap and f1 <= len(lens) and 0 <= start[f0] <= start[f1] <= tokens and (T == 0 or n - T >= s)
+            ok = 0 <= s <= cap and 0 <= f0 and f1 <= len(lens) and 0 <= start[f0] <= start[f1] <= tokens and (T == 0 or start[f0] <= start[b] and start[b + 1] <= start[f1]) and (T == 0 or s == 0 or n - T >= s)
         out.append(not ok)
     return out
 
@@ -114,11 +114,27 @@ def test_refused_rows_stay_as_they_were(q, form, dim, name, at, x):  # noqa: F81
         call.bad(f32, **call.changed(name, at, x))
 
 
+@pytest.mark.parametrize("name,at,x", [("first", 0, -1), ("first", 0, -2 ** 31), ("first", 2, 10 ** 6), ("first", -1, 10 ** 6), ("start", 3, -1), ("shared", 1, -1)])
+@pytest.mark.parametrize("many", [1, 16])
+def test_groups_that_share_nothing(q, many, name, at, x):  # noqa: F811
+    """Refused like the others where their bounds or tokens are out of range."""
+    call = Call(q, [(0, [(40, many)] * 3), (0, [(33, 1), (5, 5)]), (48, [(40, many)] * 3)], 128)
+    call.bad(True, **call.changed(name, at, x))
+
+
 @pytest.mark.parametrize("dim", [128, 256])
 def test_tokens_of_no_request_inside_a_group(q, dim):  # noqa: F811
     """Ranges of two requests out of order: their tokens belong to no request, those around them do."""
     call = Call(q, "crowd", dim)
     call.bad(True, **call.changed("start", 5, -1))
+
+
+@pytest.mark.parametrize("form,dim", [("few", 64), ("crowd", 128), ("prompts", 256)])
+def test_requests_outside_their_groups_tokens(q, form, dim):  # noqa: F811
+    """The last bound before some requests' tokens: the other pass has no part of them."""
+    forms = {"few": [(48, [(5, 1)] * 4)] * 2, "crowd": [(48, [(5, 1)] * 40)] * 2, "prompts": [(48, [(70, 66)] * 4)] * 2}
+    call = Call(q, forms[form], dim)
+    call.bad(True, **call.changed("start", -1, int(call.c.start[-1]) - (2 if form != "prompts" else 70)))
 
 
 @pytest.mark.parametrize("form", ["few", "crowd"])
