@@ -525,6 +525,7 @@ __device__ __forceinline__ bool finish_tile(Shared* sh, const ArgsEpilogue& a, c
 #pragma unroll 1
   for (int m0 = 8 * part; m0 < a.M; m0 += 8 * parts) {
     float v[8];
+    __syncwarp();                                    // the load takes whole warps: activations and stores may part them
     tmem_ld8(taddr + m0, v);
     if (e.bias != nullptr)
 #pragma unroll
