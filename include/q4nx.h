@@ -367,7 +367,8 @@ typedef struct q4nx_kv_groups {
  * kv heads of 128 from about 3000 shared positions for 48 requests, 4000 for 16, and not for 4;
  * of 256 channels later.
  * Every token of the call has to lie behind what its request shares (lens - T >= shared).
- * Requests of which that is not true, or whose numbers are out of range, are skipped and reported as
+ * Requests of which that is not true, or whose numbers are out of range (tokens outside their
+ * group's, where q_start is out of order, among them), are skipped and reported as
  * Q4NX_E_INDEX, and so are all requests of a group whose bounds, tokens or shared length are
  * out of range or that begins before the end of an earlier one.  Rows of skipped requests stay
  * as they were, and the others' are what they are without them.  Which rounding applies (fp16 weights or
